@@ -235,11 +235,13 @@ def source_hash():
     are reported only for the code they were taken on.  api.cu is left out:
     it holds the C entry points' argument checks and the host-only queries,
     and defines no kernel and no launch shape; so is rates.inc, the measured
-    table the host-only protocol selector reads."""
+    table the host-only protocol selector reads, and so are the block norms and
+    the microscaled 4-bit kernels, which no workload here launches."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "quantized_reduce_rmsnorm_gb300", "csrc")
     for f in sorted(os.listdir(d)):
-        if f in ("api.cu", "rates.inc"):
+        if f in ("api.cu", "rates.inc", "block.h", "block_norm.cu", "block_norm_grad.cu",
+                 "mx4.cu", "mx4.cuh", "mx4_matmul.cu"):
             continue
         h.update(f.encode())
         with open(os.path.join(d, f), encoding="utf-8") as fh:

@@ -316,6 +316,106 @@ fc_status fc_select_protocol(int64_t rows, int64_t hidden, int P, int min_bits,
 fc_status fc_protocol_estimate(int64_t rows, int64_t hidden, int P, fc_qspec spec,
                                const fc_link_model* link, double* est_us);
 
+/* ----------------------------------------------- around the boundary -- */
+
+/* Microscaled 4-bit floating point (MXFP4, OCP Microscaling Formats v1.0): one
+ * tensor of rows x hidden elements in blocks of 32 neighbouring elements of a
+ * row (hidden a multiple of 32).  codes: uint8[rows*hidden/2], e2m1, element
+ * 2i in the low nibble of byte i.  scales: fc_mx4_scales_bytes bytes of e8m0
+ * (2^(byte - 127); 255 is NaN) in tiles of 128 rows by 4 blocks: row r, block
+ * k at ((r/128)*ceil(hidden/128) + k/4)*512 + (r%32)*16 + (r/32%4)*4 + k%4
+ * (whole divisions).  In a row's last tile the bytes of blocks past the row's
+ * end are 0; those of rows past the last are neither written nor used.  Both
+ * pointers 16-byte aligned. */
+typedef struct {
+  void* codes;
+  void* scales;
+} fc_mx4;
+
+/* Bytes of the codes and of the scales; 0 for an invalid size. */
+size_t fc_mx4_codes_bytes(int64_t rows, int64_t hidden);
+size_t fc_mx4_scales_bytes(int64_t rows, int64_t hidden);
+
+/* Quantize [rows, hidden] of dtype FC_FMT_BF16 or FC_FMT_F32.  Per block of 32:
+ * e = max(floor(log2(max|x|)) - 2, -127), scale 2^e, codes x / 2^e rounded to
+ * the nearest e2m1 value (ties to even, at most 6 in magnitude); a block of
+ * zeros has e = -127; a block with an infinity or a NaN has the NaN scale, so
+ * all of it reads back as NaN. */
+fc_status fc_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, fc_mx4 out,
+                          fc_stream_t stream);
+
+/* Read back: out[rows, hidden] = code * scale, in out_dtype FC_FMT_BF16 or
+ * FC_FMT_F32 (both exact for every tensor that fc_mx4_quantize writes). */
+fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, int32_t out_dtype,
+                            fc_stream_t stream);
+
+/* Product of two MXFP4 tensors: out[t, n] = sum_k x[t, k] * w[n, k], x of rows x
+ * hidden (tokens), w of features x hidden (a projection's weight), out [rows,
+ * features] of out_dtype FC_FMT_BF16 or FC_FMT_F32: products exact, sums in
+ * binary32, one rounding.  features: a multiple of 16.  NaN scales make NaN of
+ * the rows (x) or columns (w) of out that they belong to.  For serving: the
+ * codes have no gradient.  d_status: optional, as for fc_group_quantize (a
+ * staging copy or a product that never completes within its bounded wait). */
+fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int64_t hidden, void* out,
+                        int32_t out_dtype, int32_t* d_status, fc_stream_t stream);
+
+/* The norms of a block, its gate and its residual scale.  All tensors are of
+ * one dtype T, FC_FMT_BF16 or FC_FMT_F32:
+ *   u = x, or x * inv(x, post_eps) * post_weight       (the norm after the block)
+ *   h = T(residual_scale * residual_in + block_scale * gate * u)   -> residual_out
+ *   y = T(h * inv(h, pre_eps) * pre_weight)            (the norm before the next)
+ *   inv(v, eps) = 1 / sqrt(mean(v^2) + eps), binary32
+ * x: [rows, hidden], the block's output.  residual_in: [rows, hidden], or NULL
+ * for none.  post_weight, pre_weight: [hidden]; NULL leaves the norm out (no y
+ * without pre_weight).  gate: [gate_rows, hidden], NULL (gate_rows 0) for none;
+ * gate_rows divides rows, and row t takes gate row t / (rows / gate_rows): 1
+ * for one gate, the number of sequences for one each, rows for one a token.
+ * hidden: a multiple of 16, at most 16384.  rows <= 2^31 - 1.  Every tensor is
+ * 32-byte aligned. */
+typedef struct {
+  const void* post_weight;
+  const void* gate;
+  const void* pre_weight;
+  int64_t gate_rows;
+  float residual_scale;
+  float block_scale;
+  float post_eps; /* in [0, 1], as pre_eps */
+  float pre_eps;
+} fc_block_norm_spec;
+
+/* y may be NULL, and y_mx4 (codes NULL: none) receives fc_mx4_quantize of y
+ * (hidden a multiple of 32); with pre_weight at least one of them is given,
+ * without it neither.  residual_out and y may be x or residual_in itself;
+ * outputs overlap nothing else. */
+fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, int64_t hidden,
+                        int32_t dtype, const fc_block_norm_spec* spec, void* residual_out, void* y,
+                        fc_mx4 y_mx4, fc_stream_t stream);
+
+/* Gradient of fc_block_norm.  x and h (= residual_out) are what the forward pass
+ * read and wrote; dy and dh are the gradients of y and of residual_out (dy with
+ * pre_weight and only then, and h with it; dh may be NULL with dy).  dx and
+ * dresidual (NULL: not wanted): [rows, hidden] of dtype.  The gradients of the
+ * weights, each NULL if not wanted: dpost_weight and dpre_weight fp32[hidden],
+ * dgate [gate_rows, hidden] of dtype, one rounding after a binary32 sum.  Sums
+ * over rows run in a fixed order: the same call gives the same bits.
+ * workspace: fc_block_norm_backward_workspace bytes, 32-byte aligned, this
+ * call's own until it has run.  rows == 0 sets the weights' gradients that are
+ * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual may be x, h, dy or dh itself;
+ * outputs overlap nothing else. */
+typedef struct {
+  void* dx;
+  void* dresidual;
+  float* dpost_weight;
+  void* dgate;
+  float* dpre_weight;
+} fc_block_norm_grads;
+
+size_t fc_block_norm_backward_workspace(int64_t rows, int64_t hidden, int64_t gate_rows);
+fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, const void* dh,
+                                 int64_t rows, int64_t hidden, int32_t dtype,
+                                 const fc_block_norm_spec* spec, const fc_block_norm_grads* grads,
+                                 void* workspace, fc_stream_t stream);
+
 /* --------------------------------------------------------------- misc --- */
 const char* fc_status_string(fc_status s);
 /* Message describing the calling thread's last non-OK status ("" if none). */

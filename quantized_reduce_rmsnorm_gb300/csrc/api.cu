@@ -9,6 +9,7 @@
 
 #include <algorithm>
 
+#include "block.h"
 #include "fcomm.h"
 #include "internal.h"
 
@@ -153,6 +154,84 @@ double estimate_us(int f, int64_t rows, int64_t hidden, int P, const fc_link_mod
     if (!kCands[f].tagged) t += 2.0 * link->barrier_us;
   }
   return t;
+}
+
+}  // namespace
+
+namespace {
+
+// Shape of the entry points below; step: what hidden is a multiple of.
+fc_status check_rows_hidden(int64_t rows, int64_t hidden, int step, int64_t most) {
+  if (rows < 0) return fail(FC_ERR_INVALID, "rows must be >= 0 (got %lld)", (long long)rows);
+  if (rows > INT32_MAX) return fail(FC_ERR_UNSUPPORTED, "rows > 2^31 - 1 is not supported");
+  if (hidden <= 0 || hidden % step != 0)
+    return fail(FC_ERR_INVALID, "hidden must be a positive multiple of %d (got %lld)", step,
+                (long long)hidden);
+  if (hidden > most) return fail(FC_ERR_UNSUPPORTED, "hidden > %lld is not supported", (long long)most);
+  return FC_OK;
+}
+
+fc_status check_dtype(int32_t dtype, const char* name) {
+  if (dtype != FC_FMT_BF16 && dtype != FC_FMT_F32)
+    return fail(FC_ERR_INVALID, "%s must be FC_FMT_BF16 or FC_FMT_F32 (got %d)", name, dtype);
+  return FC_OK;
+}
+
+fc_status check_mx4(const fc_mx4& t, const char* name) {
+  char buf[64];
+  snprintf(buf, sizeof buf, "%s.codes", name);
+  if (fc_status s = check_ptr(t.codes, 16, buf)) return s;
+  snprintf(buf, sizeof buf, "%s.scales", name);
+  return check_ptr(t.scales, 16, buf);
+}
+
+// One tensor of a call, for the check of overlaps.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+  bool in_place;  // an input that a row-wise output may be the same memory as
+};
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+// Outputs share no memory with one another, nor with inputs, except a
+// row-wise output (the first `rowwise` of them) that is a row-wise input itself.
+template <size_t NO, size_t NI>
+fc_status check_overlaps(const Span (&out)[NO], size_t rowwise, const Span (&in)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t k = i + 1; k < NO; ++k)
+      if (overlap(out[i], out[k]))
+        return fail(FC_ERR_INVALID, "%s overlaps %s", out[i].name, out[k].name);
+    for (const Span& s : in)
+      if (overlap(out[i], s) && !(i < rowwise && s.in_place && s.p == out[i].p))
+        return fail(FC_ERR_INVALID, "%s overlaps %s", out[i].name, s.name);
+  }
+  return FC_OK;
+}
+
+fc_status check_block_norm_spec(const fc_block_norm_spec* sp, int64_t rows) {
+  if (!sp) return fail(FC_ERR_INVALID, "spec must not be NULL");
+  if (sp->gate) {
+    if (sp->gate_rows < 1 || (rows > 0 && rows % sp->gate_rows != 0))
+      return fail(FC_ERR_INVALID, "gate_rows (%lld) must be positive and divide rows (%lld)",
+                  (long long)sp->gate_rows, (long long)rows);
+    if (rows > 0)
+      if (fc_status s = check_ptr(sp->gate, 32, "gate")) return s;
+  } else if (sp->gate_rows != 0) {
+    return fail(FC_ERR_INVALID, "gate_rows must be 0 without a gate (got %lld)", (long long)sp->gate_rows);
+  }
+  if (sp->post_weight && !aligned(sp->post_weight, 32))
+    return fail(FC_ERR_INVALID, "post_weight must be 32-byte aligned");
+  if (sp->pre_weight && !aligned(sp->pre_weight, 32))
+    return fail(FC_ERR_INVALID, "pre_weight must be 32-byte aligned");
+  if (!(sp->post_eps >= 0.0f) || sp->post_eps > 1.0f || !(sp->pre_eps >= 0.0f) || sp->pre_eps > 1.0f)
+    return fail(FC_ERR_INVALID, "post_eps and pre_eps must be in [0, 1]");
+  if (!std::isfinite(sp->residual_scale) || !std::isfinite(sp->block_scale))
+    return fail(FC_ERR_INVALID, "residual_scale and block_scale must be finite");
+  return FC_OK;
 }
 
 }  // namespace
@@ -473,6 +552,221 @@ fc_status fc_allreduce_residual_rmsnorm(const fc_qtensor* slabs, int P, int64_t 
   return fc_allreduce_residual_rmsnorm_ex(slabs, P, rows, hidden, spec, residual_in, residual_out,
                                           gamma, eps, requant_out, y, expected_epoch, d_status,
                                           nullptr, stream);
+}
+
+// -------------------------------------------------- around the boundary --
+size_t fc_mx4_codes_bytes(int64_t rows, int64_t hidden) {
+  if (rows < 0 || hidden <= 0 || hidden % 32 != 0) return 0;
+  return static_cast<size_t>(rows) * static_cast<size_t>(hidden) / 2;
+}
+
+size_t fc_mx4_scales_bytes(int64_t rows, int64_t hidden) {
+  if (rows < 0 || hidden <= 0 || hidden % 32 != 0) return 0;
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((hidden + 127) / 128) * 512u;
+}
+
+fc_status fc_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, fc_mx4 out,
+                          fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (fc_status s = check_mx4(out, "out")) return s;
+  const int64_t n = rows * hidden;
+  const Span o[] = {{out.codes, n / 2, "out.codes", false},
+                    {out.scales, (int64_t)fc_mx4_scales_bytes(rows, hidden), "out.scales", false}};
+  const Span i[] = {{x, n * (dtype == FC_FMT_F32 ? 4 : 2), "x", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  return cuda_status(fc::launch_mx4_quantize(dtype == FC_FMT_F32, x, rows, static_cast<int>(hidden), out.codes,
+                                             static_cast<uint8_t*>(out.scales), (cudaStream_t)stream),
+                     "fc_mx4_quantize launch");
+}
+
+fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, int32_t out_dtype,
+                            fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_mx4(in, "in")) return s;
+  if (fc_status s = check_ptr(out, 32, "out")) return s;
+  const int64_t n = rows * hidden;
+  const Span o[] = {{out, n * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false}};
+  const Span i[] = {{in.codes, n / 2, "in.codes", false},
+                    {in.scales, (int64_t)fc_mx4_scales_bytes(rows, hidden), "in.scales", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  return cuda_status(fc::launch_mx4_dequantize(out_dtype == FC_FMT_F32, in.codes,
+                                               static_cast<const uint8_t*>(in.scales), rows,
+                                               static_cast<int>(hidden), out, (cudaStream_t)stream),
+                     "fc_mx4_dequantize launch");
+}
+
+fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int64_t hidden, void* out,
+                        int32_t out_dtype, int32_t* d_status, fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (rows > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "rows > 2^22 is not supported");
+  if (features <= 0 || features % 16 != 0)
+    return fail(FC_ERR_INVALID, "features must be a positive multiple of 16 (got %lld)", (long long)features);
+  if (features > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "features > 2^22 is not supported");
+  if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_mx4(x, "x")) return s;
+  if (fc_status s = check_mx4(w, "w")) return s;
+  if (fc_status s = check_ptr(out, 32, "out")) return s;
+  if (d_status && !aligned(d_status, 4)) return fail(FC_ERR_INVALID, "d_status must be 4-byte aligned");
+  const Span o[] = {{out, rows * features * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false}};
+  const Span i[] = {{x.codes, rows * hidden / 2, "x.codes", false},
+                    {x.scales, (int64_t)fc_mx4_scales_bytes(rows, hidden), "x.scales", false},
+                    {w.codes, features * hidden / 2, "w.codes", false},
+                    {w.scales, (int64_t)fc_mx4_scales_bytes(features, hidden), "w.scales", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  fc::Mx4MatmulArgs a{};
+  a.x_codes = x.codes;
+  a.x_scales = static_cast<const uint8_t*>(x.scales);
+  a.w_codes = w.codes;
+  a.w_scales = static_cast<const uint8_t*>(w.scales);
+  a.out = out;
+  a.status = d_status;
+  a.rows = rows;
+  a.features = features;
+  a.H = static_cast<int>(hidden);
+  a.out_f32 = out_dtype == FC_FMT_F32;
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+  return cuda_status(fc::launch_mx4_matmul(a, (cudaStream_t)stream), "fc_mx4_matmul launch");
+}
+
+fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, int64_t hidden,
+                        int32_t dtype, const fc_block_norm_spec* spec, void* residual_out, void* y,
+                        fc_mx4 y_mx4, fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, y_mx4.codes ? 32 : 16, fc::kBlockNormMaxHidden)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (fc_status s = check_block_norm_spec(spec, rows)) return s;
+  if (spec->pre_weight && !y && !y_mx4.codes)
+    return fail(FC_ERR_INVALID, "pre_weight needs y or y_mx4");
+  if (!spec->pre_weight && (y || y_mx4.codes))
+    return fail(FC_ERR_INVALID, "y and y_mx4 need pre_weight");
+  if (rows == 0) return ok();
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (residual_in && !aligned(residual_in, 32))
+    return fail(FC_ERR_INVALID, "residual_in must be 32-byte aligned");
+  if (fc_status s = check_ptr(residual_out, 32, "residual_out")) return s;
+  if (y && !aligned(y, 32)) return fail(FC_ERR_INVALID, "y must be 32-byte aligned");
+  if (y_mx4.codes)
+    if (fc_status s = check_mx4(y_mx4, "y_mx4")) return s;
+  const int64_t es = dtype == FC_FMT_F32 ? 4 : 2, n = rows * hidden;
+  const Span o[] = {
+      {residual_out, n * es, "residual_out", false},
+      {y, n * es, "y", false},
+      {y_mx4.codes, n / 2, "y_mx4.codes", false},
+      {y_mx4.codes ? y_mx4.scales : nullptr, (int64_t)fc_mx4_scales_bytes(rows, hidden), "y_mx4.scales", false}};
+  const Span i[] = {{x, n * es, "x", true},
+                    {residual_in, n * es, "residual_in", true},
+                    {spec->gate, spec->gate_rows * hidden * es, "gate", false},
+                    {spec->post_weight, hidden * es, "post_weight", false},
+                    {spec->pre_weight, hidden * es, "pre_weight", false}};
+  if (fc_status s = check_overlaps(o, 2, i)) return s;
+  fc::BlockNormArgs a{};
+  a.x = x;
+  a.res_in = residual_in;
+  a.res_out = residual_out;
+  a.y = y;
+  a.y_codes = y_mx4.codes;
+  a.y_scales = static_cast<uint8_t*>(y_mx4.scales);
+  a.post_w = spec->post_weight;
+  a.gate = spec->gate;
+  a.pre_w = spec->pre_weight;
+  a.rows = rows;
+  a.gate_seg = spec->gate ? rows / spec->gate_rows : rows;
+  a.H = static_cast<int>(hidden);
+  a.alpha = spec->residual_scale;
+  a.beta = spec->block_scale;
+  a.eps_post = spec->post_eps;
+  a.eps_pre = spec->pre_eps;
+  return cuda_status(fc::launch_block_norm(dtype == FC_FMT_F32, a, (cudaStream_t)stream), "fc_block_norm launch");
+}
+
+size_t fc_block_norm_backward_workspace(int64_t rows, int64_t hidden, int64_t gate_rows) {
+  if (rows <= 0 || hidden <= 0 || gate_rows < 0) return 0;
+  // the CTAs' sums for the two weights and, where a gate row's rows may be cut
+  // into pieces (gate_rows below the CTAs), those of the pieces
+  const size_t ctas = static_cast<size_t>(std::min<int64_t>(rows, fc::kNormGradMaxCtas));
+  const bool cut = gate_rows > 0 && gate_rows < rows && gate_rows < fc::kNormGradMaxCtas;
+  return ctas * static_cast<size_t>(hidden) * sizeof(float) * (cut ? 3u : 2u);
+}
+
+fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, const void* dh,
+                                 int64_t rows, int64_t hidden, int32_t dtype,
+                                 const fc_block_norm_spec* spec, const fc_block_norm_grads* grads,
+                                 void* workspace, fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 16, fc::kBlockNormMaxHidden)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (fc_status s = check_block_norm_spec(spec, rows)) return s;
+  if (!grads) return fail(FC_ERR_INVALID, "grads must not be NULL");
+  const fc_block_norm_grads& g = *grads;
+  if ((g.dpost_weight && !spec->post_weight) || (g.dgate && !spec->gate) || (g.dpre_weight && !spec->pre_weight))
+    return fail(FC_ERR_INVALID, "a gradient is asked for that the spec has no weight or gate for");
+  const int64_t es = dtype == FC_FMT_F32 ? 4 : 2, n = rows * hidden;
+  if (!aligned(g.dpost_weight, 4) || !aligned(g.dpre_weight, 4))
+    return fail(FC_ERR_INVALID, "dpost_weight and dpre_weight must be 4-byte aligned");
+  if (g.dgate && !aligned(g.dgate, 32)) return fail(FC_ERR_INVALID, "dgate must be 32-byte aligned");
+  if (rows == 0) {  // sums of nothing
+    void* const p[3] = {g.dpost_weight, g.dpre_weight, g.dgate};
+    const int64_t bytes[3] = {hidden * 4, hidden * 4, spec->gate_rows * hidden * es};
+    for (int k = 0; k < 3; ++k)
+      if (p[k])
+        if (fc_status s = cuda_status(cudaMemsetAsync(p[k], 0, bytes[k], (cudaStream_t)stream), "gradient of no rows"))
+          return s;
+    return ok();
+  }
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (spec->pre_weight) {
+    if (fc_status s = check_ptr(dy, 32, "dy")) return s;
+    if (fc_status s = check_ptr(h, 32, "h")) return s;
+    if (dh && !aligned(dh, 32)) return fail(FC_ERR_INVALID, "dh must be 32-byte aligned");
+  } else {
+    if (dy) return fail(FC_ERR_INVALID, "dy needs pre_weight");
+    if (fc_status s = check_ptr(dh, 32, "dh")) return s;
+  }
+  if (fc_status s = check_ptr(g.dx, 32, "dx")) return s;
+  if (g.dresidual && !aligned(g.dresidual, 32)) return fail(FC_ERR_INVALID, "dresidual must be 32-byte aligned");
+  if (fc_status s = check_ptr(workspace, 32, "workspace")) return s;
+  const Span o[] = {
+      {g.dx, n * es, "dx", false},
+      {g.dresidual, n * es, "dresidual", false},
+      {g.dpost_weight, hidden * 4, "dpost_weight", false},
+      {g.dgate, spec->gate_rows * hidden * es, "dgate", false},
+      {g.dpre_weight, hidden * 4, "dpre_weight", false},
+      {workspace, (int64_t)fc_block_norm_backward_workspace(rows, hidden, spec->gate_rows), "workspace", false}};
+  const Span i[] = {{x, n * es, "x", true},
+                    {h, n * es, "h", true},
+                    {dy, n * es, "dy", true},
+                    {dh, n * es, "dh", true},
+                    {spec->gate, spec->gate_rows * hidden * es, "gate", false},
+                    {spec->post_weight, hidden * es, "post_weight", false},
+                    {spec->pre_weight, hidden * es, "pre_weight", false}};
+  if (fc_status s = check_overlaps(o, 2, i)) return s;
+  fc::BlockNormGradArgs a{};
+  a.x = x;
+  a.h = h;
+  a.dy = dy;
+  a.dh = dh;
+  a.post_w = spec->post_weight;
+  a.gate = spec->gate;
+  a.pre_w = spec->pre_weight;
+  a.dx = g.dx;
+  a.dres = g.dresidual;
+  a.dgate = g.dgate;
+  a.dpost_w = g.dpost_weight;
+  a.dpre_w = g.dpre_weight;
+  a.ws = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.gate_rows = spec->gate_rows;
+  a.H = static_cast<int>(hidden);
+  a.alpha = spec->residual_scale;
+  a.beta = spec->block_scale;
+  a.eps_post = spec->post_eps;
+  a.eps_pre = spec->pre_eps;
+  return cuda_status(fc::launch_block_norm_grad(dtype == FC_FMT_F32, a, (cudaStream_t)stream),
+                     "fc_block_norm_backward launch");
 }
 
 fc_status fc_token_split(int P, int64_t rows, int64_t hidden, fc_qspec spec, int64_t* split,

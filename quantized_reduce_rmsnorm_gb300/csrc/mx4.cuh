@@ -1,0 +1,179 @@
+// mx4.cuh -- microscaled 4-bit floating point (MXFP4) device helpers.
+//
+// A block is 32 neighbouring elements of a row.  With m the largest |x| of
+// the block and e = floor(log2 m) - 2 (the exponent of the largest e2m1
+// value, 6 = 1.5 * 2^2, is 2), the block's scale is 2^e, stored as the byte
+// e + 127 (e8m0), and each element's code is x / 2^e rounded to the nearest
+// e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), ties to the even code,
+// saturating at 6.  Scaling by a power of two is exact in binary32 (values
+// that it makes subnormal are far below 0.25 and round to 0 either way), so a
+// code is one rounding of its element.  e is held at -127 or above: a block
+// of zeros, and one whose m is below 2^-125, has the byte 0.  A block with an
+// infinity or a NaN gets the byte 0xFF, which stands for NaN.
+//
+// Scales lie in tiles of 128 rows by 4 blocks (512 bytes), tile (r / 128,
+// k / 4) at ((r / 128) * ceil(hidden / 128) + k / 4) * 512, and in it row r,
+// block k at (r % 32) * 16 + (r / 32 % 4) * 4 + k % 4: the order in which the
+// tensor core wants 128 rows' scales in its memory (32 lanes of 16 bytes), so
+// a tile goes there with one copy of 512 neighbouring bytes.
+#pragma once
+
+#include "device.cuh"
+
+namespace fc {
+
+__host__ __device__ __forceinline__ int64_t mx4_tiles_k(int H) { return (H + 127) / 128; }
+// Byte offset of the four scales of row r, blocks 4 * kt .. 4 * kt + 3.
+__device__ __forceinline__ int64_t mx4_scale_word(int64_t r, int64_t kt, int64_t KT) {
+  return ((r >> 7) * KT + kt) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// Largest |v| of 16 floats as bits: as unsigned numbers the bit patterns of
+// non-negative floats order as the floats do, infinity and NaN above all.
+__device__ __forceinline__ uint32_t absmax_bits16(const float v[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+// The same of 16 packed bf16, without unpacking them.
+__device__ __forceinline__ uint32_t absmax_bits16(const V8& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v.w[i] & 0x7FFF7FFFu);
+  return max(m << 16, m & 0xFFFF0000u);
+}
+
+// e8m0 byte of a block whose largest |v| has these bits.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax_bits) {
+  const int E = static_cast<int>(amax_bits >> 23);
+  return E == 255 ? 255u : static_cast<uint32_t>(max(E - 2, 0));
+}
+// 2^-e of that byte (for the NaN byte any factor serves: the scale decides).
+__device__ __forceinline__ float mx4_inv_scale(uint32_t byte) {
+  return __uint_as_float((254u - min(byte, 252u)) << 23);
+}
+// 2^e; the byte 0 is 2^-127, a subnormal.
+__device__ __forceinline__ float mx4_scale(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FC00000u)
+                      : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+// Eight floats -> eight e2m1 codes, element 2i in the low nibble of byte i.
+__device__ __forceinline__ uint32_t mx4_encode8(const float* v, float inv) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(v[i], inv);
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(r)
+      : "f"(s[0]), "f"(s[1]), "f"(s[2]), "f"(s[3]), "f"(s[4]), "f"(s[5]), "f"(s[6]), "f"(s[7]));
+  return r;
+}
+// Eight codes -> eight floats, times the block's scale.
+__device__ __forceinline__ void mx4_decode8(uint32_t w, float scale, float* v) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h[i]));
+    v[2 * i] = __fmul_rn(lo, scale);
+    v[2 * i + 1] = __fmul_rn(hi, scale);
+  }
+}
+
+// One warp's share of a quantisation: every lane holds 16 elements, eight
+// neighbouring lanes one scale word's 128 (`live`: the lane's elements are
+// inside the row).  Writes the lane's 8 bytes of codes and, by the first of
+// the eight, the word of four scale bytes (0 past the row's end).  amax_bits
+// is that of the lane's 16 elements, 0 for a lane that is not live.
+__device__ __forceinline__ void mx4_store16(const float v[16], uint32_t amax_bits, bool live,
+                                            bool word, uint8_t* codes, uint8_t* scales) {
+  const uint32_t m = max(amax_bits, __shfl_xor_sync(kFull, amax_bits, 1));
+  const uint32_t byte = live ? mx4_scale_byte(m) : 0u;
+  if (live) {
+    const float inv = mx4_inv_scale(byte);
+    uint2 c;
+    c.x = mx4_encode8(v, inv);
+    c.y = mx4_encode8(v + 8, inv);
+    *reinterpret_cast<uint2*>(codes) = c;
+  }
+  uint32_t w = byte | (__shfl_down_sync(kFull, byte, 2) << 8);
+  w |= __shfl_down_sync(kFull, w, 4) << 16;
+  if (word) *reinterpret_cast<uint32_t*>(scales) = w;
+}
+
+// ------------------------------------------------ rows of bf16 or fp32 --
+// 16 neighbouring elements of a row tensor (coherent loads: an output may be
+// the input's own memory).
+template <bool F32>
+struct Raw16 {
+  V8 v[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw16<F32> load_raw16(const void* base, int64_t elem) {
+  Raw16<F32> r;
+  const char* p = static_cast<const char*>(base) + elem * (F32 ? 4 : 2);
+  r.v[0] = ld256_coherent(p);
+  if constexpr (F32) r.v[1] = ld256_coherent(p + 32);
+  return r;
+}
+// Weights and gates, which every row re-reads.
+template <bool F32>
+__device__ __forceinline__ Raw16<F32> load_weight16(const void* base, int64_t elem) {
+  Raw16<F32> r;
+  const char* p = static_cast<const char*>(base) + elem * (F32 ? 4 : 2);
+  r.v[0] = ld256_keep(p);
+  if constexpr (F32) r.v[1] = ld256_keep(p + 32);
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack_raw(const Raw16<F32>& r, float f[16]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r.v[i / 8].w[i % 8]);
+  } else {
+    unpack16(r.v[0], f);
+  }
+}
+// Rounds 16 floats to the row type (bf16: to nearest even; fp32: as they are).
+template <bool F32>
+__device__ __forceinline__ Raw16<F32> pack_raw(const float f[16]) {
+  Raw16<F32> r;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r.v[i / 8].w[i % 8] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[0].w[i] = pack_bf2(f[2 * i], f[2 * i + 1]);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void store_raw16(void* base, int64_t elem, const Raw16<F32>& r) {
+  char* p = static_cast<char*>(base) + elem * (F32 ? 4 : 2);
+  st256(p, r.v[0]);
+  if constexpr (F32) st256(p + 32, r.v[1]);
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t absmax_raw(const Raw16<F32>& r) {
+  if constexpr (F32) {
+    float f[16];
+    unpack_raw<true>(r, f);
+    return absmax_bits16(f);
+  } else {
+    return absmax_bits16(r.v[0]);
+  }
+}
+
+}  // namespace fc

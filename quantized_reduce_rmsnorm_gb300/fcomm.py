@@ -28,7 +28,9 @@ EXPORTS = (
     "fc_pack_tagged_multi", "fc_group_quantize_tagged",
     "fc_allreduce_residual_rmsnorm", "fc_allreduce_residual_rmsnorm_ex", "fc_status_string",
     "fc_last_error", "fc_version", "fc_token_split", "fc_select_protocol", "fc_allgather_dequant",
-    "fc_protocol_estimate",
+    "fc_protocol_estimate", "fc_mx4_codes_bytes", "fc_mx4_scales_bytes", "fc_mx4_quantize",
+    "fc_mx4_dequantize", "fc_mx4_matmul", "fc_block_norm", "fc_block_norm_backward_workspace",
+    "fc_block_norm_backward",
 )
 
 
@@ -60,6 +62,23 @@ class LinkModel(ctypes.Structure):
 
 class LaunchOpts(ctypes.Structure):
     _fields_ = [("max_ctas", ctypes.c_int32), ("kernel", ctypes.c_int32)]
+
+
+class Mx4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class BlockNormSpec(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float)]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dresidual", ctypes.c_void_p),
+                ("dpost_weight", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dpre_weight", ctypes.c_void_p)]
 
 
 KERNEL_AUTO, KERNEL_STREAM, KERNEL_TMA = 0, 1, 2
@@ -114,6 +133,14 @@ def load(path: Optional[str] = None):
         "fc_select_protocol": (i32, [i64, i64, i32, i32, P, ctypes.POINTER(QSpec),
                                      ctypes.POINTER(ctypes.c_double)]),
         "fc_protocol_estimate": (i32, [i64, i64, i32, QS, P, ctypes.POINTER(ctypes.c_double)]),
+        "fc_mx4_codes_bytes": (ctypes.c_size_t, [i64, i64]),
+        "fc_mx4_scales_bytes": (ctypes.c_size_t, [i64, i64]),
+        "fc_mx4_quantize": (i32, [P, i32, i64, i64, Mx4, P]),
+        "fc_mx4_dequantize": (i32, [Mx4, i64, i64, P, i32, P]),
+        "fc_mx4_matmul": (i32, [Mx4, Mx4, i64, i64, i64, P, i32, P, P]),
+        "fc_block_norm": (i32, [P, P, i64, i64, i32, P, P, P, Mx4, P]),
+        "fc_block_norm_backward_workspace": (ctypes.c_size_t, [i64, i64, i64]),
+        "fc_block_norm_backward": (i32, [P, P, P, P, i64, i64, i32, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -163,12 +190,14 @@ class Bound:
     itself.  The object holds a reference to every tensor it was bound to,
     so their memory cannot be freed and handed to another tensor while the
     bound call exists.  For the calls that carry an epoch (tagged formats),
-    `epoch` may be changed between calls."""
-    __slots__ = ("_fn", "_args", "_si", "_ei", "_keep")
+    `epoch` may be changed between calls.  A call bound to a `device` runs on
+    that device's current stream whichever device is current."""
+    __slots__ = ("_fn", "_args", "_si", "_ei", "_keep", "_dev")
 
-    def __init__(self, fn, args, stream_index, epoch_index=None, keep=()):
+    def __init__(self, fn, args, stream_index, epoch_index=None, keep=(), device=None):
         self._fn, self._args, self._si, self._ei, self._keep = fn, list(args), stream_index, \
             epoch_index, keep
+        self._dev = device
 
     @property
     def epoch(self) -> int:
@@ -179,6 +208,9 @@ class Bound:
         self._args[self._ei] = ctypes.c_uint32(e & 0xFFFFFFFF)
 
     def __call__(self, stream=None):
+        if self._dev is not None and torch.cuda.current_device() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self(stream)
         a = self._args
         a[self._si] = _stream(stream)
         st = self._fn(*a)
@@ -414,3 +446,205 @@ def protocol_estimate(rows: int, hidden: int, P: int, spec: QSpec,
                                        ctypes.byref(link) if link is not None else None,
                                        ctypes.byref(est)))
     return est.value
+
+
+# --------------------------------------------------- around the boundary ---
+def _dtype(t: torch.Tensor, name: str) -> int:
+    try:
+        return {torch.bfloat16: FMT_BF16, torch.float32: FMT_F32}[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})") from None
+
+
+def _want(t: Optional[torch.Tensor], shape, dtype, name: str):
+    """t's pointer, after checking its shape and type (None: NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} (got {tuple(t.shape)} {t.dtype})")
+    return _ptr(t)
+
+
+def _mx4(q, rows: int, hidden: int, name: str) -> Mx4:
+    if q is None:
+        return Mx4(None, None)
+    codes, scales = q
+    for t, n, what in ((codes, mx4_codes_bytes(rows, hidden), "codes"),
+                       (scales, mx4_scales_bytes(rows, hidden), "scales")):
+        if t.dtype != torch.uint8 or t.numel() < n:
+            raise ValueError(f"{name}'s {what} must be {n} uint8 (got {t.numel()} {t.dtype})")
+    return Mx4(_ptr(codes), _ptr(scales))
+
+
+def _one_device(*tensors) -> int:
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"the tensors of a call are on one device (got {sorted(map(str, devices))})")
+    return devices.pop().index
+
+
+def _once(call: Bound, stream):
+    """Run a call bound for this one time.  On a stream other than the current
+    one, its tensors' memory is kept from reuse until that stream is done."""
+    call(stream)
+    if isinstance(stream, torch.cuda.Stream):
+        for t in call._keep:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+
+
+def mx4_codes_bytes(rows: int, hidden: int) -> int:
+    return load().fc_mx4_codes_bytes(rows, hidden)
+
+
+def mx4_scales_bytes(rows: int, hidden: int) -> int:
+    return load().fc_mx4_scales_bytes(rows, hidden)
+
+
+def alloc_mx4(rows: int, hidden: int, device="cuda"):
+    """Caller-owned (codes, scales) of a microscaled 4-bit [rows, hidden] tensor."""
+    if hidden <= 0 or hidden % 32:
+        raise ValueError(f"hidden must be a positive multiple of 32 (got {hidden})")
+    return (torch.empty(rows, hidden // 2, dtype=torch.uint8, device=device),
+            torch.empty(mx4_scales_bytes(rows, hidden), dtype=torch.uint8, device=device))
+
+
+def bind_mx4_quantize(x: torch.Tensor, out) -> Bound:
+    rows, hidden = _rows_hidden(x)
+    return Bound(load().fc_mx4_quantize,
+                 [ctypes.c_void_p(_ptr(x)), _dtype(x, "x"), rows, hidden,
+                  _mx4(out, rows, hidden, "out"), None], 5,
+                 keep=(x, *out), device=_one_device(x, *out))
+
+
+def mx4_quantize(x: torch.Tensor, out, stream=None):
+    """Quantize [rows, hidden] bf16 or fp32 to microscaled 4-bit out = (codes, scales)."""
+    _once(bind_mx4_quantize(x, out), stream)
+
+
+def bind_mx4_dequantize(q, out: torch.Tensor) -> Bound:
+    rows, hidden = _rows_hidden(out)
+    return Bound(load().fc_mx4_dequantize,
+                 [_mx4(q, rows, hidden, "q"), rows, hidden, ctypes.c_void_p(_ptr(out)),
+                  _dtype(out, "out"), None], 5,
+                 keep=(*q, out), device=_one_device(*q, out))
+
+
+def mx4_dequantize(q, out: torch.Tensor, stream=None):
+    """out[rows, hidden] (bf16 or fp32) = the values q = (codes, scales) stands for."""
+    _once(bind_mx4_dequantize(q, out), stream)
+
+
+def bind_mx4_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None) -> Bound:
+    rows, features = _rows_hidden(out)
+    if w[0].dim() != 2 or w[0].shape[0] != features:
+        raise ValueError(f"w's codes must be [{features}, hidden / 2] (got {tuple(w[0].shape)})")
+    hidden = 2 * w[0].shape[1]
+    return Bound(load().fc_mx4_matmul,
+                 [_mx4(x, rows, hidden, "x"), _mx4(w, features, hidden, "w"), rows, features,
+                  hidden, ctypes.c_void_p(_ptr(out)), _dtype(out, "out"),
+                  ctypes.c_void_p(_want(d_status, (2,), torch.int32, "d_status")), None], 8,
+                 keep=(*x, *w, out, d_status), device=_one_device(*x, *w, out, d_status))
+
+
+def mx4_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None, stream=None):
+    """out[rows, features] = x w^T of two microscaled tensors: x = (codes, scales) of
+    [rows, hidden], w of [features, hidden], both as alloc_mx4 lays them out."""
+    _once(bind_mx4_matmul(x, w, out, d_status), stream)
+
+
+def _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
+                     pre_eps) -> BlockNormSpec:
+    rows, hidden = _rows_hidden(x)
+    gate_rows = 0
+    if gate is not None:
+        if gate.dim() != 2:
+            raise ValueError("gate must be [gate_rows, hidden]")
+        gate_rows = gate.shape[0]
+    return BlockNormSpec(_want(post_weight, (hidden,), x.dtype, "post_weight"),
+                         _want(gate, (gate_rows, hidden), x.dtype, "gate"),
+                         _want(pre_weight, (hidden,), x.dtype, "pre_weight"),
+                         gate_rows, residual_scale, block_scale, post_eps, pre_eps)
+
+
+def bind_block_norm(x: torch.Tensor, residual_in: Optional[torch.Tensor],
+                    residual_out: torch.Tensor, y: Optional[torch.Tensor] = None,
+                    post_weight: Optional[torch.Tensor] = None,
+                    gate: Optional[torch.Tensor] = None,
+                    pre_weight: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                    block_scale: float = 1.0, post_eps: float = 1e-5, pre_eps: float = 1e-5,
+                    y_mx4=None) -> Bound:
+    rows, hidden = _rows_hidden(x)
+    spec = _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
+                            pre_eps)
+    P = ctypes.c_void_p
+    args = [P(_ptr(x)), P(_want(residual_in, x.shape, x.dtype, "residual_in")), rows, hidden,
+            _dtype(x, "x"), ctypes.byref(spec),
+            P(_want(residual_out, x.shape, x.dtype, "residual_out")),
+            P(_want(y, x.shape, x.dtype, "y")), _mx4(y_mx4, rows, hidden, "y_mx4"), None]
+    keep = (x, residual_in, residual_out, y, post_weight, gate, pre_weight, *(y_mx4 or ()))
+    return Bound(load().fc_block_norm, args, 9, keep=(*keep, spec), device=_one_device(*keep))
+
+
+def block_norm(x: torch.Tensor, residual_in: Optional[torch.Tensor], residual_out: torch.Tensor,
+               y: Optional[torch.Tensor] = None, stream=None, **spec):
+    """The norms after a block and before the next, with the block's gate and the
+    residual scale, in one pass over the rows:
+
+    residual_out = residual_scale * residual_in + block_scale * gate * norm(x; post_weight)
+    y            = norm(residual_out; pre_weight)
+
+    x, residual_in, residual_out, y: [rows, hidden], bf16 or fp32.  Keywords:
+    post_weight, pre_weight [hidden] and gate [gate_rows, hidden], each optional
+    (rows / gate_rows neighbouring rows share a row of gate), residual_scale,
+    block_scale, post_eps, pre_eps; y_mx4 = (codes, scales) receives y quantised."""
+    _once(bind_block_norm(x, residual_in, residual_out, y, **spec), stream)
+
+
+def alloc_block_norm_workspace(rows: int, hidden: int, gate_rows: int = 0, device="cuda"):
+    """Workspace of one block_norm_backward call at a time (gate_rows: 0 without a gate)."""
+    n = load().fc_block_norm_backward_workspace(rows, hidden, gate_rows)
+    return torch.empty(max(n, 32), dtype=torch.uint8, device=device)
+
+
+def bind_block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor],
+                             dy: Optional[torch.Tensor], dh: Optional[torch.Tensor],
+                             dx: torch.Tensor, workspace: torch.Tensor,
+                             dresidual: Optional[torch.Tensor] = None,
+                             dpost_weight: Optional[torch.Tensor] = None,
+                             dgate: Optional[torch.Tensor] = None,
+                             dpre_weight: Optional[torch.Tensor] = None,
+                             post_weight: Optional[torch.Tensor] = None,
+                             gate: Optional[torch.Tensor] = None,
+                             pre_weight: Optional[torch.Tensor] = None,
+                             residual_scale: float = 1.0, block_scale: float = 1.0,
+                             post_eps: float = 1e-5, pre_eps: float = 1e-5) -> Bound:
+    rows, hidden = _rows_hidden(x)
+    spec = _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
+                            pre_eps)
+    need = load().fc_block_norm_backward_workspace(rows, hidden, spec.gate_rows)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    grads = BlockNormGrads(_want(dx, x.shape, x.dtype, "dx"),
+                           _want(dresidual, x.shape, x.dtype, "dresidual"),
+                           _want(dpost_weight, (hidden,), torch.float32, "dpost_weight"),
+                           _want(dgate, (spec.gate_rows, hidden), x.dtype, "dgate"),
+                           _want(dpre_weight, (hidden,), torch.float32, "dpre_weight"))
+    P = ctypes.c_void_p
+    args = [P(_ptr(x)), P(_want(h, x.shape, x.dtype, "h")), P(_want(dy, x.shape, x.dtype, "dy")),
+            P(_want(dh, x.shape, x.dtype, "dh")), rows, hidden, _dtype(x, "x"),
+            ctypes.byref(spec), ctypes.byref(grads), P(_ptr(workspace)), None]
+    keep = (x, h, dy, dh, dx, workspace, dresidual, dpost_weight, dgate, dpre_weight, post_weight,
+            gate, pre_weight)
+    return Bound(load().fc_block_norm_backward, args, 10, keep=(*keep, spec, grads),
+                 device=_one_device(*keep))
+
+
+def block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor], dy: Optional[torch.Tensor],
+                        dh: Optional[torch.Tensor], dx: torch.Tensor, workspace: torch.Tensor,
+                        stream=None, **kw):
+    """Gradient of block_norm.  x and h (= residual_out) are what the forward pass
+    read and wrote, dy and dh the gradients of y and residual_out; writes dx and,
+    where given, dresidual, dpost_weight, dpre_weight (fp32) and dgate.  Keywords
+    as block_norm's; workspace from alloc_block_norm_workspace."""
+    _once(bind_block_norm_backward(x, h, dy, dh, dx, workspace, **kw), stream)
