@@ -401,7 +401,8 @@ fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, in
  * workspace: fc_block_norm_backward_workspace bytes, 32-byte aligned, this
  * call's own until it has run.  rows == 0 sets the weights' gradients that are
  * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual may be x, h, dy or dh itself;
- * outputs overlap nothing else. */
+ * outputs overlap nothing else.  d_status: optional, as for fc_group_quantize (a
+ * staged row that never lands). */
 typedef struct {
   void* dx;
   void* dresidual;
@@ -414,7 +415,7 @@ size_t fc_block_norm_backward_workspace(int64_t rows, int64_t hidden, int64_t ga
 fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, const void* dh,
                                  int64_t rows, int64_t hidden, int32_t dtype,
                                  const fc_block_norm_spec* spec, const fc_block_norm_grads* grads,
-                                 void* workspace, fc_stream_t stream);
+                                 void* workspace, int32_t* d_status, fc_stream_t stream);
 
 /* --------------------------------------------------------------- misc --- */
 const char* fc_status_string(fc_status s);

@@ -696,7 +696,7 @@ size_t fc_block_norm_backward_workspace(int64_t rows, int64_t hidden, int64_t ga
 fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, const void* dh,
                                  int64_t rows, int64_t hidden, int32_t dtype,
                                  const fc_block_norm_spec* spec, const fc_block_norm_grads* grads,
-                                 void* workspace, fc_stream_t stream) {
+                                 void* workspace, int32_t* d_status, fc_stream_t stream) {
   if (fc_status s = check_rows_hidden(rows, hidden, 16, fc::kBlockNormMaxHidden)) return s;
   if (fc_status s = check_dtype(dtype, "dtype")) return s;
   if (fc_status s = check_block_norm_spec(spec, rows)) return s;
@@ -729,6 +729,7 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
   if (fc_status s = check_ptr(g.dx, 32, "dx")) return s;
   if (g.dresidual && !aligned(g.dresidual, 32)) return fail(FC_ERR_INVALID, "dresidual must be 32-byte aligned");
   if (fc_status s = check_ptr(workspace, 32, "workspace")) return s;
+  if (d_status && !aligned(d_status, 4)) return fail(FC_ERR_INVALID, "d_status must be 4-byte aligned");
   const Span o[] = {
       {g.dx, n * es, "dx", false},
       {g.dresidual, n * es, "dresidual", false},
@@ -758,6 +759,7 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
   a.dpost_w = g.dpost_weight;
   a.dpre_w = g.dpre_weight;
   a.ws = static_cast<float*>(workspace);
+  a.status = d_status;
   a.rows = rows;
   a.gate_rows = spec->gate_rows;
   a.H = static_cast<int>(hidden);
@@ -765,6 +767,7 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
   a.beta = spec->block_scale;
   a.eps_post = spec->post_eps;
   a.eps_pre = spec->pre_eps;
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
   return cuda_status(fc::launch_block_norm_grad(dtype == FC_FMT_F32, a, (cudaStream_t)stream),
                      "fc_block_norm_backward launch");
 }

@@ -50,6 +50,7 @@ struct BlockNormGradArgs {
   float* dpost_w;
   float* dpre_w;
   float* ws;
+  int32_t* status;      // NULL, or word 0 set to FC_ERR_CUDA if a staged row never lands
   int64_t rows;
   int64_t gate_rows;
   int H;

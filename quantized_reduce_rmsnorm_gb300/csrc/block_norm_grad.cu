@@ -23,6 +23,8 @@
 namespace fc {
 namespace {
 
+constexpr int kErrCuda = 2;  // FC_ERR_CUDA
+
 // Sums over the row's threads of N values at once; red: N * 32 floats.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* red) {
@@ -196,60 +198,369 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
   }
 }
 
-// Adds the CTAs' sums: 32 columns a CTA, eight warps over the addends, in a
-// fixed order.  blockIdx.y: 0 the norm before, 1 the norm after, 2 + s gate row s.
+// ------------------------------------------------------ staged rows -----
+// The same gradient with the rows staged in shared memory by bulk copies, and
+// all of a row's sums taken at once.  With a = dy * pre_weight, gw = beta * gate *
+// post_weight (one factor a column) and k = inv_h^3 * mean(a * h):
+//   dh' = dh + inv_h * a - k * h
+//   sum(e * x) = sum gw x dh + inv_h * sum gw x a - k * sum gw x h
+// so the six sums h^2, a h, x^2, gw x dh, gw x a and gw x h, which need nothing of
+// the row before them, give every factor of the row: one barrier a row, and the
+// row goes from shared memory to registers once.  Its stage is free again at
+// that barrier.  With r = sum over rows of inv_x * dh' * x (one column), dgate =
+// beta * post_weight * r and, for a gate that the piece's rows share,
+// dpost_weight = beta * gate * r: one running sum serves both.  It and
+// dpre_weight's are in registers.  A thread has eight columns, in groups of 16
+// bytes, the live threads side by side: no bank conflicts.
+constexpr int kW = 8;  // columns of a thread
+
 template <bool F32>
-__global__ void __launch_bounds__(256) k_block_norm_grad_sum(const GradJob job) {
-  __shared__ float red[8][32];
-  pdl_begin();
-  const int H = job.a.H, col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
-  for (int64_t y = blockIdx.y;; y += gridDim.y) {
-    const float* src;
-    int n;
-    if (y == 0) {
-      src = job.a.dpre_w ? job.ws_pre : nullptr, n = job.p.grid;
-    } else if (y == 1) {
-      src = job.a.dpost_w ? job.ws_post : nullptr, n = job.p.grid;
-    } else {
-      if (!job.ws_gate || y - 2 >= job.p.segs) return;
-      src = job.ws_gate + (y - 2) * job.p.cuts * H, n = job.p.cuts;
-    }
-    if (!src) continue;
-    float s = 0.0f;
-    if (col < H)
-      for (int i = w; i < n; i += 8) s += src[static_cast<int64_t>(i) * H + col];
-    red[w][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (w == 0 && col < H) {
+struct Cols {
+  static constexpr int kPer = F32 ? 4 : 8;  // columns of a group
+  static constexpr int kGroups = kW / kPer;
+  // first column of group j of thread t, `live` threads in all
+  static __device__ __forceinline__ int at(int j, int t, int live) { return (j * live + t) * kPer; }
+};
+
+template <bool F32>
+struct RawCols {
+  uint4 g[Cols<F32>::kGroups];
+};
+// The thread's columns of a row (or of a weight), from shared or global memory.
+template <bool F32>
+__device__ __forceinline__ RawCols<F32> load_cols(const void* row, int t, int live) {
+  constexpr int es = F32 ? 4 : 2;
+  RawCols<F32> r;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
-      if (y == 0)
-        job.a.dpre_w[col] = s;
-      else if (y == 1)
-        job.a.dpost_w[col] = s;
-      else if (F32)
-        static_cast<float*>(job.a.dgate)[(y - 2) * H + col] = s;
-      else
-        static_cast<__nv_bfloat16*>(job.a.dgate)[(y - 2) * H + col] = __float2bfloat16_rn(s);
-    }
-    __syncthreads();
+  for (int j = 0; j < Cols<F32>::kGroups; ++j)
+    r.g[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + Cols<F32>::at(j, t, live) * es);
+  return r;
+}
+// Columns 2i and 2i + 1 of them.
+template <bool F32>
+__device__ __forceinline__ float2 pair(const RawCols<F32>& r, int i) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.g);
+  if constexpr (F32) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  return make_float2(bf_lo(w[i]), bf_hi(w[i]));
+}
+template <bool F32>
+__device__ __forceinline__ void store_cols(void* row, int t, int live, const float2 f[kW / 2]) {
+  constexpr int es = F32 ? 4 : 2;
+#pragma unroll
+  for (int j = 0; j < Cols<F32>::kGroups; ++j) {
+    uint4 w;
+    if constexpr (F32)
+      w = make_uint4(__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y), __float_as_uint(f[2 * j + 1].x),
+                     __float_as_uint(f[2 * j + 1].y));
+    else
+      w = make_uint4(pack_bf2(f[0].x, f[0].y), pack_bf2(f[1].x, f[1].y), pack_bf2(f[2].x, f[2].y),
+                     pack_bf2(f[3].x, f[3].y));
+    st128(static_cast<char*>(row) + Cols<F32>::at(j, t, live) * es, w);
+  }
+}
+// The same columns of a row of fp32 sums.
+template <bool F32>
+__device__ __forceinline__ void store_sums(float* row, int t, int live, const float2 f[kW / 2]) {
+#pragma unroll
+  for (int k = 0; k < kW / 4; ++k) {
+    const int at = F32 ? Cols<F32>::at(k, t, live) : Cols<F32>::at(0, t, live) + 4 * k;
+    *reinterpret_cast<float4*>(row + at) = make_float4(f[2 * k].x, f[2 * k].y, f[2 * k + 1].x, f[2 * k + 1].y);
   }
 }
 
-template <bool F32, int MAXT>
-cudaError_t launch(GradJob& job, int threads, cudaStream_t st) {
-  auto* kern = k_block_norm_grad<F32, MAXT>;
-  const int smem = threads * 12 * static_cast<int>(sizeof(float4));
-  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem)) return e;
-  const int occ = occupancy_memo(reinterpret_cast<const void*>(kern), threads, smem, 1, [&] {
-    int v = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem);
-    return v;
-  });
-  if (occ < 1) return cudaErrorInvalidConfiguration;
+// Sums of eight values over the CTA, each thread ending with all eight.  Within a
+// warp the values are folded onto one another (lanes give away the half that
+// the other lanes keep), so that eight sums take 9 shuffles and not 40; lane l
+// ends with value l / 4.  red: 8 rows of kRedStride floats (an odd number of
+// 16-byte groups apart: no bank conflicts), one for each warp, those past the
+// CTA's warps 0.
+constexpr int kRedStride = 36;
+__device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
+  const int l = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 16, n = 4; m >= 4; m >>= 1, n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool hi = l & m;
+      const float keep = hi ? v[i + n] : v[i], give = hi ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(kFull, give, m);
+    }
+  float s = v[0];
+  s += __shfl_xor_sync(kFull, s, 2);
+  s += __shfl_xor_sync(kFull, s, 1);
+  float* mine = red + (l >> 2) * kRedStride;
+  if ((l & 3) == 0) mine[threadIdx.x >> 5] = s;
+  __syncthreads();
+  const float4 a = *reinterpret_cast<const float4*>(mine + (l & 3) * 8);
+  const float4 b = *reinterpret_cast<const float4*>(mine + (l & 3) * 8 + 4);
+  s = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  s += __shfl_xor_sync(kFull, s, 2);
+  s += __shfl_xor_sync(kFull, s, 1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kFull, s, i * 4);
+}
+
+// 1 / sqrt(v): the hardware's approximation (relative error about 2^-22) and one
+// step of Newton's method, which squares the error; what is left is its
+// rounding, below 2^-22.  v > 0 and finite, or 0 (infinity, as of 1 / sqrt(0)).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float y = rsqrtf(v);
+  const float e = __fmaf_rn(-v * y, y, 1.0f);  // 1 - v y^2
+  const float r = __fmaf_rn(0.5f * y, e, y);
+  return v > 0.0f ? r : y;
+}
+
+constexpr int kMostStages = 4;
+
+// TOKEN: a gate row for every row, staged with the row.
+template <bool F32, bool TOKEN, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const GradJob job, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) float red[2][8 * kRedStride];  // neighbouring rows take turns
+  __shared__ uint64_t full[kMostStages];
+  __shared__ volatile int late;
+  __shared__ struct { int piece, row, end, count; } next;
+  constexpr int es = F32 ? 4 : 2, kP = kW / 2;
+  const BlockNormGradArgs& a = job.a;
+  const GradPlan& p = job.p;
+  const int t = threadIdx.x, live = a.H / kW;
+  const int H = a.H, row_bytes = H * es;
+  const bool on = t < live;
+  const bool pre = a.dy != nullptr, post = a.post_w != nullptr;
+  // slots of a stage: x, h, dy, dh, gate row; absent tensors take none
+  const int slot_h = 1, slot_dy = 2, slot_dh = pre ? 3 : 1, slot_g = slot_dh + (a.dh ? 1 : 0);
+  const int slots = slot_g + (TOKEN ? 1 : 0);
+  float4* acc_post = reinterpret_cast<float4*>(ring + static_cast<size_t>(stages) * slots * row_bytes);
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(full + s, 1);
+    late = 0;
+    mbar_init_fence();
+  }
+  for (int i = t; i < 2 * 8 * kRedStride; i += blockDim.x) red[0][i] = 0.0f;
+  for (int j = 0; j < kW / 4; ++j) acc_post[j * blockDim.x + t] = make_float4(0, 0, 0, 0);
+  __syncthreads();
+  pdl_begin();
+
+  const int pieces = static_cast<int>(p.segs) * p.cuts;  // at most the rows
+  auto piece_rows = [&](int piece, int& r0, int& r1) {
+    const int seg = piece / p.cuts, cut = piece - seg * p.cuts;
+    r0 = static_cast<int>(seg * p.seg_rows + p.seg_rows * cut / p.cuts);
+    r1 = static_cast<int>(seg * p.seg_rows + p.seg_rows * (cut + 1) / p.cuts);
+  };
+  // Stages the next row (thread 0; `next` keeps its place out of the registers).
+  auto stage_next = [&] {
+    if (next.piece >= pieces) return;
+    const int s = next.count++ % stages, row = next.row++;
+    fence_proxy_async_smem();
+    uint8_t* dst = ring + static_cast<size_t>(s) * slots * row_bytes;
+    const int64_t off = static_cast<int64_t>(row) * row_bytes;
+    auto copy = [&](int slot, const void* src) {
+      bulk_load(dst + slot * row_bytes, static_cast<const char*>(src) + off, row_bytes, full + s);
+    };
+    mbar_expect_tx(full + s, slots * row_bytes);
+    copy(0, a.x);
+    if (pre) copy(slot_h, a.h), copy(slot_dy, a.dy);
+    if (a.dh) copy(slot_dh, a.dh);
+    if (TOKEN) copy(slot_g, a.gate);
+    if (row + 1 == next.end) {
+      next.piece += gridDim.x;
+      if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
+    }
+  };
+  if (t == 0) {
+    next.piece = blockIdx.x;
+    next.count = 0;
+    if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
+    for (int s = 0; s < stages; ++s) stage_next();
+  }
+
+  const float inv_n = 1.0f / static_cast<float>(H);
+  const float2 zero = make_float2(0.0f, 0.0f);
+  float2 gw[kP], acc_pre[kP], acc_r[kP];
+  RawCols<F32> w2{};
+  if (on && a.pre_w) w2 = load_cols<F32>(a.pre_w, t, live);
+#pragma unroll
+  for (int i = 0; i < kP; ++i) acc_pre[i] = acc_r[i] = zero;
+  int count = 0, s = 0;  // rows done; the row's stage
+  uint32_t phase = 0;
+  bool stop = false;
+  for (int piece = blockIdx.x; piece < pieces && !stop; piece += gridDim.x) {
+    int r0, r1;
+    piece_rows(piece, r0, r1);
+    const int64_t seg_off = static_cast<int64_t>(piece / p.cuts) * row_bytes;  // its gate row
+#pragma unroll
+    for (int i = 0; i < kP; ++i) gw[i] = dup2(a.beta);
+    if (on && post) {
+      const RawCols<F32> w = load_cols<F32>(a.post_w, t, live);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32>(w, i));
+    }
+    if (on && !TOKEN && a.gate) {
+      const RawCols<F32> w = load_cols<F32>(static_cast<const char*>(a.gate) + seg_off, t, live);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32>(w, i));
+    }
+    for (int row = r0; row < r1; ++row, ++count) {
+      const int64_t off = static_cast<int64_t>(row) * row_bytes;
+      const uint8_t* src = ring + s * slots * row_bytes;
+      if (!mbar_wait_bounded(full + s, phase)) late = 1;
+      RawCols<F32> x, h{}, dy{}, dh{}, g;
+      float r[8] = {};
+      if (on) {
+        x = load_cols<F32>(src, t, live);
+        if (pre) h = load_cols<F32>(src + slot_h * row_bytes, t, live);
+        if (pre) dy = load_cols<F32>(src + slot_dy * row_bytes, t, live);
+        if (a.dh) dh = load_cols<F32>(src + slot_dh * row_bytes, t, live);
+        if (TOKEN) g = load_cols<F32>(src + slot_g * row_bytes, t, live);
+        float2 s0 = zero, s1 = zero, s2 = zero, s3 = zero, s4 = zero, s5 = zero;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const float2 xi = pair<F32>(x, i), hi = pair<F32>(h, i), ai = pmul(pair<F32>(dy, i), pair<F32>(w2, i));
+          float2 gx = pmul(gw[i], xi);
+          if (TOKEN) gx = pmul(gx, pair<F32>(g, i));
+          s0 = pfma(hi, hi, s0);
+          s1 = pfma(ai, hi, s1);
+          s2 = pfma(xi, xi, s2);
+          s3 = pfma(gx, pair<F32>(dh, i), s3);
+          s4 = pfma(gx, ai, s4);
+          s5 = pfma(gx, hi, s5);
+        }
+        r[0] = s0.x + s0.y, r[1] = s1.x + s1.y, r[2] = s2.x + s2.y;
+        r[3] = s3.x + s3.y, r[4] = s4.x + s4.y, r[5] = s5.x + s5.y;
+      }
+      row_sums8(r, red[count & 1]);
+      if (late) {
+        stop = true;
+        break;
+      }
+      if (t == 0) stage_next();
+      if (++s == stages) s = 0, phase ^= 1;
+      const float inv = pre ? inv_sqrt(__fadd_rn(r[0] * inv_n, a.eps_pre)) : 0.0f;
+      const float k = inv * inv * inv * (r[1] * inv_n);
+      const float inv_x = post ? inv_sqrt(__fadd_rn(r[2] * inv_n, a.eps_post)) : 1.0f;
+      const float c = inv_x * inv_x * inv_x * (__fmaf_rn(inv, r[4], r[3]) - k * r[5]) * inv_n;
+      if (!on) continue;
+      const float2 vi = dup2(inv), vk = dup2(-k), vx = dup2(inv_x), vc = dup2(-c);
+      float2 d[kP], o[kP];
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float2 hi = pair<F32>(h, i), e = pmul(pair<F32>(dy, i), vi);
+        acc_pre[i] = pfma(e, hi, acc_pre[i]);
+        d[i] = padd(pair<F32>(dh, i), pfma(e, pair<F32>(w2, i), pmul(vk, hi)));
+      }
+      if (a.dres) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = pmul(d[i], dup2(a.alpha));
+        store_cols<F32>(static_cast<char*>(a.dres) + off, t, live, o);
+      }
+      if (TOKEN) {
+        // dgate row = beta * post_weight * dh' * xh; what remains is as without a gate
+        if (a.dgate) {
+#pragma unroll
+          for (int i = 0; i < kP; ++i) o[i] = pmul(pmul(gw[i], vx), pmul(d[i], pair<F32>(x, i)));
+          store_cols<F32>(static_cast<char*>(a.dgate) + off, t, live, o);
+        }
+#pragma unroll
+        for (int i = 0; i < kP; ++i) d[i] = pmul(d[i], pair<F32>(g, i));
+      }
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float2 xi = pair<F32>(x, i);
+        acc_r[i] = pfma(pmul(d[i], xi), vx, acc_r[i]);
+        o[i] = pmul(pmul(d[i], gw[i]), vx);
+        if (post) o[i] = pfma(xi, vc, o[i]);
+      }
+      store_cols<F32>(static_cast<char*>(a.dx) + off, t, live, o);
+    }
+    if (on && !stop) {
+      float2 o[kP];
+      if (a.dgate && !TOKEN) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = pmul(acc_r[i], dup2(a.beta));
+        if (post) {
+          const RawCols<F32> w = load_cols<F32>(a.post_w, t, live);
+#pragma unroll
+          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32>(w, i));
+        }
+        if (p.gate_final)
+          store_cols<F32>(static_cast<char*>(a.dgate) + seg_off, t, live, o);
+        else
+          store_sums<F32>(job.ws_gate + static_cast<int64_t>(piece) * H, t, live, o);
+      }
+      if (a.dpost_w) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = pmul(acc_r[i], dup2(a.beta));
+        if (!TOKEN && a.gate) {
+          const RawCols<F32> w = load_cols<F32>(static_cast<const char*>(a.gate) + seg_off, t, live);
+#pragma unroll
+          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32>(w, i));
+        }
+#pragma unroll
+        for (int j = 0; j < kW / 4; ++j) {
+          float4 x = acc_post[j * blockDim.x + t];
+          x.x += o[2 * j].x, x.y += o[2 * j].y, x.z += o[2 * j + 1].x, x.w += o[2 * j + 1].y;
+          acc_post[j * blockDim.x + t] = x;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kP; ++i) acc_r[i] = zero;
+    }
+  }
+  if (on && !stop) {
+    if (a.dpre_w) store_sums<F32>(job.ws_pre + static_cast<int64_t>(blockIdx.x) * H, t, live, acc_pre);
+    if (a.dpost_w) {
+      float2 o[kP];
+#pragma unroll
+      for (int j = 0; j < kW / 4; ++j) {
+        const float4 x = acc_post[j * blockDim.x + t];
+        o[2 * j] = make_float2(x.x, x.y), o[2 * j + 1] = make_float2(x.z, x.w);
+      }
+      store_sums<F32>(job.ws_post + static_cast<int64_t>(blockIdx.x) * H, t, live, o);
+    }
+  }
+  if (stop && t == 0) {  // a copy never landed: say so, and let those in flight land
+    if (a.status) *a.status = kErrCuda;
+    for (int i = count; i < next.count; ++i) mbar_wait_bounded(full + i % stages, (i / stages) & 1);
+  }
+}
+
+constexpr int kSumWarps = 16, kSumCols = 64;
+// Adds the CTAs' sums: 64 columns a CTA (a lane has two), 16 warps over the
+// addends, in a fixed order.  blockIdx.y: 0 the norm before, 1 the norm after, 2 +
+// s gate row s (segs is below kNormGradMaxCtas where their sums are in pieces).
+template <bool F32>
+__global__ void __launch_bounds__(kSumWarps * 32) k_block_norm_grad_sum(const GradJob job) {
+  __shared__ float2 red[kSumWarps][32];
+  pdl_begin();
+  const int H = job.a.H, l = threadIdx.x & 31, w = threadIdx.x >> 5, y = blockIdx.y;
+  const int col = blockIdx.x * kSumCols + 2 * l;
+  const float* src = y == 0 ? job.ws_pre : y == 1 ? job.ws_post : job.ws_gate + (y - 2) * static_cast<int64_t>(job.p.cuts) * H;
+  const int n = y < 2 ? job.p.grid : job.p.cuts;
+  if ((y == 0 && !job.a.dpre_w) || (y == 1 && !job.a.dpost_w)) return;
+  float2 s = make_float2(0.0f, 0.0f);
+  if (col < H)
+#pragma unroll 8
+    for (int i = w; i < n; i += kSumWarps) s = padd(s, *reinterpret_cast<const float2*>(src + static_cast<int64_t>(i) * H + col));
+  red[w][l] = s;
+  __syncthreads();
+  if (w != 0 || col >= H) return;
+#pragma unroll
+  for (int i = 1; i < kSumWarps; ++i) s = padd(s, red[i][l]);
+  if (y < 2) {  // 4-byte aligned
+    float* out = (y == 0 ? job.a.dpre_w : job.a.dpost_w) + col;
+    out[0] = s.x, out[1] = s.y;
+  } else if (F32) {
+    *reinterpret_cast<float2*>(static_cast<float*>(job.a.dgate) + static_cast<int64_t>(y - 2) * H + col) = s;
+  } else {
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(job.a.dgate) + static_cast<int64_t>(y - 2) * H + col) =
+        pack_bf2(s.x, s.y);
+  }
+}
+
+// Cuts the rows for `most` CTAs and lays the workspace out.
+void plan(GradJob& job, int64_t most) {
   const BlockNormGradArgs& a = job.a;
   GradPlan& p = job.p;
-  const int64_t most = std::min<int64_t>(kNormGradMaxCtas, static_cast<int64_t>(num_sms()) * occ);
   p.gate_direct = a.gate && a.gate_rows == a.rows;
   p.segs = a.gate && !p.gate_direct ? a.gate_rows : 1;
   p.seg_rows = a.rows / p.segs;
@@ -257,16 +568,62 @@ cudaError_t launch(GradJob& job, int threads, cudaStream_t st) {
   p.cuts = static_cast<int>(std::max<int64_t>(1, std::min(most / p.segs, p.seg_rows)));
   p.gate_final = p.cuts == 1;
   p.grid = static_cast<int>(std::min(most, p.segs * p.cuts));
-  const int64_t H = a.H;
   job.ws_pre = a.ws;
-  job.ws_post = a.ws + p.grid * H;
-  const bool sum_gate = a.dgate && !p.gate_direct && !p.gate_final;
-  job.ws_gate = sum_gate ? a.ws + 2 * p.grid * H : nullptr;
-  if (cudaError_t e = launch_pdl(kern, dim3(p.grid), dim3(threads), smem, st, job)) return e;
-  if (!a.dpre_w && !a.dpost_w && !sum_gate) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((H + 31) / 32),
-                  static_cast<unsigned>(std::min<int64_t>(65535, 2 + (sum_gate ? p.segs : 0))));
-  return launch_pdl(k_block_norm_grad_sum<F32>, grid, dim3(256), 0, st, job);
+  job.ws_post = a.ws + static_cast<int64_t>(p.grid) * a.H;
+  job.ws_gate = a.dgate && !p.gate_direct && !p.gate_final ? a.ws + 2 * static_cast<int64_t>(p.grid) * a.H : nullptr;
+}
+
+// CTAs that the GPU holds at once, 0 if none fits.
+template <class K>
+int64_t resident(K* kern, int threads, int smem) {
+  if (raise_smem_limit(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return 0;
+  const int occ = occupancy_memo(reinterpret_cast<const void*>(kern), threads, smem, 1, [&] {
+    int v = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem);
+    return v;
+  });
+  return std::min<int64_t>(kNormGradMaxCtas, static_cast<int64_t>(num_sms()) * occ);
+}
+
+template <bool F32, int MAXT>
+cudaError_t launch_direct(GradJob& job, int threads, cudaStream_t st) {
+  auto* kern = k_block_norm_grad<F32, MAXT>;
+  const int smem = threads * 12 * static_cast<int>(sizeof(float4));
+  const int64_t most = resident(kern, threads, smem);
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  plan(job, most);
+  return launch_pdl(kern, dim3(job.p.grid), dim3(threads), smem, st, job);
+}
+
+template <bool F32, bool TOKEN, int MAXT, int MINB>
+cudaError_t launch_staged(GradJob& job, int threads, int stages, int smem, cudaStream_t st) {
+  auto* kern = k_block_norm_grad_staged<F32, TOKEN, MAXT, MINB>;
+  const int64_t most = resident(kern, threads, smem);
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  plan(job, most);
+  return launch_pdl(kern, dim3(job.p.grid), dim3(threads), smem, st, job, stages);
+}
+
+template <bool F32, bool TOKEN>
+cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
+  const BlockNormGradArgs& a = job.a;
+  const int slots = 1 + (a.dy ? 2 : 0) + (a.dh ? 1 : 0) + (TOKEN ? 1 : 0);
+  const int threads = (a.H / kW + 31) / 32 * 32;
+  const int stage = slots * a.H * (F32 ? 4 : 2), acc = threads * kW * 4;
+  constexpr int kMost = 220 * 1024;
+  // two CTAs an SM where both have two stages, else one with as many as fit
+  int stages = std::min(kMostStages, (kMost / 2 - acc) / stage);
+  if (threads <= 256 && stages >= 2)
+    return launch_staged<F32, TOKEN, 256, 2>(job, threads, stages, stages * stage + acc, st);
+  if (threads <= 384 && stages >= 2)
+    return launch_staged<F32, TOKEN, 384, 2>(job, threads, stages, stages * stage + acc, st);
+  stages = std::min(kMostStages, (kMost - acc) / stage);
+  if (threads <= 640 && stages >= 1)
+    return launch_staged<F32, TOKEN, 640, 1>(job, threads, stages, stages * stage + acc, st);
+  if (threads <= 1024 && stages >= 1)
+    return launch_staged<F32, TOKEN, 1024, 1>(job, threads, stages, stages * stage + acc, st);
+  const int wide = (a.H / 16 + 31) / 32 * 32;  // 16 columns a thread
+  return wide <= 512 ? launch_direct<F32, 512>(job, wide, st) : launch_direct<F32, 1024>(job, wide, st);
 }
 
 }  // namespace
@@ -274,9 +631,16 @@ cudaError_t launch(GradJob& job, int threads, cudaStream_t st) {
 cudaError_t launch_block_norm_grad(bool f32, const BlockNormGradArgs& a, cudaStream_t st) {
   GradJob job{};
   job.a = a;
-  const int threads = (a.H / 16 + 31) / 32 * 32;
-  if (threads <= 512) return f32 ? launch<true, 512>(job, threads, st) : launch<false, 512>(job, threads, st);
-  return f32 ? launch<true, 1024>(job, threads, st) : launch<false, 1024>(job, threads, st);
+  const bool token = a.gate && a.gate_rows == a.rows;
+  if (cudaError_t e = f32 ? token ? launch_grad<true, true>(job, st) : launch_grad<true, false>(job, st)
+                          : token ? launch_grad<false, true>(job, st)
+                                  : launch_grad<false, false>(job, st))
+    return e;
+  const bool sum_gate = job.ws_gate != nullptr;
+  if (!a.dpre_w && !a.dpost_w && !sum_gate) return cudaSuccess;
+  const dim3 grid((a.H + kSumCols - 1) / kSumCols, static_cast<unsigned>(2 + (sum_gate ? job.p.segs : 0)));
+  return f32 ? launch_pdl(k_block_norm_grad_sum<true>, grid, dim3(kSumWarps * 32), 0, st, job)
+             : launch_pdl(k_block_norm_grad_sum<false>, grid, dim3(kSumWarps * 32), 0, st, job);
 }
 
 }  // namespace fc

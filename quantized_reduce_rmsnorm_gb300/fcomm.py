@@ -140,7 +140,7 @@ def load(path: Optional[str] = None):
         "fc_mx4_matmul": (i32, [Mx4, Mx4, i64, i64, i64, P, i32, P, P]),
         "fc_block_norm": (i32, [P, P, i64, i64, i32, P, P, P, Mx4, P]),
         "fc_block_norm_backward_workspace": (ctypes.c_size_t, [i64, i64, i64]),
-        "fc_block_norm_backward": (i32, [P, P, P, P, i64, i64, i32, P, P, P, P]),
+        "fc_block_norm_backward": (i32, [P, P, P, P, i64, i64, i32, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -166,8 +166,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: a torch Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -618,7 +618,8 @@ def bind_block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor],
                              gate: Optional[torch.Tensor] = None,
                              pre_weight: Optional[torch.Tensor] = None,
                              residual_scale: float = 1.0, block_scale: float = 1.0,
-                             post_eps: float = 1e-5, pre_eps: float = 1e-5) -> Bound:
+                             post_eps: float = 1e-5, pre_eps: float = 1e-5,
+                             d_status: Optional[torch.Tensor] = None) -> Bound:
     rows, hidden = _rows_hidden(x)
     spec = _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
                             pre_eps)
@@ -633,10 +634,11 @@ def bind_block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor],
     P = ctypes.c_void_p
     args = [P(_ptr(x)), P(_want(h, x.shape, x.dtype, "h")), P(_want(dy, x.shape, x.dtype, "dy")),
             P(_want(dh, x.shape, x.dtype, "dh")), rows, hidden, _dtype(x, "x"),
-            ctypes.byref(spec), ctypes.byref(grads), P(_ptr(workspace)), None]
+            ctypes.byref(spec), ctypes.byref(grads), P(_ptr(workspace)),
+            P(_want(d_status, (2,), torch.int32, "d_status")), None]
     keep = (x, h, dy, dh, dx, workspace, dresidual, dpost_weight, dgate, dpre_weight, post_weight,
-            gate, pre_weight)
-    return Bound(load().fc_block_norm_backward, args, 10, keep=(*keep, spec, grads),
+            gate, pre_weight, d_status)
+    return Bound(load().fc_block_norm_backward, args, 11, keep=(*keep, spec, grads),
                  device=_one_device(*keep))
 
 

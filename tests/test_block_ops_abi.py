@@ -122,8 +122,8 @@ def test_block_norm_refusals():
     assert fc.load().fc_block_norm(*norm(pre, rows=0, y=A[3])) == fc.FC_OK
 
 
-def back(sp, g, x=A[0], h=A[1], dy=A[2], dh=A[3], rows=6, hidden=64, dtype=BF16, ws=A[4]):
-    return (x, h, dy, dh, rows, hidden, dtype, ctypes.byref(sp), None if g is None else ctypes.byref(g), ws, None)
+def back(sp, g, x=A[0], h=A[1], dy=A[2], dh=A[3], rows=6, hidden=64, dtype=BF16, ws=A[4], st=None):
+    return (x, h, dy, dh, rows, hidden, dtype, ctypes.byref(sp), None if g is None else ctypes.byref(g), ws, st, None)
 
 
 def test_block_norm_backward_refusals():
@@ -140,6 +140,7 @@ def test_block_norm_backward_refusals():
     refused(n, *back(full, fc.BlockNormGrads(None, A[9])), says="dx")
     refused(n, *back(full, g, ws=None), says="workspace")
     refused(n, *back(full, g, ws=A[4] + 16), says="workspace")
+    refused(n, *back(full, g, st=A[13] + 2), says="d_status")
     refused(n, *back(full, fc.BlockNormGrads(A[8], A[8])), says="overlaps")
     refused(n, *back(full, fc.BlockNormGrads(A[8], None, None, A[6])), says="overlaps")
     refused(n, *back(full, g, ws=A[12]), says="overlaps")
