@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float red[2][8 * kRedStride];  // neighbouring rows take turns
   __shared__ uint64_t full[kMostStages];
-  __shared__ volatile int late;
+  __shared__ volatile int late[2];  // a copy did not land in time, by turns as red
   __shared__ struct { int piece, row, end, count; } next;
   constexpr int es = F32 ? 4 : 2, kP = kW / 2;
   const BlockNormGradArgs& a = job.a;
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   float4* acc_post = reinterpret_cast<float4*>(ring + static_cast<size_t>(stages) * slots * row_bytes);
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(full + s, 1);
-    late = 0;
+    late[0] = late[1] = 0;
     mbar_init_fence();
   }
   for (int i = t; i < 2 * 8 * kRedStride; i += blockDim.x) red[0][i] = 0.0f;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
     for (int row = r0; row < r1; ++row, ++count) {
       const int64_t off = static_cast<int64_t>(row) * row_bytes;
       const uint8_t* src = ring + s * slots * row_bytes;
-      if (!mbar_wait_bounded(full + s, phase)) late = 1;
+      if (!mbar_wait_bounded(full + s, phase)) late[count & 1] = 1;
       RawCols<F32> x, h{}, dy{}, dh{}, g;
       float r[8] = {};
       if (on) {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
         r[3] = s3.x + s3.y, r[4] = s4.x + s4.y, r[5] = s5.x + s5.y;
       }
       row_sums8(r, red[count & 1]);
-      if (late) {
+      if (late[count & 1]) {  // set before this row's barrier only, so all read the same
         stop = true;
         break;
       }

@@ -20,20 +20,20 @@ namespace {
 constexpr int kM = 128;          // features of a tile
 constexpr int kStageK = 256;     // elements of k a stage: 128 bytes of codes a row
 constexpr int kThreads = 192;    // warps 0-3: result; 4: copies; 5: products
+constexpr int kMostParts = 8;    // of k, in one cluster
 constexpr int kErrCuda = 2;      // FC_ERR_CUDA
 
 template <int BN>
 struct Tile {
-  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : 5;
-  static constexpr int kSfbTiles = BN > 128 ? 2 : 1;  // 128-row scale tiles of the tokens
+  static constexpr int kStages = BN >= 128 ? 3 : BN >= 32 ? 4 : 5;  // two CTAs an SM
   static constexpr int kABytes = kM * 128, kBBytes = BN * 128;
   static constexpr int kSfBytes = 1024;               // 128 rows, 256 elements of k
-  static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes * (1 + kSfbTiles);
+  static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
   static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
   // columns of the tensor core's memory: the accumulator, then each stage's scales
-  static constexpr int kSfCols = 8 * (1 + kSfbTiles);
+  static constexpr int kSfCols = 16;
   static constexpr int kColsUsed = BN + kStages * kSfCols;
-  static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+  static constexpr int kCols = kColsUsed <= 128 ? 128 : 256;
 };
 
 struct Job {
@@ -92,6 +92,31 @@ __device__ __forceinline__ void tc_load16(uint32_t tmem, uint32_t v[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp.  The tcgen05 and TMA instructions are issued
+// under this predicate and not under `lane == 0`: the compiler knows it to be
+// uniform, and their operands then need no loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// Barrier of some whole warps of the CTA; the second form gives all of them the
+// same answer to whether any passed true.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_any(int id, int threads, bool mine) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
+               : "memory");
+  return r != 0;
+}
+
 // Shared-memory matrix descriptors: rows of 128 bytes with the 128-byte
 // swizzle, 1024 bytes from one group of eight rows to the next; and rows of 16
 // bytes without a swizzle, 128 bytes from group to group.
@@ -108,11 +133,44 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf) {
          (static_cast<uint32_t>(kM >> 4) << 24) | (sf << 29);
 }
 
+__device__ __forceinline__ void store_out(const Job& j, int64_t t, int f, float v) {
+  if (j.out_f32)
+    static_cast<float*>(j.out)[t * j.features + f] = v;
+  else
+    static_cast<__nv_bfloat16*>(j.out)[t * j.features + f] = __float2bfloat16_rn(v);
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+
+// ------------------------------------------------ few tokens: k in parts --
+// With few tokens the weights' bytes count and there are fewer tiles than SMs:
+// the CTAs of a cluster take the parts of k of one tile, leave their sums in
+// their shared memory, and each adds up a slice of the features over the parts,
+// in order (no atomics: the same bits every time).
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
 template <int BN>
@@ -124,16 +182,20 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* sa = base;                                    // [stage][128 rows][128 bytes]
   uint8_t* sb = sa + T::kStages * T::kABytes;            // [stage][BN rows][128 bytes]
   uint8_t* ssa = sb + T::kStages * T::kBBytes;           // [stage][1024]
-  uint8_t* ssb = ssa + T::kStages * T::kSfBytes;         // [stage][tiles][1024]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ssb + T::kStages * T::kSfBytes * T::kSfbTiles);
+  uint8_t* ssb = ssa + T::kStages * T::kSfBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ssb + T::kStages * T::kSfBytes);
   uint64_t* empty = full + T::kStages;
   uint64_t* done = empty + T::kStages;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
   volatile uint32_t* failed = tmem_at + 1;
+  float* part = reinterpret_cast<float*>(base);          // [BN][128] sums, when the stages are done with
+  static_assert(BN * kM * 4 <= T::kStages * T::kStageBytes, "the sums fit where the stages were");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kM;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * BN;
+  const int parts = gridDim.z, part_id = blockIdx.z;     // a cluster is the parts of a tile
   const int stages_k = (j.H + kStageK - 1) / kStageK;
+  const int i0 = stages_k * part_id / parts, i1 = stages_k * (part_id + 1) / parts;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
@@ -143,6 +205,11 @@ __global__ void __launch_bounds__(kThreads)
   }
   // taken before the next kernel may start, so that all of this grid's CTAs have theirs
   if (warp == 5) tmem_alloc(tmem_at, T::kCols);
+  if (warp == 4 && elect_one())
+    for (int i = i0; i < i1 && i < i0 + T::kStages; ++i) {
+      tma_prefetch_2d(&map_w, i * 128, n0);
+      prefetch_l2(j.w_scales + (static_cast<int64_t>(blockIdx.x) * j.KT + 2 * i) * 512, j.KT - 2 * i >= 2 ? 1024 : 512);
+    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -150,37 +217,36 @@ __global__ void __launch_bounds__(kThreads)
   pdl_begin();
 
   if (warp == 4) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < stages_k; ++i) {
-        const int s = i % T::kStages, n = i / T::kStages;
-        if (n > 0 && !mbar_wait_bounded(empty + s, (n - 1) & 1)) {
+    if (elect_one()) {
+      int s = 0, used = 0;
+      uint32_t phase = 1;  // a first pass over the stages waits for nothing
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_bounded(empty + s, phase)) {
           *failed = 1;
           break;
         }
-        // the last stage may hold one scale tile of k, not two
-        const uint32_t sf = j.KT - 2 * i >= 2 ? 1024u : 512u;
-        int sfb_tiles = 1;
-        if (T::kSfbTiles == 2 && t0 + 128 < j.rows) sfb_tiles = 2;
-        mbar_expect_tx(full + s, T::kABytes + T::kBBytes + sf * (1 + sfb_tiles));
+        const uint32_t sf = j.KT - 2 * i >= 2 ? 1024u : 512u;  // the last stage may hold one scale tile of k
+        mbar_expect_tx(full + s, T::kABytes + T::kBBytes + 2 * sf);
         tma_load_2d(sa + s * T::kABytes, &map_w, i * 128, n0, full + s);
+        bulk_load(ssa + s * T::kSfBytes, j.w_scales + (static_cast<int64_t>(blockIdx.x) * j.KT + 2 * i) * 512, sf,
+                  full + s);
         tma_load_2d(sb + s * T::kBBytes, &map_x, i * 128, static_cast<int>(t0), full + s);
-        bulk_load(ssa + s * T::kSfBytes, j.w_scales + (static_cast<int64_t>(blockIdx.x) * j.KT + 2 * i) * 512,
-                  sf, full + s);
-        for (int q = 0; q < sfb_tiles; ++q)
-          bulk_load(ssb + (s * T::kSfbTiles + q) * T::kSfBytes,
-                    j.x_scales + ((t0 / 128 + q) * j.KT + 2 * i) * 512, sf, full + s);
+        bulk_load(ssb + s * T::kSfBytes, j.x_scales + (t0 / 128 * j.KT + 2 * i) * 512, sf, full + s);
+        used = min(used + 1, T::kStages);
+        if (++s == T::kStages) s = 0, phase ^= 1;
       }
-      // after a failure: the copies in flight land before the CTA ends
-      if (i < stages_k)
-        for (int q = max(0, i - T::kStages); q < i; ++q)
-          mbar_wait_bounded(full + q % T::kStages, (q / T::kStages) & 1);
+      if (*failed)  // the copies in flight land before the CTA ends
+        for (int q = 0; q < used; ++q) {
+          if (--s < 0) s = T::kStages - 1, phase ^= 1;
+          mbar_wait_bounded(full + s, phase ^ 1);
+        }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      for (int i = 0; i < stages_k; ++i) {
-        const int s = i % T::kStages, n = i / T::kStages;
-        if (!mbar_wait_bounded(full + s, n & 1)) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 0;
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_bounded(full + s, phase)) {
           *failed = 1;
           break;
         }
@@ -189,19 +255,18 @@ __global__ void __launch_bounds__(kThreads)
         const int halves = j.KT - 2 * i >= 2 ? 2 : 1;  // scale tiles of k in this stage
         for (int q = 0; q < halves; ++q) {
           tc_copy_scales(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
-          for (int r = 0; r < T::kSfbTiles; ++r)  // columns: [half of k][token tile]
-            tc_copy_scales(sf + 8 + 4 * (q * T::kSfbTiles + r),
-                           desc_scales(smem_u32(ssb + (s * T::kSfbTiles + r) * T::kSfBytes + q * 512)));
+          tc_copy_scales(sf + 8 + 4 * q, desc_scales(smem_u32(ssb + s * T::kSfBytes + q * 512)));
         }
         const uint64_t da = desc_codes(smem_u32(sa + s * T::kABytes));
         const uint64_t db = desc_codes(smem_u32(sb + s * T::kBBytes));
         const int steps = min(4, (j.H - i * kStageK + 63) / 64);
-        for (int k = 0; k < steps; ++k) {  // 64 elements: 32 bytes further along the row
-          const int q = k >> 1;
-          tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(BN, (k & 1) * 2), sf + 4 * q,
-                      sf + 8 + 4 * q * T::kSfbTiles, i > 0 || k > 0);
-        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 64 elements: 32 bytes further along the row
+          if (k < steps)
+            tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(BN, (k & 1) * 2), sf + 4 * (k >> 1),
+                        sf + 8 + 4 * (k >> 1), i > i0 || k > 0);
         tc_commit(empty + s);
+        if (++s == T::kStages) s = 0, phase ^= 1;
       }
       tc_commit(done);
     }
@@ -209,29 +274,274 @@ __global__ void __launch_bounds__(kThreads)
     if (!mbar_wait_bounded(done, 0)) *failed = 1;
     tc_fence_after();
     __syncwarp();
-    if (!*failed) {
-      const int64_t f = n0 + warp * 32 + lane;
-      for (int c = 0; c < BN && t0 + c < j.rows; c += 16) {
-        uint32_t v[16];
-        tc_load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
-        if (f < j.features) {
+    const int f = warp * 32 + lane;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int c = 0; c < tokens; c += 16) {
+      uint32_t v[16];
+      tc_load16(mine + c, v);
+      if (parts > 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int64_t t = t0 + c + i;
-            if (t >= j.rows) break;
-            if (j.out_f32)
-              static_cast<float*>(j.out)[t * j.features + f] = __uint_as_float(v[i]);
-            else
-              static_cast<__nv_bfloat16*>(j.out)[t * j.features + f] = __float2bfloat16_rn(__uint_as_float(v[i]));
-          }
-        }
+        for (int i = 0; i < 16; ++i) part[(c + i) * kM + f] = __uint_as_float(v[i]);
+      } else if (n0 + f < j.features && !*failed) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < tokens) store_out(j, t0 + c + i, n0 + f, __uint_as_float(v[i]));
       }
     }
     tc_fence_before();
   }
-  __syncthreads();
+  __syncwarp();
+  if (parts > 1) {
+    cluster_sync_all();  // every part's sums are in its shared memory
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
+    const int shift = 5 - (31 - __clz(parts));  // log2 of the slice's groups of four features
+    if (!*failed)
+      for (int k = threadIdx.x; k < tokens << shift; k += kThreads) {
+        const int t = k >> shift, f = ((part_id << shift) + (k & ((1 << shift) - 1))) * 4;
+        const float* p = part + t * kM + f;
+        float4 v[kMostParts], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int r = 0; r < kMostParts; ++r)
+          if (r < parts) v[r] = ld_cluster(cluster_addr(p, r));
+#pragma unroll
+        for (int r = 0; r < kMostParts; ++r)
+          if (r < parts) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+        if (n0 + f < j.features) {  // a multiple of 16: all four or none
+          const int64_t at = (t0 + t) * j.features + n0 + f;
+          if (j.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = s;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.out) + at) =
+                make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
+        }
+      }
+    __syncwarp();
+    cluster_sync_all();  // no part's memory goes before the others have read it
+  } else {
+    __syncthreads();
+  }
   if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
   if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, T::kCols);
+  }
+}
+
+// ------------------------------------------------- many tokens: persistent --
+// One CTA an SM takes tile after tile (128 features by BN tokens).  Copies run
+// ahead into the next tile; the eight result warps take the accumulator into
+// registers (each 32 features by BN / 2 tokens) and hand it back, so that the
+// next tile's products start while they round, stage and store this one's:
+// 16 tokens at a time to shared memory, and from there by bulk tensor stores
+// (a lane's elements are a row of `out` apart).
+template <int BN>
+struct Wide {
+  static constexpr int kStages = BN == 256 ? 4 : 5;
+  static constexpr int kThreads = 320;  // warps 0-7: result; 8: copies; 9: products
+  static constexpr int kSfbTiles = BN / 128;
+  static constexpr int kABytes = kM * 128, kBBytes = BN * 128, kSfBytes = 1024;
+  static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes * (1 + kSfbTiles);
+  static constexpr int kOutBytes = 8192;  // of one half of the tokens: 16 tokens fp32, or 2 x 16 bf16
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024 + 256;
+  static constexpr int kSfCols = 8 * (1 + kSfbTiles);
+  static constexpr int kColsUsed = BN + kStages * kSfCols;
+  static constexpr int kCols = kColsUsed <= 256 ? 256 : 512;
+};
+
+template <int N>  // N * 32 neighbouring columns of this warp's 32 lanes
+__device__ __forceinline__ void tc_load_all(uint32_t tmem, uint32_t (&v)[N * 32]) {
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    uint32_t* r = v + b * 32;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(tmem + b * 32));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(y), "r"(smem_u32(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+template <int BN, bool OUT32>
+__global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
+    k_mx4_matmul_wide(const Job j, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_out) {
+  using T = Wide<BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sa = base;
+  uint8_t* sb = sa + T::kStages * T::kABytes;
+  uint8_t* ssa = sb + T::kStages * T::kBBytes;
+  uint8_t* ssb = ssa + T::kStages * T::kSfBytes;
+  uint8_t* so = ssb + T::kStages * T::kSfBytes * T::kSfbTiles;
+  uint64_t* full = reinterpret_cast<uint64_t*>(so + 2 * T::kOutBytes);
+  uint64_t* empty = full + T::kStages;
+  uint64_t* acc_full = empty + T::kStages;   // the accumulator holds a tile
+  uint64_t* acc_free = acc_full + 1;         // it is in the result warps' registers
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 1);
+  volatile uint32_t* failed = tmem_at + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages_k = (j.H + kStageK - 1) / kStageK;
+  const int tiles_n = static_cast<int>((j.features + kM - 1) / kM);
+  const int tiles = tiles_n * static_cast<int>((j.rows + BN - 1) / BN);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 8);
+    *failed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(tmem_at, T::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_begin();
+
+  if (warp == 8) {
+    if (elect_one()) {
+      int s = 0, used = 0;
+      uint32_t phase = 1;  // a first pass over the stages waits for nothing
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int nt = tile % tiles_n;
+        const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * BN;
+        const int sfb_tiles = T::kSfbTiles == 2 && t0 + 128 < j.rows ? 2 : 1;
+        const uint8_t* wsf = j.w_scales + static_cast<int64_t>(nt) * j.KT * 512;
+        const uint8_t* xsf = j.x_scales + t0 / 128 * j.KT * 512;
+        for (int i = 0; i < stages_k; ++i) {
+          if (!mbar_wait_bounded(empty + s, phase)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sf = j.KT - 2 * i >= 2 ? 1024u : 512u;  // the last stage may hold one scale tile of k
+          mbar_expect_tx(full + s, T::kABytes + T::kBBytes + sf * (1 + sfb_tiles));
+          tma_load_2d(sa + s * T::kABytes, &map_w, i * 128, nt * kM, full + s);
+          tma_load_2d(sb + s * T::kBBytes, &map_x, i * 128, static_cast<int>(t0), full + s);
+          bulk_load(ssa + s * T::kSfBytes, wsf + i * 1024, sf, full + s);
+          for (int q = 0; q < sfb_tiles; ++q)
+            bulk_load(ssb + (s * T::kSfbTiles + q) * T::kSfBytes,
+                      xsf + static_cast<int64_t>(q) * j.KT * 512 + i * 1024, sf, full + s);
+          used = min(used + 1, T::kStages);
+          if (++s == T::kStages) s = 0, phase ^= 1;
+        }
+      }
+      if (!ok) {  // the copies in flight land before the CTA ends
+        *failed = 1;
+        for (int q = 0; q < used; ++q) {
+          if (--s < 0) s = T::kStages - 1, phase ^= 1;
+          mbar_wait_bounded(full + s, phase ^ 1);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 0, acc_phase = 1;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        if (!mbar_wait_bounded(acc_free, acc_phase)) {
+          ok = false;
+          break;
+        }
+        acc_phase ^= 1;
+        for (int i = 0; i < stages_k; ++i) {
+          if (!mbar_wait_bounded(full + s, phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf = tmem + BN + s * T::kSfCols;
+          const int halves = j.KT - 2 * i >= 2 ? 2 : 1;
+          for (int q = 0; q < halves; ++q) {
+            tc_copy_scales(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
+            for (int r = 0; r < T::kSfbTiles; ++r)
+              tc_copy_scales(sf + 8 + 4 * (q * T::kSfbTiles + r),
+                             desc_scales(smem_u32(ssb + (s * T::kSfbTiles + r) * T::kSfBytes + q * 512)));
+          }
+          const uint64_t da = desc_codes(smem_u32(sa + s * T::kABytes));
+          const uint64_t db = desc_codes(smem_u32(sb + s * T::kBBytes));
+          const int steps = min(4, (j.H - i * kStageK + 63) / 64);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(BN, (k & 1) * 2), sf + 4 * (k >> 1),
+                          sf + 8 + 4 * (k >> 1) * T::kSfbTiles, i > 0 || k > 0);
+          tc_commit(empty + s);
+          if (++s == T::kStages) s = 0, phase ^= 1;
+        }
+        if (ok) tc_commit(acc_full);
+      }
+      if (!ok) {  // what was issued ends before the memory it uses is given back
+        *failed = 1;
+        tc_commit(acc_full);
+        mbar_wait_bounded(acc_full, 0);
+        mbar_wait_bounded(acc_full, 1);
+      }
+    }
+  } else {
+    constexpr int kCols = BN / 2, kBufs = OUT32 ? 1 : 2;
+    const int half = warp >> 2, f = (warp & 3) * 32 + lane;
+    const bool issuer = (threadIdx.x & 127) == 0;
+    uint8_t* buf0 = so + half * T::kOutBytes;
+    uint32_t phase = 0;
+    int turn = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      const bool there = mbar_wait_bounded(acc_full, phase);
+      phase ^= 1;
+      if (named_any(1 + half, 128, !there || *failed)) {
+        *failed = 1;
+        break;
+      }
+      tc_fence_after();
+      uint32_t v[kCols];
+      tc_load_all<kCols / 32>(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kCols, v);
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(acc_free);
+      const int n0 = tile % tiles_n * kM;
+      const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * BN + half * kCols;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        if (t0 + c >= j.rows) break;
+        uint8_t* buf = buf0 + (turn & (kBufs - 1)) * (T::kOutBytes / kBufs);
+        ++turn;
+        // the buffer's last store has read it
+        if (issuer) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBufs - 1) : "memory");
+        named_sync(1 + half, 128);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if constexpr (OUT32)
+            reinterpret_cast<uint32_t*>(buf)[i * kM + f] = v[c + i];
+          else
+            reinterpret_cast<__nv_bfloat16*>(buf)[i * kM + f] = __float2bfloat16_rn(__uint_as_float(v[c + i]));
+        }
+        fence_proxy_async_smem();
+        named_sync(1 + half, 128);
+        if (issuer) tma_store_2d(&map_out, n0, static_cast<int>(t0 + c), buf);
+      }
+    }
+    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
+  if (warp == 9) {
     __syncwarp();
     tc_fence_after();
     tmem_free(tmem, T::kCols);
@@ -271,15 +581,56 @@ cudaError_t codes_map(CUtensorMap* m, const void* codes, int64_t rows, int H, in
              : cudaErrorInvalidValue;
 }
 
+// out [rows, features] in boxes of 128 features by 16 tokens; what lies past the end is not written.
+cudaError_t out_map(CUtensorMap* m, const Mx4MatmulArgs& a) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.features), static_cast<cuuint64_t>(a.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.features) * (a.out_f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {kM, 16}, step[2] = {1, 1};
+  return fn(m, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides,
+            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int BN, bool OUT32>
+cudaError_t launch_wide(const Mx4MatmulArgs& a, const Job& j, cudaStream_t st) {
+  auto* kern = k_mx4_matmul_wide<BN, OUT32>;
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Wide<BN>::kSmem)) return e;
+  CUtensorMap mw, mx, mo;
+  if (cudaError_t e = codes_map(&mw, a.w_codes, a.features, a.H, kM)) return e;
+  if (cudaError_t e = codes_map(&mx, a.x_codes, a.rows, a.H, BN)) return e;
+  if (cudaError_t e = out_map(&mo, a)) return e;
+  const int64_t tiles = ((a.features + kM - 1) / kM) * ((a.rows + BN - 1) / BN);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()));
+  return launch_pdl(kern, grid, dim3(Wide<BN>::kThreads), Wide<BN>::kSmem, st, j, mw, mx, mo);
+}
+
 template <int BN>
-cudaError_t launch(const Mx4MatmulArgs& a, const Job& j, cudaStream_t st) {
+cudaError_t launch(const Mx4MatmulArgs& a, const Job& j, int parts, cudaStream_t st) {
   auto* kern = k_mx4_matmul<BN>;
   if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Tile<BN>::kSmem)) return e;
   CUtensorMap mw, mx;
   if (cudaError_t e = codes_map(&mw, a.w_codes, a.features, a.H, kM)) return e;
   if (cudaError_t e = codes_map(&mx, a.x_codes, a.rows, a.H, BN)) return e;
-  const dim3 grid(static_cast<unsigned>((a.features + kM - 1) / kM), static_cast<unsigned>((a.rows + BN - 1) / BN));
-  return launch_pdl(kern, grid, dim3(kThreads), Tile<BN>::kSmem, st, j, mw, mx);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = static_cast<unsigned>(parts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.features + kM - 1) / kM), static_cast<unsigned>((a.rows + BN - 1) / BN),
+                     static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Tile<BN>::kSmem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, j, mw, mx);
 }
 
 }  // namespace
@@ -287,11 +638,24 @@ cudaError_t launch(const Mx4MatmulArgs& a, const Job& j, cudaStream_t st) {
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, cudaStream_t st) {
   const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, a.H,
               static_cast<int>(mx4_tiles_k(a.H)), a.out_f32 ? 1 : 0};
-  if (a.rows <= 16) return launch<16>(a, j, st);
-  if (a.rows <= 32) return launch<32>(a, j, st);
-  if (a.rows <= 64) return launch<64>(a, j, st);
-  if (a.rows <= 128) return launch<128>(a, j, st);
-  return launch<256>(a, j, st);
+  // The kernel that cuts k holds two CTAs an SM.  Its parts: as many as keep all
+  // CTAs resident at once, at least four stages each (measured, us, 1 / 2 / 4 / 8
+  // parts: 1 token 8192 x 8192 12.6 / 9.8 / 8.3 / -, 64 tokens 4096 x 4096 8.8 / 7.0 /
+  // 5.4 / 7.6 at two stages a part).  Above 128 tokens, and where k is not cut, the
+  // persistent kernel's wider tile wins (512 tokens 8192 x 8192 17.5 against 20.9,
+  // 2048 tokens 4096 x 4096 17.5 against 26.9); with k cut it does not (512 tokens
+  // 2048 x 8192: 15.9 against 11.8).
+  const int64_t stages = (a.H + kStageK - 1) / kStageK;
+  const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : 128;
+  const int64_t tiles = ((a.features + kM - 1) / kM) * ((a.rows + bn - 1) / bn);
+  int parts = 1;
+  while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  if (a.rows > 128 && parts == 1)
+    return a.out_f32 ? launch_wide<256, true>(a, j, st) : launch_wide<256, false>(a, j, st);
+  if (bn == 16) return launch<16>(a, j, parts, st);
+  if (bn == 32) return launch<32>(a, j, parts, st);
+  if (bn == 64) return launch<64>(a, j, parts, st);
+  return launch<128>(a, j, parts, st);
 }
 
 }  // namespace fc
