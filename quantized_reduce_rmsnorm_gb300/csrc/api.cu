@@ -177,6 +177,14 @@ fc_status check_dtype(int32_t dtype, const char* name) {
   return FC_OK;
 }
 
+// Scale words of four blocks are counted in 32 bits (2^31 of them are 2^38 elements).
+fc_status check_mx4_size(int64_t rows, int64_t hidden) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (rows * ((hidden + 127) / 128) > INT32_MAX)
+    return fail(FC_ERR_UNSUPPORTED, "rows * ceil(hidden / 128) > 2^31 - 1 is not supported");
+  return FC_OK;
+}
+
 fc_status check_mx4(const fc_mx4& t, const char* name) {
   char buf[64];
   snprintf(buf, sizeof buf, "%s.codes", name);
@@ -567,7 +575,7 @@ size_t fc_mx4_scales_bytes(int64_t rows, int64_t hidden) {
 
 fc_status fc_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, fc_mx4 out,
                           fc_stream_t stream) {
-  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (fc_status s = check_mx4_size(rows, hidden)) return s;
   if (fc_status s = check_dtype(dtype, "dtype")) return s;
   if (rows == 0) return ok();
   if (fc_status s = check_ptr(x, 32, "x")) return s;
@@ -584,7 +592,7 @@ fc_status fc_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hi
 
 fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, int32_t out_dtype,
                             fc_stream_t stream) {
-  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
+  if (fc_status s = check_mx4_size(rows, hidden)) return s;
   if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
   if (rows == 0) return ok();
   if (fc_status s = check_mx4(in, "in")) return s;

@@ -8,9 +8,8 @@
 // the residual stream.  Everything else is binary32.
 //
 // Bound by memory: x and r in, h and y out.  One CTA holds one row in
-// registers (16 neighbouring elements a thread, so a warp's loads and stores
-// cover 1 KB), and each row is read once.  Rows of at most 512 elements take
-// one warp each.  The quantised y (mx4.cuh) leaves from the registers that
+// registers (32 neighbouring bytes a thread, so a warp's loads and stores
+// cover 1 KB), and each row is read once.  Rows that fit one warp take one each.  The quantised y (mx4.cuh) leaves from the registers that
 // hold it.
 #include "block.h"
 #include "mx4.cuh"
@@ -29,102 +28,97 @@ __device__ __forceinline__ float row_sum(float v, float* red, bool one_warp) {
   return warp_sum(l < n ? red[l] : 0.0f);
 }
 
-__device__ __forceinline__ float inv_rms_rn(float ss, int H, float eps) {
-  return __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(H)), eps));
-}
-
-// TEAM: one warp a row, blockDim.x / 32 rows a CTA; else one row a CTA.
-template <bool F32, bool TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_block_norm(const BlockNormArgs a) {
+// TEAM: one warp a row, four rows a CTA; else one row a CTA.  W: columns of a
+// thread, 32 bytes of them or (fp32 rows above 8192) 64.
+template <bool F32, int W, bool TEAM>
+__global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNormArgs a) {
   __shared__ float red[2][32];
   pdl_begin();
-  const int64_t row = TEAM ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const uint32_t row = TEAM ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
   const int t = TEAM ? threadIdx.x & 31 : threadIdx.x;
-  const int e = t * 16;
+  const int e = t * W;
   if (row >= a.rows) return;  // TEAM only: a whole warp
   const bool live = e < a.H;
-  const int64_t at = row * a.H + e;
-  Raw16<F32> xr, rr, gr, w1, w2;
+  const int64_t at = static_cast<int64_t>(row) * a.H + e;
+  const float inv_n = 1.0f / static_cast<float>(a.H);
+  Raw<F32, W> xr, rr, gr, w1, w2;
   if (live) {
-    xr = load_raw16<F32>(a.x, at);
-    if (a.res_in) rr = load_raw16<F32>(a.res_in, at);
-    if (a.gate) gr = load_weight16<F32>(a.gate, row / a.gate_seg * a.H + e);
-    if (a.post_w) w1 = load_weight16<F32>(a.post_w, e);
-    if (a.pre_w) w2 = load_weight16<F32>(a.pre_w, e);
+    xr = load_raw<F32, W>(a.x, at);
+    if (a.res_in) rr = load_raw<F32, W>(a.res_in, at);
+    if (a.gate)
+      gr = load_weight<F32, W>(a.gate, static_cast<int64_t>(row / static_cast<uint32_t>(a.gate_seg)) * a.H + e);
+    if (a.post_w) w1 = load_weight<F32, W>(a.post_w, e);
+    if (a.pre_w) w2 = load_weight<F32, W>(a.pre_w, e);
   }
-  float u[16] = {};
-  if (live) unpack_raw<F32>(xr, u);
+  const float2 zero = make_float2(0.0f, 0.0f);
+  float inv = 1.0f;
   if (a.post_w) {
-    float ss = 0.0f;
+    float2 ss = zero;
+    if (live)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = __fmaf_rn(u[i], u[i], ss);
-    const float inv = inv_rms_rn(row_sum(ss, red[0], TEAM), a.H, a.eps_post);
-    if (live) {
-      float w[16];
-      unpack_raw<F32>(w1, w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] = u[i] * inv * w[i];
-    }
+      for (int i = 0; i < W / 2; ++i) ss = pfma(pair<F32, W>(xr, i), pair<F32, W>(xr, i), ss);
+    inv = inv_sqrt(row_sum(ss.x + ss.y, red[0], TEAM) * inv_n + a.eps_post);
   }
-  Raw16<F32> hr;
+  Raw<F32, W> hr;
+  float2 ss = zero;
   if (live) {
-    float g[16], r[16];
-    if (a.gate) {
-      unpack_raw<F32>(gr, g);
+    float2 u[W / 2];
+    const float2 f = dup2(a.beta * inv);  // of x: the norm's factor and the block's scale
 #pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] *= g[i];
-    }
-    if (a.res_in) {
-      unpack_raw<F32>(rr, r);
+    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pair<F32, W>(xr, i), f);
+    if (a.post_w)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] = __fmaf_rn(a.beta, u[i], a.alpha * r[i]);
-    } else {
+      for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(w1, i));
+    if (a.gate)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] *= a.beta;
-    }
-    hr = pack_raw<F32>(u);
-    store_raw16<F32>(a.res_out, at, hr);
-    unpack_raw<F32>(hr, u);
+      for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(gr, i));
+    if (a.res_in)
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) u[i] = pfma(pair<F32, W>(rr, i), dup2(a.alpha), u[i]);
+    hr = pack_raw<F32, W>(u);
+    store_raw<F32, W>(a.res_out, at, hr);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) ss = pfma(pair<F32, W>(hr, i), pair<F32, W>(hr, i), ss);
   }
   if (!a.pre_w) return;
-  float ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) ss = __fmaf_rn(u[i], u[i], ss);
-  const float inv = inv_rms_rn(row_sum(ss, red[1], TEAM), a.H, a.eps_pre);
-  Raw16<F32> yr;
-  uint32_t m = 0;
+  inv = inv_sqrt(row_sum(ss.x + ss.y, red[1], TEAM) * inv_n + a.eps_pre);
+  Raw<F32, W> yr;
   if (live) {
-    float w[16];
-    unpack_raw<F32>(w2, w);
+    float2 u[W / 2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) u[i] = u[i] * inv * w[i];
-    yr = pack_raw<F32>(u);
-    if (a.y) store_raw16<F32>(a.y, at, yr);
-    unpack_raw<F32>(yr, u);  // what is quantised is y as it is stored
-    m = absmax_raw<F32>(yr);
+    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pmul(pair<F32, W>(hr, i), dup2(inv)), pair<F32, W>(w2, i));
+    yr = pack_raw<F32, W>(u);
+    if (a.y) store_raw<F32, W>(a.y, at, yr);
   }
-  if (a.y_codes) {
+  if (a.y_codes) {  // what is quantised is y as it is stored
+    float v[W] = {};
+    uint32_t m = 0;
+    if (live) {
+      m = absmax_raw<F32, W>(yr);
+      unpack_raw<F32, W>(yr, v);
+    }
     const int KT = static_cast<int>(mx4_tiles_k(a.H));
-    mx4_store16(u, m, live, (t & 7) == 0 && live, static_cast<uint8_t*>(a.y_codes) + at / 2,
-                a.y_scales + mx4_scale_word(row, min(t >> 3, KT - 1), KT));
+    mx4_store<W>(v, m, live, live && t % (128 / W) == 0, static_cast<uint8_t*>(a.y_codes) + at / 2,
+                 a.y_scales + mx4_scale_word(row, min(e / 128, KT - 1), KT));
   }
+}
+
+template <bool F32, int W>
+cudaError_t launch_rows(const BlockNormArgs& a, cudaStream_t st) {
+  return launch_pdl(k_block_norm<F32, W, false>, dim3(static_cast<unsigned>(a.rows)),
+                    dim3(static_cast<unsigned>((a.H / W + 31) / 32 * 32)), 0, st, a);
+}
+template <bool F32, int W>
+cudaError_t launch_teams(const BlockNormArgs& a, cudaStream_t st) {
+  return launch_pdl(k_block_norm<F32, W, true>, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(bool f32, const BlockNormArgs& a, cudaStream_t st) {
-  if (a.H <= 512) {
-    const dim3 grid(static_cast<unsigned>((a.rows + 3) / 4));
-    return f32 ? launch_pdl(k_block_norm<true, true, 128>, grid, dim3(128), 0, st, a)
-               : launch_pdl(k_block_norm<false, true, 128>, grid, dim3(128), 0, st, a);
-  }
-  const dim3 grid(static_cast<unsigned>(a.rows));
-  const dim3 block(static_cast<unsigned>((a.H / 16 + 31) / 32 * 32));
-  if (block.x <= 512)
-    return f32 ? launch_pdl(k_block_norm<true, false, 512>, grid, block, 0, st, a)
-               : launch_pdl(k_block_norm<false, false, 512>, grid, block, 0, st, a);
-  return f32 ? launch_pdl(k_block_norm<true, false, 1024>, grid, block, 0, st, a)
-             : launch_pdl(k_block_norm<false, false, 1024>, grid, block, 0, st, a);
+  if (!f32) return a.H <= 512 ? launch_teams<false, 16>(a, st) : launch_rows<false, 16>(a, st);
+  if (a.H <= 256) return launch_teams<true, 8>(a, st);
+  return a.H <= 8192 ? launch_rows<true, 8>(a, st) : launch_rows<true, 16>(a, st);
 }
 
 }  // namespace fc

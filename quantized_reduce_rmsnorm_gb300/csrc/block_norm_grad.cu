@@ -58,6 +58,14 @@ __device__ __forceinline__ void acc_take(float4* acc, float v[16]) {
   }
 }
 
+template <bool F32>
+__device__ __forceinline__ void store16(void* base, int64_t elem, const float v[16]) {
+  float2 p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = make_float2(v[2 * i], v[2 * i + 1]);
+  store_raw<F32, 16>(base, elem, pack_raw<F32, 16>(p));
+}
+
 // How the rows are cut: `segs` runs of seg_rows rows that share a gate row,
 // each into `cuts` pieces; piece i of the segs * cuts is CTA i, i + grid, ...
 struct GradPlan {
@@ -97,11 +105,11 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
   const float inv_n = 1.0f / static_cast<float>(a.H);
   float w1[16], w2[16];
   {
-    Raw16<F32> r{};
-    if (live && a.post_w) r = load_weight16<F32>(a.post_w, e);
-    unpack_raw<F32>(r, w1);
-    if (live && a.pre_w) r = load_weight16<F32>(a.pre_w, e);
-    unpack_raw<F32>(r, w2);
+    Raw<F32, 16> r{};
+    if (live && a.post_w) r = load_weight<F32, 16>(a.post_w, e);
+    unpack_raw<F32, 16>(r, w1);
+    if (live && a.pre_w) r = load_weight<F32, 16>(a.pre_w, e);
+    unpack_raw<F32, 16>(r, w2);
   }
   for (int64_t piece = blockIdx.x; piece < p.segs * p.cuts; piece += gridDim.x) {
     const int64_t seg = piece / p.cuts, cut = piece - seg * p.cuts;
@@ -111,14 +119,14 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
       const int64_t at = row * a.H + e;
       float x[16] = {}, h[16] = {}, dy[16] = {}, dh[16] = {}, g[16];
       if (live) {
-        unpack_raw<F32>(load_raw16<F32>(a.x, at), x);
+        unpack_raw<F32, 16>(load_raw<F32, 16>(a.x, at), x);
         if (a.dy) {
-          unpack_raw<F32>(load_raw16<F32>(a.h, at), h);
-          unpack_raw<F32>(load_raw16<F32>(a.dy, at), dy);
+          unpack_raw<F32, 16>(load_raw<F32, 16>(a.h, at), h);
+          unpack_raw<F32, 16>(load_raw<F32, 16>(a.dy, at), dy);
         }
-        if (a.dh) unpack_raw<F32>(load_raw16<F32>(a.dh, at), dh);
+        if (a.dh) unpack_raw<F32, 16>(load_raw<F32, 16>(a.dh, at), dh);
         if (a.gate)
-          unpack_raw<F32>(load_weight16<F32>(a.gate, (p.gate_direct ? row : seg) * a.H + e), g);
+          unpack_raw<F32, 16>(load_weight<F32, 16>(a.gate, (p.gate_direct ? row : seg) * a.H + e), g);
       }
       float s[3] = {0, 0, 0};
 #pragma unroll
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
         float t[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) t[i] = a.alpha * dh[i];
-        store_raw16<F32>(a.dres, at, pack_raw<F32>(t));
+        store16<F32>(a.dres, at, t);
       }
       const float inv_x = a.post_w ? __frsqrt_rn(__fadd_rn(s[2] * inv_n, a.eps_post)) : 1.0f;
 #pragma unroll
@@ -158,7 +166,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) t[i] = dh[i] * (a.post_w ? x[i] * w1[i] : x[i]);
         if (g_sum) acc_add(acc_gate, t);
-        if (live && a.dgate && p.gate_direct) store_raw16<F32>(a.dgate, at, pack_raw<F32>(t));
+        if (live && a.dgate && p.gate_direct) store16<F32>(a.dgate, at, t);
 #pragma unroll
         for (int i = 0; i < 16; ++i) dh[i] = live ? dh[i] * g[i] : 0.0f;  // now du
       }
@@ -174,27 +182,27 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dh[i] = inv_x * __fmaf_rn(dh[i], w1[i], -(x[i] * c));
       }
-      if (live) store_raw16<F32>(a.dx, at, pack_raw<F32>(dh));
+      if (live) store16<F32>(a.dx, at, dh);
     }
     if (g_sum) {
       float t[16];
       acc_take(acc_gate, t);
       if (live) {
         if (p.gate_final)
-          store_raw16<F32>(a.dgate, seg * a.H + e, pack_raw<F32>(t));
+          store16<F32>(a.dgate, seg * a.H + e, t);
         else
-          store_raw16<true>(job.ws_gate, piece * a.H + e, pack_raw<true>(t));
+          store16<true>(job.ws_gate, piece * a.H + e, t);
       }
     }
   }
   float t[16];
   if (w_pre) {
     acc_take(acc_pre, t);
-    if (live) store_raw16<true>(job.ws_pre, static_cast<int64_t>(blockIdx.x) * a.H + e, pack_raw<true>(t));
+    if (live) store16<true>(job.ws_pre, static_cast<int64_t>(blockIdx.x) * a.H + e, t);
   }
   if (w_post) {
     acc_take(acc_post, t);
-    if (live) store_raw16<true>(job.ws_post, static_cast<int64_t>(blockIdx.x) * a.H + e, pack_raw<true>(t));
+    if (live) store16<true>(job.ws_post, static_cast<int64_t>(blockIdx.x) * a.H + e, t);
   }
 }
 
@@ -298,16 +306,6 @@ __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
   s += __shfl_xor_sync(kFull, s, 1);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kFull, s, i * 4);
-}
-
-// 1 / sqrt(v): the hardware's approximation (relative error about 2^-22) and one
-// step of Newton's method, which squares the error; what is left is its
-// rounding, below 2^-22.  v > 0 and finite, or 0 (infinity, as of 1 / sqrt(0)).
-__device__ __forceinline__ float inv_sqrt(float v) {
-  const float y = rsqrtf(v);
-  const float e = __fmaf_rn(-v * y, y, 1.0f);  // 1 - v y^2
-  const float r = __fmaf_rn(0.5f * y, e, y);
-  return v > 0.0f ? r : y;
 }
 
 constexpr int kMostStages = 4;

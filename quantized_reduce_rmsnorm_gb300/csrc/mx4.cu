@@ -12,84 +12,98 @@ namespace fc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWords = kThreads / 8;  // scale words of a CTA's turn
+constexpr int kTurns = 2;             // turns whose loads are in flight together
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads)
-    k_mx4_quantize(const void* x, int64_t words, int H, int KT, uint8_t* codes, uint8_t* scales) {
+    k_mx4_quantize(const void* x, uint32_t words, int H, uint32_t KT, uint8_t* codes, uint8_t* scales) {
   pdl_begin();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 8);
-  // a warp's four words are handled together: every lane makes as many turns
   const int sub = threadIdx.x & 7;
-  for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 8) + (threadIdx.x >> 5) * 4;
-       w0 < words; w0 += step) {
-    const int64_t w = w0 + ((threadIdx.x >> 3) & 3);
-    const bool word = w < words;
-    const int64_t row = word ? w / KT : 0;
-    const int kt = static_cast<int>(w - row * KT);
+  Raw<F32, 16> r[kTurns];
+  int64_t at[kTurns], sw[kTurns];
+  bool live[kTurns], word[kTurns];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const uint32_t w = (blockIdx.x * kTurns + i) * kWords + (threadIdx.x >> 3);
+    const uint32_t row = w / KT, kt = w - row * KT;
     const int e = kt * 128 + sub * 16;
-    const bool live = word && e < H;
-    const int64_t at = row * H + e;
+    word[i] = w < words;
+    live[i] = word[i] && e < H;
+    at[i] = static_cast<int64_t>(row) * H + e;
+    sw[i] = mx4_scale_word(row, kt, KT);
+    if (live[i]) r[i] = load_raw<F32, 16>(x, at[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
     float v[16] = {};
     uint32_t m = 0;
-    if (live) {
-      const Raw16<F32> r = load_raw16<F32>(x, at);
-      m = absmax_raw<F32>(r);
-      unpack_raw<F32>(r, v);
+    if (live[i]) {
+      m = absmax_raw<F32, 16>(r[i]);
+      unpack_raw<F32, 16>(r[i], v);
     }
-    mx4_store16(v, m, live, word && sub == 0, codes + at / 2,
-                scales + (word ? mx4_scale_word(row, kt, KT) : 0));
+    mx4_store<16>(v, m, live[i], word[i] && sub == 0, codes + at[i] / 2, scales + sw[i]);
   }
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads)
-    k_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t words, int H, int KT,
-                     void* out) {
+    k_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, uint32_t words, int H, uint32_t KT, void* out) {
   pdl_begin();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 8);
   const int sub = threadIdx.x & 7;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 8) + (threadIdx.x >> 3);
-       w < words; w += step) {
-    const int64_t row = w / KT;
-    const int kt = static_cast<int>(w - row * KT);
+  uint2 c[kTurns];
+  uint32_t byte[kTurns];
+  int64_t at[kTurns];
+  bool live[kTurns];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const uint32_t w = (blockIdx.x * kTurns + i) * kWords + (threadIdx.x >> 3);
+    const uint32_t row = w / KT, kt = w - row * KT;
     const int e = kt * 128 + sub * 16;
-    if (e >= H) continue;
-    const int64_t at = row * H + e;
-    const uint2 c = ld64_stream(codes + at / 2);
-    const float s = mx4_scale(scales[mx4_scale_word(row, kt, KT) + (sub >> 1)]);
+    live[i] = w < words && e < H;
+    at[i] = static_cast<int64_t>(row) * H + e;
+    if (live[i]) {
+      c[i] = ld64_stream(codes + at[i] / 2);
+      byte[i] = scales[mx4_scale_word(row, kt, KT) + (sub >> 1)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    if (!live[i]) continue;
+    const float s = mx4_scale(byte[i]);
     float v[16];
-    mx4_decode8(c.x, s, v);
-    mx4_decode8(c.y, s, v + 8);
-    store_raw16<F32>(out, at, pack_raw<F32>(v));
+    mx4_decode8(c[i].x, s, v);
+    mx4_decode8(c[i].y, s, v + 8);
+    float2 p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = make_float2(v[2 * k], v[2 * k + 1]);
+    store_raw<F32, 16>(out, at[i], pack_raw<F32, 16>(p));
   }
 }
 
-unsigned grid_for(int64_t words) {
-  const int64_t want = (words + kThreads / 8 - 1) / (kThreads / 8);
-  return static_cast<unsigned>(want < (1 << 30) ? want : (1 << 30));
-}
+dim3 grid_for(int64_t words) { return dim3(static_cast<unsigned>((words + kWords * kTurns - 1) / (kWords * kTurns))); }
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(bool f32, const void* x, int64_t rows, int H, void* codes,
                                 uint8_t* scales, cudaStream_t st) {
-  const int KT = static_cast<int>(mx4_tiles_k(H));
-  const int64_t words = rows * KT;
+  const uint32_t KT = static_cast<uint32_t>(mx4_tiles_k(H));
+  const uint32_t words = static_cast<uint32_t>(rows * KT);  // below 2^31: the caller's check
   auto* c = static_cast<uint8_t*>(codes);
-  return f32 ? launch_pdl(k_mx4_quantize<true>, dim3(grid_for(words)), dim3(kThreads), 0, st, x, words, H,
+  return f32 ? launch_pdl(k_mx4_quantize<true>, grid_for(words), dim3(kThreads), 0, st, x, words, H,
                           KT, c, scales)
-             : launch_pdl(k_mx4_quantize<false>, dim3(grid_for(words)), dim3(kThreads), 0, st, x, words, H,
+             : launch_pdl(k_mx4_quantize<false>, grid_for(words), dim3(kThreads), 0, st, x, words, H,
                           KT, c, scales);
 }
 
 cudaError_t launch_mx4_dequantize(bool f32, const void* codes, const uint8_t* scales, int64_t rows,
                                   int H, void* out, cudaStream_t st) {
-  const int KT = static_cast<int>(mx4_tiles_k(H));
-  const int64_t words = rows * KT;
+  const uint32_t KT = static_cast<uint32_t>(mx4_tiles_k(H));
+  const uint32_t words = static_cast<uint32_t>(rows * KT);  // below 2^31: the caller's check
   auto* c = static_cast<const uint8_t*>(codes);
-  return f32 ? launch_pdl(k_mx4_dequantize<true>, dim3(grid_for(words)), dim3(kThreads), 0, st, c, scales,
+  return f32 ? launch_pdl(k_mx4_dequantize<true>, grid_for(words), dim3(kThreads), 0, st, c, scales,
                           words, H, KT, out)
-             : launch_pdl(k_mx4_dequantize<false>, dim3(grid_for(words)), dim3(kThreads), 0, st, c, scales,
+             : launch_pdl(k_mx4_dequantize<false>, grid_for(words), dim3(kThreads), 0, st, c, scales,
                           words, H, KT, out);
 }
 

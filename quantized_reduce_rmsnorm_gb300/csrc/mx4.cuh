@@ -28,21 +28,8 @@ __device__ __forceinline__ int64_t mx4_scale_word(int64_t r, int64_t kt, int64_t
   return ((r >> 7) * KT + kt) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
-// Largest |v| of 16 floats as bits: as unsigned numbers the bit patterns of
-// non-negative floats order as the floats do, infinity and NaN above all.
-__device__ __forceinline__ uint32_t absmax_bits16(const float v[16]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
-}
-// The same of 16 packed bf16, without unpacking them.
-__device__ __forceinline__ uint32_t absmax_bits16(const V8& v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v.w[i] & 0x7FFF7FFFu);
-  return max(m << 16, m & 0xFFFF0000u);
-}
+// The largest |v| of a block is found on bits: as unsigned numbers the bit patterns
+// of non-negative floats order as the floats do, infinity and NaN above all.
 
 // e8m0 byte of a block whose largest |v| has these bits.
 __device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax_bits) {
@@ -92,87 +79,115 @@ __device__ __forceinline__ void mx4_decode8(uint32_t w, float scale, float* v) {
   }
 }
 
-// One warp's share of a quantisation: every lane holds 16 elements, eight
-// neighbouring lanes one scale word's 128 (`live`: the lane's elements are
-// inside the row).  Writes the lane's 8 bytes of codes and, by the first of
-// the eight, the word of four scale bytes (0 past the row's end).  amax_bits
-// is that of the lane's 16 elements, 0 for a lane that is not live.
-__device__ __forceinline__ void mx4_store16(const float v[16], uint32_t amax_bits, bool live,
-                                            bool word, uint8_t* codes, uint8_t* scales) {
-  const uint32_t m = max(amax_bits, __shfl_xor_sync(kFull, amax_bits, 1));
+// One warp's share of a quantisation: every lane holds W (8 or 16) elements, 32 / W
+// neighbouring lanes a block, 128 / W of them one scale word (`live`: the lane's
+// elements are inside the row).  Writes the lane's codes and, by the lane with
+// `word` (the first of the word's), the word of four scale bytes (0 past the row's
+// end).  amax_bits is that of the lane's elements, 0 for a lane that is not live.
+template <int W>
+__device__ __forceinline__ void mx4_store(const float* v, uint32_t amax_bits, bool live, bool word, uint8_t* codes,
+                                          uint8_t* scales) {
+  uint32_t m = max(amax_bits, __shfl_xor_sync(kFull, amax_bits, 1));
+  if constexpr (W == 8) m = max(m, __shfl_xor_sync(kFull, m, 2));
   const uint32_t byte = live ? mx4_scale_byte(m) : 0u;
   if (live) {
     const float inv = mx4_inv_scale(byte);
-    uint2 c;
-    c.x = mx4_encode8(v, inv);
-    c.y = mx4_encode8(v + 8, inv);
-    *reinterpret_cast<uint2*>(codes) = c;
+    if constexpr (W == 8) {
+      *reinterpret_cast<uint32_t*>(codes) = mx4_encode8(v, inv);
+    } else {
+      uint2 c;
+      c.x = mx4_encode8(v, inv);
+      c.y = mx4_encode8(v + 8, inv);
+      *reinterpret_cast<uint2*>(codes) = c;
+    }
   }
-  uint32_t w = byte | (__shfl_down_sync(kFull, byte, 2) << 8);
-  w |= __shfl_down_sync(kFull, w, 4) << 16;
+  constexpr int kBlock = 32 / W;  // lanes
+  uint32_t w = byte | (__shfl_down_sync(kFull, byte, kBlock) << 8);
+  w |= __shfl_down_sync(kFull, w, 2 * kBlock) << 16;
   if (word) *reinterpret_cast<uint32_t*>(scales) = w;
 }
 
+// 1 / sqrt(v): the hardware's approximation (relative error about 2^-22) and one
+// step of Newton's method, which squares the error; what is left is its
+// rounding, below 2^-22.  0, infinity and NaN give what the approximation does.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float y = rsqrtf(v);
+  const float e = __fmaf_rn(-v * y, y, 1.0f);  // 1 - v y^2
+  const float r = __fmaf_rn(0.5f * y, e, y);
+  return v > 0.0f && v < __uint_as_float(0x7F800000u) ? r : y;
+}
+
 // ------------------------------------------------ rows of bf16 or fp32 --
-// 16 neighbouring elements of a row tensor (coherent loads: an output may be
-// the input's own memory).
-template <bool F32>
-struct Raw16 {
-  V8 v[F32 ? 2 : 1];
+// W neighbouring elements of a row tensor in 256-bit pieces (coherent loads: an
+// output may be the input's own memory).
+template <bool F32, int W>
+struct Raw {
+  static constexpr int kPieces = W * (F32 ? 4 : 2) / 32;
+  V8 v[kPieces];
 };
-template <bool F32>
-__device__ __forceinline__ Raw16<F32> load_raw16(const void* base, int64_t elem) {
-  Raw16<F32> r;
+template <bool F32, int W>
+__device__ __forceinline__ Raw<F32, W> load_raw(const void* base, int64_t elem) {
+  Raw<F32, W> r;
   const char* p = static_cast<const char*>(base) + elem * (F32 ? 4 : 2);
-  r.v[0] = ld256_coherent(p);
-  if constexpr (F32) r.v[1] = ld256_coherent(p + 32);
+#pragma unroll
+  for (int i = 0; i < r.kPieces; ++i) r.v[i] = ld256_coherent(p + 32 * i);
   return r;
 }
 // Weights and gates, which every row re-reads.
-template <bool F32>
-__device__ __forceinline__ Raw16<F32> load_weight16(const void* base, int64_t elem) {
-  Raw16<F32> r;
+template <bool F32, int W>
+__device__ __forceinline__ Raw<F32, W> load_weight(const void* base, int64_t elem) {
+  Raw<F32, W> r;
   const char* p = static_cast<const char*>(base) + elem * (F32 ? 4 : 2);
-  r.v[0] = ld256_keep(p);
-  if constexpr (F32) r.v[1] = ld256_keep(p + 32);
+#pragma unroll
+  for (int i = 0; i < r.kPieces; ++i) r.v[i] = ld256_keep(p + 32 * i);
   return r;
 }
-template <bool F32>
-__device__ __forceinline__ void unpack_raw(const Raw16<F32>& r, float f[16]) {
-  if constexpr (F32) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r.v[i / 8].w[i % 8]);
-  } else {
-    unpack16(r.v[0], f);
-  }
+// Elements 2i and 2i + 1.
+template <bool F32, int W>
+__device__ __forceinline__ float2 pair(const Raw<F32, W>& r, int i) {
+  if constexpr (F32)
+    return make_float2(__uint_as_float(r.v[i / 4].w[2 * i % 8]), __uint_as_float(r.v[i / 4].w[2 * i % 8 + 1]));
+  else
+    return make_float2(bf_lo(r.v[i / 8].w[i % 8]), bf_hi(r.v[i / 8].w[i % 8]));
 }
-// Rounds 16 floats to the row type (bf16: to nearest even; fp32: as they are).
-template <bool F32>
-__device__ __forceinline__ Raw16<F32> pack_raw(const float f[16]) {
-  Raw16<F32> r;
-  if constexpr (F32) {
+// Rounds W floats to the row type (bf16: to nearest even; fp32: as they are).
+template <bool F32, int W>
+__device__ __forceinline__ Raw<F32, W> pack_raw(const float2* f) {
+  Raw<F32, W> r;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r.v[i / 8].w[i % 8] = __float_as_uint(f[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[0].w[i] = pack_bf2(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < W / 2; ++i) {
+    if constexpr (F32) {
+      r.v[i / 4].w[2 * i % 8] = __float_as_uint(f[i].x);
+      r.v[i / 4].w[2 * i % 8 + 1] = __float_as_uint(f[i].y);
+    } else {
+      r.v[i / 8].w[i % 8] = pack_bf2(f[i].x, f[i].y);
+    }
   }
   return r;
 }
-template <bool F32>
-__device__ __forceinline__ void store_raw16(void* base, int64_t elem, const Raw16<F32>& r) {
+template <bool F32, int W>
+__device__ __forceinline__ void store_raw(void* base, int64_t elem, const Raw<F32, W>& r) {
   char* p = static_cast<char*>(base) + elem * (F32 ? 4 : 2);
-  st256(p, r.v[0]);
-  if constexpr (F32) st256(p + 32, r.v[1]);
+#pragma unroll
+  for (int i = 0; i < r.kPieces; ++i) st256(p + 32 * i, r.v[i]);
 }
-template <bool F32>
-__device__ __forceinline__ uint32_t absmax_raw(const Raw16<F32>& r) {
-  if constexpr (F32) {
-    float f[16];
-    unpack_raw<true>(r, f);
-    return absmax_bits16(f);
-  } else {
-    return absmax_bits16(r.v[0]);
+// Largest |element| as bits: bf16 without unpacking.
+template <bool F32, int W>
+__device__ __forceinline__ uint32_t absmax_raw(const Raw<F32, W>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < r.kPieces; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      m = F32 ? max(m, r.v[i].w[k] & 0x7FFFFFFFu) : __vmaxu2(m, r.v[i].w[k] & 0x7FFF7FFFu);
+  return F32 ? m : max(m << 16, m & 0xFFFF0000u);
+}
+template <bool F32, int W>
+__device__ __forceinline__ void unpack_raw(const Raw<F32, W>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    const float2 p = pair<F32, W>(r, i);
+    f[2 * i] = p.x, f[2 * i + 1] = p.y;
   }
 }
 
