@@ -30,8 +30,8 @@ __device__ __forceinline__ float row_sum(float v, float* red, bool one_warp) {
 
 // TEAM: one warp a row, four rows a CTA; else one row a CTA.  W: columns of a
 // thread, 32 bytes of them or (fp32 rows above 8192) 64.
-template <bool F32, int W, bool TEAM>
-__global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNormArgs a) {
+template <bool F32, int W, bool TEAM, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const BlockNormArgs a) {
   __shared__ float red[2][32];
   pdl_begin();
   const uint32_t row = TEAM ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
@@ -41,14 +41,12 @@ __global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNor
   const bool live = e < a.H;
   const int64_t at = static_cast<int64_t>(row) * a.H + e;
   const float inv_n = 1.0f / static_cast<float>(a.H);
-  Raw<F32, W> xr, rr, gr, w1, w2;
+  Raw<F32, W> xr, rr, gr;
   if (live) {
     xr = load_raw<F32, W>(a.x, at);
     if (a.res_in) rr = load_raw<F32, W>(a.res_in, at);
     if (a.gate)
       gr = load_weight<F32, W>(a.gate, static_cast<int64_t>(row / static_cast<uint32_t>(a.gate_seg)) * a.H + e);
-    if (a.post_w) w1 = load_weight<F32, W>(a.post_w, e);
-    if (a.pre_w) w2 = load_weight<F32, W>(a.pre_w, e);
   }
   const float2 zero = make_float2(0.0f, 0.0f);
   float inv = 1.0f;
@@ -66,9 +64,11 @@ __global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNor
     const float2 f = dup2(a.beta * inv);  // of x: the norm's factor and the block's scale
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) u[i] = pmul(pair<F32, W>(xr, i), f);
-    if (a.post_w)
+    if (a.post_w) {
+      const Raw<F32, W> w = load_weight<F32, W>(a.post_w, e);
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(w1, i));
+      for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(w, i));
+    }
     if (a.gate)
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(gr, i));
@@ -84,9 +84,10 @@ __global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNor
   inv = inv_sqrt(row_sum(ss.x + ss.y, red[1], TEAM) * inv_n + a.eps_pre);
   Raw<F32, W> yr;
   if (live) {
+    const Raw<F32, W> w = load_weight<F32, W>(a.pre_w, e);
     float2 u[W / 2];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pmul(pair<F32, W>(hr, i), dup2(inv)), pair<F32, W>(w2, i));
+    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pmul(pair<F32, W>(hr, i), dup2(inv)), pair<F32, W>(w, i));
     yr = pack_raw<F32, W>(u);
     if (a.y) store_raw<F32, W>(a.y, at, yr);
   }
@@ -103,22 +104,32 @@ __global__ void __launch_bounds__(TEAM ? 128 : 1024) k_block_norm(const BlockNor
   }
 }
 
-template <bool F32, int W>
+template <bool F32, int W, int MAXT, int MINB>
 cudaError_t launch_rows(const BlockNormArgs& a, cudaStream_t st) {
-  return launch_pdl(k_block_norm<F32, W, false>, dim3(static_cast<unsigned>(a.rows)),
+  return launch_pdl(k_block_norm<F32, W, false, MAXT, MINB>, dim3(static_cast<unsigned>(a.rows)),
                     dim3(static_cast<unsigned>((a.H / W + 31) / 32 * 32)), 0, st, a);
 }
 template <bool F32, int W>
 cudaError_t launch_teams(const BlockNormArgs& a, cudaStream_t st) {
-  return launch_pdl(k_block_norm<F32, W, true>, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st, a);
+  return launch_pdl(k_block_norm<F32, W, true, 128, 1>, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st,
+                    a);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(bool f32, const BlockNormArgs& a, cudaStream_t st) {
-  if (!f32) return a.H <= 512 ? launch_teams<false, 16>(a, st) : launch_rows<false, 16>(a, st);
+  // Registers for three CTAs of 512 threads an SM spill a little: worth it where
+  // rows come in waves (8192 x 8192: 88.2 us, with two 93.4), not for a few (64 x
+  // 8192: 3.6 us against 3.1).  fp32 rows: two CTAs of 640 threads (1037 x 5120:
+  // 16.6 us, with one 22.0, with three 21.0).
+  if (!f32) {
+    if (a.H <= 512) return launch_teams<false, 16>(a, st);
+    if (a.H > 8192) return launch_rows<false, 16, 1024, 1>(a, st);
+    return a.rows > 4 * num_sms() ? launch_rows<false, 16, 512, 3>(a, st) : launch_rows<false, 16, 512, 2>(a, st);
+  }
   if (a.H <= 256) return launch_teams<true, 8>(a, st);
-  return a.H <= 8192 ? launch_rows<true, 8>(a, st) : launch_rows<true, 16>(a, st);
+  if (a.H <= 5120) return launch_rows<true, 8, 640, 2>(a, st);
+  return a.H <= 8192 ? launch_rows<true, 8, 1024, 1>(a, st) : launch_rows<true, 16, 1024, 1>(a, st);
 }
 
 }  // namespace fc

@@ -101,22 +101,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Barrier of some whole warps of the CTA; the second form gives all of them the
-// same answer to whether any passed true.
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  __syncwarp();
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ bool named_any(int id, int threads, bool mine) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-               : "=r"(r)
-               : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
-               : "memory");
-  return r != 0;
-}
-
 // Shared-memory matrix descriptors: rows of 128 bytes with the 128-byte
 // swizzle, 1024 bytes from one group of eight rows to the next; and rows of 16
 // bytes without a swizzle, 128 bytes from group to group.
@@ -333,9 +317,9 @@ __global__ void __launch_bounds__(kThreads)
 // One CTA an SM takes tile after tile (128 features by BN tokens).  Copies run
 // ahead into the next tile; the eight result warps take the accumulator into
 // registers (each 32 features by BN / 2 tokens) and hand it back, so that the
-// next tile's products start while they round, stage and store this one's:
-// 16 tokens at a time to shared memory, and from there by bulk tensor stores
-// (a lane's elements are a row of `out` apart).
+// next tile's products start while they round, stage and store this one's, each
+// warp by itself: 16 tokens at a time to shared memory, and from there by bulk
+// tensor stores (a lane's elements are a row of `out` apart).
 template <int BN>
 struct Wide {
   static constexpr int kStages = BN == 256 ? 4 : 5;
@@ -343,8 +327,8 @@ struct Wide {
   static constexpr int kSfbTiles = BN / 128;
   static constexpr int kABytes = kM * 128, kBBytes = BN * 128, kSfBytes = 1024;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes * (1 + kSfbTiles);
-  static constexpr int kOutBytes = 8192;  // of one half of the tokens: 16 tokens fp32, or 2 x 16 bf16
-  static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024 + 256;
+  static constexpr int kOutBytes = 2048;  // of a result warp: 32 features by 16 tokens fp32, or 2 x 16 bf16
+  static constexpr int kSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
   static constexpr int kSfCols = 8 * (1 + kSfbTiles);
   static constexpr int kColsUsed = BN + kStages * kSfCols;
   static constexpr int kCols = kColsUsed <= 256 ? 256 : 512;
@@ -365,6 +349,33 @@ __device__ __forceinline__ void tc_load_all(uint32_t tmem, uint32_t (&v)[N * 32]
         : "r"(tmem + b * 32));
   }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// N * 64 neighbouring columns of 16 lanes (0 or 16 on from tmem's), as fragments of
+// 16 lanes by 8 columns: thread l has lane l / 4, columns 2 (l % 4) and the next, in
+// the first two of a fragment's four registers, and lane l / 4 + 8 in the others.
+template <int N>
+__device__ __forceinline__ void tc_load_fragments(uint32_t tmem, uint32_t (&v)[N * 32]) {
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    uint32_t* r = v + b * 32;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+        "[%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(tmem + b * 64));
+  }
+}
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: thread l's
+// register m holds row l / 4, columns 2 (l % 4) and the next of matrix m; `row` is
+// where column l % 8 of matrix l / 8 goes.
+__device__ __forceinline__ void store_transposed(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -389,7 +400,7 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
   uint8_t* ssa = sb + T::kStages * T::kBBytes;
   uint8_t* ssb = ssa + T::kStages * T::kSfBytes;
   uint8_t* so = ssb + T::kStages * T::kSfBytes * T::kSfbTiles;
-  uint64_t* full = reinterpret_cast<uint64_t*>(so + 2 * T::kOutBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(so + 8 * T::kOutBytes);
   uint64_t* empty = full + T::kStages;
   uint64_t* acc_full = empty + T::kStages;   // the accumulator holds a tile
   uint64_t* acc_free = acc_full + 1;         // it is in the result warps' registers
@@ -497,46 +508,60 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
     }
   } else {
     constexpr int kCols = BN / 2, kBufs = OUT32 ? 1 : 2;
-    const int half = warp >> 2, f = (warp & 3) * 32 + lane;
-    const bool issuer = (threadIdx.x & 127) == 0;
-    uint8_t* buf0 = so + half * T::kOutBytes;
+    const int half = warp >> 2;
+    uint8_t* buf0 = so + warp * T::kOutBytes;
     uint32_t phase = 0;
     int turn = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const bool there = mbar_wait_bounded(acc_full, phase);
       phase ^= 1;
-      if (named_any(1 + half, 128, !there || *failed)) {
+      if (__any_sync(kFull, !there || *failed)) {
         *failed = 1;
         break;
       }
       tc_fence_after();
-      uint32_t v[kCols];
-      tc_load_all<kCols / 32>(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kCols, v);
+      const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kCols;
+      uint32_t v[OUT32 ? kCols : kCols / 2], u[kCols / 2];  // bf16: lanes 0-15 in v, 16-31 in u
+      if constexpr (OUT32) {
+        tc_load_all<kCols / 32>(mine, v);
+      } else {
+        tc_load_fragments<kCols / 64>(mine, v);
+        tc_load_fragments<kCols / 64>(mine + (16u << 16), u);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      }
       tc_fence_before();
       if (lane == 0) mbar_arrive(acc_free);
-      const int n0 = tile % tiles_n * kM;
+      const int n0 = tile % tiles_n * kM + (warp & 3) * 32;
       const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * BN + half * kCols;
+      if (n0 >= j.features) continue;
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         if (t0 + c >= j.rows) break;
         uint8_t* buf = buf0 + (turn & (kBufs - 1)) * (T::kOutBytes / kBufs);
         ++turn;
         // the buffer's last store has read it
-        if (issuer) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBufs - 1) : "memory");
-        named_sync(1 + half, 128);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBufs - 1) : "memory");
+        __syncwarp();
+        if constexpr (OUT32) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if constexpr (OUT32)
-            reinterpret_cast<uint32_t*>(buf)[i * kM + f] = v[c + i];
-          else
-            reinterpret_cast<__nv_bfloat16*>(buf)[i * kM + f] = __float2bfloat16_rn(__uint_as_float(v[c + i]));
+          for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(buf)[i * 32 + lane] = v[c + i];
+        } else {
+          // 16 tokens of 64 bytes, 16-byte groups in the order of the 64-byte swizzle
+          // (group g of row t at g ^ (t / 2 % 4)): eight rows' groups hit all banks once
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = h * 8 + (lane & 7), k = (c / 8 + h) * 4;
+            const uint32_t row = smem_u32(buf) + t * 64 + (((lane >> 3) ^ (t >> 1 & 3)) * 16);
+            auto pk = [](uint32_t lo, uint32_t hi) { return pack_bf2(__uint_as_float(lo), __uint_as_float(hi)); };
+            store_transposed(row, pk(v[k], v[k + 1]), pk(v[k + 2], v[k + 3]), pk(u[k], u[k + 1]), pk(u[k + 2], u[k + 3]));
+          }
         }
         fence_proxy_async_smem();
-        named_sync(1 + half, 128);
-        if (issuer) tma_store_2d(&map_out, n0, static_cast<int>(t0 + c), buf);
+        __syncwarp();
+        if (lane == 0) tma_store_2d(&map_out, n0, static_cast<int>(t0 + c), buf);
       }
     }
-    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   __syncthreads();
@@ -581,15 +606,17 @@ cudaError_t codes_map(CUtensorMap* m, const void* codes, int64_t rows, int H, in
              : cudaErrorInvalidValue;
 }
 
-// out [rows, features] in boxes of 128 features by 16 tokens; what lies past the end is not written.
+// out [rows, features] in boxes of 32 features by 16 tokens (bf16: 64-byte swizzle);
+// what lies past the end is not written.
 cudaError_t out_map(CUtensorMap* m, const Mx4MatmulArgs& a) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.features), static_cast<cuuint64_t>(a.rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.features) * (a.out_f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {kM, 16}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {32, 16}, step[2] = {1, 1};
   return fn(m, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides,
-            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, a.out_f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;

@@ -166,6 +166,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
+    if stream.__class__ is int:
+        return stream
     if stream is None:  # the handle alone: a torch Stream object costs more than a launch
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
@@ -208,10 +210,13 @@ class Bound:
         self._args[self._ei] = ctypes.c_uint32(e & 0xFFFFFFFF)
 
     def __call__(self, stream=None):
-        if self._dev is not None and torch.cuda.current_device() != self._dev:
-            with torch.cuda.device(self._dev):
-                return self(stream)
         a = self._args
+        if self._dev is not None:
+            if torch._C._cuda_getDevice() != self._dev:
+                with torch.cuda.device(self._dev):
+                    return self(stream)
+            if stream is None:
+                stream = torch._C._cuda_getCurrentRawStream(self._dev)
         a[self._si] = _stream(stream)
         st = self._fn(*a)
         if st != FC_OK:
