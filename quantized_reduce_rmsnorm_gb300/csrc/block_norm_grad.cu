@@ -83,8 +83,8 @@ struct GradJob {
   float* ws_gate;     // [segs * cuts, H]
 };
 
-template <bool F32, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
+template <bool F32>
+__global__ void __launch_bounds__(1024) k_block_norm_grad(const GradJob job) {
   extern __shared__ float4 acc[];
   // a row's three sums and one more, each its own floats; neighbouring rows take
   // turns, so a row's first barrier frees what the row before it read
@@ -218,60 +218,59 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_grad(const GradJob job) {
 // that barrier.  With r = sum over rows of inv_x * dh' * x (one column), dgate =
 // beta * post_weight * r and, for a gate that the piece's rows share,
 // dpost_weight = beta * gate * r: one running sum serves both.  It and
-// dpre_weight's are in registers.  A thread has eight columns, in groups of 16
+// dpre_weight's are in registers.  A thread has W columns, in groups of 16
 // bytes, the live threads side by side: no bank conflicts.
-constexpr int kW = 8;  // columns of a thread
-
-template <bool F32>
+template <bool F32, int W>
 struct Cols {
   static constexpr int kPer = F32 ? 4 : 8;  // columns of a group
-  static constexpr int kGroups = kW / kPer;
+  static constexpr int kGroups = W / kPer;
   // first column of group j of thread t, `live` threads in all
   static __device__ __forceinline__ int at(int j, int t, int live) { return (j * live + t) * kPer; }
 };
 
-template <bool F32>
+template <bool F32, int W>
 struct RawCols {
-  uint4 g[Cols<F32>::kGroups];
+  uint4 g[Cols<F32, W>::kGroups];
 };
 // The thread's columns of a row (or of a weight), from shared or global memory.
-template <bool F32>
-__device__ __forceinline__ RawCols<F32> load_cols(const void* row, int t, int live) {
+template <bool F32, int W>
+__device__ __forceinline__ RawCols<F32, W> load_cols(const void* row, int t, int live) {
   constexpr int es = F32 ? 4 : 2;
-  RawCols<F32> r;
+  RawCols<F32, W> r;
 #pragma unroll
-  for (int j = 0; j < Cols<F32>::kGroups; ++j)
-    r.g[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + Cols<F32>::at(j, t, live) * es);
+  for (int j = 0; j < Cols<F32, W>::kGroups; ++j)
+    r.g[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + Cols<F32, W>::at(j, t, live) * es);
   return r;
 }
 // Columns 2i and 2i + 1 of them.
-template <bool F32>
-__device__ __forceinline__ float2 pair(const RawCols<F32>& r, int i) {
+template <bool F32, int W>
+__device__ __forceinline__ float2 pair(const RawCols<F32, W>& r, int i) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(r.g);
   if constexpr (F32) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   return make_float2(bf_lo(w[i]), bf_hi(w[i]));
 }
-template <bool F32>
-__device__ __forceinline__ void store_cols(void* row, int t, int live, const float2 f[kW / 2]) {
-  constexpr int es = F32 ? 4 : 2;
+template <bool F32, int W>
+__device__ __forceinline__ void store_cols(void* row, int t, int live, const float2 f[W / 2]) {
+  constexpr int es = F32 ? 4 : 2, kPairs = Cols<F32, W>::kPer / 2;
 #pragma unroll
-  for (int j = 0; j < Cols<F32>::kGroups; ++j) {
+  for (int j = 0; j < Cols<F32, W>::kGroups; ++j) {
+    const float2* v = f + j * kPairs;
     uint4 w;
     if constexpr (F32)
-      w = make_uint4(__float_as_uint(f[2 * j].x), __float_as_uint(f[2 * j].y), __float_as_uint(f[2 * j + 1].x),
-                     __float_as_uint(f[2 * j + 1].y));
+      w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
     else
-      w = make_uint4(pack_bf2(f[0].x, f[0].y), pack_bf2(f[1].x, f[1].y), pack_bf2(f[2].x, f[2].y),
-                     pack_bf2(f[3].x, f[3].y));
-    st128(static_cast<char*>(row) + Cols<F32>::at(j, t, live) * es, w);
+      w = make_uint4(pack_bf2(v[0].x, v[0].y), pack_bf2(v[1].x, v[1].y), pack_bf2(v[2].x, v[2].y),
+                     pack_bf2(v[3].x, v[3].y));
+    st128(static_cast<char*>(row) + Cols<F32, W>::at(j, t, live) * es, w);
   }
 }
 // The same columns of a row of fp32 sums.
-template <bool F32>
-__device__ __forceinline__ void store_sums(float* row, int t, int live, const float2 f[kW / 2]) {
+template <bool F32, int W>
+__device__ __forceinline__ void store_sums(float* row, int t, int live, const float2 f[W / 2]) {
+  constexpr int kPer = Cols<F32, W>::kPer;
 #pragma unroll
-  for (int k = 0; k < kW / 4; ++k) {
-    const int at = F32 ? Cols<F32>::at(k, t, live) : Cols<F32>::at(0, t, live) + 4 * k;
+  for (int k = 0; k < W / 4; ++k) {  // four columns at a time
+    const int at = Cols<F32, W>::at(4 * k / kPer, t, live) + 4 * k % kPer;
     *reinterpret_cast<float4*>(row + at) = make_float4(f[2 * k].x, f[2 * k].y, f[2 * k + 1].x, f[2 * k + 1].y);
   }
 }
@@ -311,17 +310,17 @@ __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
 constexpr int kMostStages = 4;
 
 // TOKEN: a gate row for every row, staged with the row.
-template <bool F32, bool TOKEN, int MAXT, int MINB>
+template <bool F32, bool TOKEN, int W, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const GradJob job, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float red[2][8 * kRedStride];  // neighbouring rows take turns
   __shared__ uint64_t full[kMostStages];
   __shared__ volatile int late[2];  // a copy did not land in time, by turns as red
   __shared__ struct { int piece, row, end, count; } next;
-  constexpr int es = F32 ? 4 : 2, kP = kW / 2;
+  constexpr int es = F32 ? 4 : 2, kP = W / 2;
   const BlockNormGradArgs& a = job.a;
   const GradPlan& p = job.p;
-  const int t = threadIdx.x, live = a.H / kW;
+  const int t = threadIdx.x, live = a.H / W;
   const int H = a.H, row_bytes = H * es;
   const bool on = t < live;
   const bool pre = a.dy != nullptr, post = a.post_w != nullptr;
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
     mbar_init_fence();
   }
   for (int i = t; i < 2 * 8 * kRedStride; i += blockDim.x) red[0][i] = 0.0f;
-  for (int j = 0; j < kW / 4; ++j) acc_post[j * blockDim.x + t] = make_float4(0, 0, 0, 0);
+  for (int j = 0; j < W / 4; ++j) acc_post[j * blockDim.x + t] = make_float4(0, 0, 0, 0);
   __syncthreads();
   pdl_begin();
 
@@ -375,8 +374,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   const float inv_n = 1.0f / static_cast<float>(H);
   const float2 zero = make_float2(0.0f, 0.0f);
   float2 gw[kP], acc_pre[kP], acc_r[kP];
-  RawCols<F32> w2{};
-  if (on && a.pre_w) w2 = load_cols<F32>(a.pre_w, t, live);
+  RawCols<F32, W> w2{};
+  if (on && a.pre_w) w2 = load_cols<F32, W>(a.pre_w, t, live);
 #pragma unroll
   for (int i = 0; i < kP; ++i) acc_pre[i] = acc_r[i] = zero;
   int count = 0, s = 0;  // rows done; the row's stage
@@ -389,37 +388,37 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
 #pragma unroll
     for (int i = 0; i < kP; ++i) gw[i] = dup2(a.beta);
     if (on && post) {
-      const RawCols<F32> w = load_cols<F32>(a.post_w, t, live);
+      const RawCols<F32, W> w = load_cols<F32, W>(a.post_w, t, live);
 #pragma unroll
-      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32>(w, i));
+      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32, W>(w, i));
     }
     if (on && !TOKEN && a.gate) {
-      const RawCols<F32> w = load_cols<F32>(static_cast<const char*>(a.gate) + seg_off, t, live);
+      const RawCols<F32, W> w = load_cols<F32, W>(static_cast<const char*>(a.gate) + seg_off, t, live);
 #pragma unroll
-      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32>(w, i));
+      for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32, W>(w, i));
     }
     for (int row = r0; row < r1; ++row, ++count) {
       const int64_t off = static_cast<int64_t>(row) * row_bytes;
       const uint8_t* src = ring + s * slots * row_bytes;
       if (!mbar_wait_bounded(full + s, phase)) late[count & 1] = 1;
-      RawCols<F32> x, h{}, dy{}, dh{}, g;
+      RawCols<F32, W> x, h{}, dy{}, dh{}, g;
       float r[8] = {};
       if (on) {
-        x = load_cols<F32>(src, t, live);
-        if (pre) h = load_cols<F32>(src + slot_h * row_bytes, t, live);
-        if (pre) dy = load_cols<F32>(src + slot_dy * row_bytes, t, live);
-        if (a.dh) dh = load_cols<F32>(src + slot_dh * row_bytes, t, live);
-        if (TOKEN) g = load_cols<F32>(src + slot_g * row_bytes, t, live);
+        x = load_cols<F32, W>(src, t, live);
+        if (pre) h = load_cols<F32, W>(src + slot_h * row_bytes, t, live);
+        if (pre) dy = load_cols<F32, W>(src + slot_dy * row_bytes, t, live);
+        if (a.dh) dh = load_cols<F32, W>(src + slot_dh * row_bytes, t, live);
+        if (TOKEN) g = load_cols<F32, W>(src + slot_g * row_bytes, t, live);
         float2 s0 = zero, s1 = zero, s2 = zero, s3 = zero, s4 = zero, s5 = zero;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-          const float2 xi = pair<F32>(x, i), hi = pair<F32>(h, i), ai = pmul(pair<F32>(dy, i), pair<F32>(w2, i));
+          const float2 xi = pair<F32, W>(x, i), hi = pair<F32, W>(h, i), ai = pmul(pair<F32, W>(dy, i), pair<F32, W>(w2, i));
           float2 gx = pmul(gw[i], xi);
-          if (TOKEN) gx = pmul(gx, pair<F32>(g, i));
+          if (TOKEN) gx = pmul(gx, pair<F32, W>(g, i));
           s0 = pfma(hi, hi, s0);
           s1 = pfma(ai, hi, s1);
           s2 = pfma(xi, xi, s2);
-          s3 = pfma(gx, pair<F32>(dh, i), s3);
+          s3 = pfma(gx, pair<F32, W>(dh, i), s3);
           s4 = pfma(gx, ai, s4);
           s5 = pfma(gx, hi, s5);
         }
@@ -442,33 +441,33 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       float2 d[kP], o[kP];
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
-        const float2 hi = pair<F32>(h, i), e = pmul(pair<F32>(dy, i), vi);
+        const float2 hi = pair<F32, W>(h, i), e = pmul(pair<F32, W>(dy, i), vi);
         acc_pre[i] = pfma(e, hi, acc_pre[i]);
-        d[i] = padd(pair<F32>(dh, i), pfma(e, pair<F32>(w2, i), pmul(vk, hi)));
+        d[i] = padd(pair<F32, W>(dh, i), pfma(e, pair<F32, W>(w2, i), pmul(vk, hi)));
       }
       if (a.dres) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) o[i] = pmul(d[i], dup2(a.alpha));
-        store_cols<F32>(static_cast<char*>(a.dres) + off, t, live, o);
+        store_cols<F32, W>(static_cast<char*>(a.dres) + off, t, live, o);
       }
       if (TOKEN) {
         // dgate row = beta * post_weight * dh' * xh; what remains is as without a gate
         if (a.dgate) {
 #pragma unroll
-          for (int i = 0; i < kP; ++i) o[i] = pmul(pmul(gw[i], vx), pmul(d[i], pair<F32>(x, i)));
-          store_cols<F32>(static_cast<char*>(a.dgate) + off, t, live, o);
+          for (int i = 0; i < kP; ++i) o[i] = pmul(pmul(gw[i], vx), pmul(d[i], pair<F32, W>(x, i)));
+          store_cols<F32, W>(static_cast<char*>(a.dgate) + off, t, live, o);
         }
 #pragma unroll
-        for (int i = 0; i < kP; ++i) d[i] = pmul(d[i], pair<F32>(g, i));
+        for (int i = 0; i < kP; ++i) d[i] = pmul(d[i], pair<F32, W>(g, i));
       }
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
-        const float2 xi = pair<F32>(x, i);
+        const float2 xi = pair<F32, W>(x, i);
         acc_r[i] = pfma(pmul(d[i], xi), vx, acc_r[i]);
         o[i] = pmul(pmul(d[i], gw[i]), vx);
         if (post) o[i] = pfma(xi, vc, o[i]);
       }
-      store_cols<F32>(static_cast<char*>(a.dx) + off, t, live, o);
+      store_cols<F32, W>(static_cast<char*>(a.dx) + off, t, live, o);
     }
     if (on && !stop) {
       float2 o[kP];
@@ -476,25 +475,25 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
 #pragma unroll
         for (int i = 0; i < kP; ++i) o[i] = pmul(acc_r[i], dup2(a.beta));
         if (post) {
-          const RawCols<F32> w = load_cols<F32>(a.post_w, t, live);
+          const RawCols<F32, W> w = load_cols<F32, W>(a.post_w, t, live);
 #pragma unroll
-          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32>(w, i));
+          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32, W>(w, i));
         }
         if (p.gate_final)
-          store_cols<F32>(static_cast<char*>(a.dgate) + seg_off, t, live, o);
+          store_cols<F32, W>(static_cast<char*>(a.dgate) + seg_off, t, live, o);
         else
-          store_sums<F32>(job.ws_gate + static_cast<int64_t>(piece) * H, t, live, o);
+          store_sums<F32, W>(job.ws_gate + static_cast<int64_t>(piece) * H, t, live, o);
       }
       if (a.dpost_w) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) o[i] = pmul(acc_r[i], dup2(a.beta));
         if (!TOKEN && a.gate) {
-          const RawCols<F32> w = load_cols<F32>(static_cast<const char*>(a.gate) + seg_off, t, live);
+          const RawCols<F32, W> w = load_cols<F32, W>(static_cast<const char*>(a.gate) + seg_off, t, live);
 #pragma unroll
-          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32>(w, i));
+          for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32, W>(w, i));
         }
 #pragma unroll
-        for (int j = 0; j < kW / 4; ++j) {
+        for (int j = 0; j < W / 4; ++j) {
           float4 x = acc_post[j * blockDim.x + t];
           x.x += o[2 * j].x, x.y += o[2 * j].y, x.z += o[2 * j + 1].x, x.w += o[2 * j + 1].y;
           acc_post[j * blockDim.x + t] = x;
@@ -505,15 +504,15 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
     }
   }
   if (on && !stop) {
-    if (a.dpre_w) store_sums<F32>(job.ws_pre + static_cast<int64_t>(blockIdx.x) * H, t, live, acc_pre);
+    if (a.dpre_w) store_sums<F32, W>(job.ws_pre + static_cast<int64_t>(blockIdx.x) * H, t, live, acc_pre);
     if (a.dpost_w) {
       float2 o[kP];
 #pragma unroll
-      for (int j = 0; j < kW / 4; ++j) {
+      for (int j = 0; j < W / 4; ++j) {
         const float4 x = acc_post[j * blockDim.x + t];
         o[2 * j] = make_float2(x.x, x.y), o[2 * j + 1] = make_float2(x.z, x.w);
       }
-      store_sums<F32>(job.ws_post + static_cast<int64_t>(blockIdx.x) * H, t, live, o);
+      store_sums<F32, W>(job.ws_post + static_cast<int64_t>(blockIdx.x) * H, t, live, o);
     }
   }
   if (stop && t == 0) {  // a copy never landed: say so, and let those in flight land
@@ -583,9 +582,9 @@ int64_t resident(K* kern, int threads, int smem) {
   return std::min<int64_t>(kNormGradMaxCtas, static_cast<int64_t>(num_sms()) * occ);
 }
 
-template <bool F32, int MAXT>
+template <bool F32>
 cudaError_t launch_direct(GradJob& job, int threads, cudaStream_t st) {
-  auto* kern = k_block_norm_grad<F32, MAXT>;
+  auto* kern = k_block_norm_grad<F32>;
   const int smem = threads * 12 * static_cast<int>(sizeof(float4));
   const int64_t most = resident(kern, threads, smem);
   if (most < 1) return cudaErrorInvalidConfiguration;
@@ -593,9 +592,9 @@ cudaError_t launch_direct(GradJob& job, int threads, cudaStream_t st) {
   return launch_pdl(kern, dim3(job.p.grid), dim3(threads), smem, st, job);
 }
 
-template <bool F32, bool TOKEN, int MAXT, int MINB>
+template <bool F32, bool TOKEN, int W, int MAXT, int MINB>
 cudaError_t launch_staged(GradJob& job, int threads, int stages, int smem, cudaStream_t st) {
-  auto* kern = k_block_norm_grad_staged<F32, TOKEN, MAXT, MINB>;
+  auto* kern = k_block_norm_grad_staged<F32, TOKEN, W, MAXT, MINB>;
   const int64_t most = resident(kern, threads, smem);
   if (most < 1) return cudaErrorInvalidConfiguration;
   plan(job, most);
@@ -606,22 +605,38 @@ template <bool F32, bool TOKEN>
 cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
   const BlockNormGradArgs& a = job.a;
   const int slots = 1 + (a.dy ? 2 : 0) + (a.dh ? 1 : 0) + (TOKEN ? 1 : 0);
-  const int threads = (a.H / kW + 31) / 32 * 32;
-  const int stage = slots * a.H * (F32 ? 4 : 2), acc = threads * kW * 4;
   constexpr int kMost = 220 * 1024;
-  // two CTAs an SM where both have two stages, else one with as many as fit
-  int stages = std::min(kMostStages, (kMost / 2 - acc) / stage);
-  if (threads <= 256 && stages >= 2)
-    return launch_staged<F32, TOKEN, 256, 2>(job, threads, stages, stages * stage + acc, st);
-  if (threads <= 384 && stages >= 2)
-    return launch_staged<F32, TOKEN, 384, 2>(job, threads, stages, stages * stage + acc, st);
-  stages = std::min(kMostStages, (kMost - acc) / stage);
-  if (threads <= 640 && stages >= 1)
-    return launch_staged<F32, TOKEN, 640, 1>(job, threads, stages, stages * stage + acc, st);
-  if (threads <= 1024 && stages >= 1)
-    return launch_staged<F32, TOKEN, 1024, 1>(job, threads, stages, stages * stage + acc, st);
+  // W columns a thread; `ctas` CTAs share an SM's memory; the stages that fit
+  const int stage = slots * a.H * (F32 ? 4 : 2);
+  auto threads = [&](int W) { return (a.H / W + 31) / 32 * 32; };
+  auto stages = [&](int W, int ctas) { return std::min(kMostStages, (kMost / ctas - threads(W) * W * 4) / stage); };
+  auto smem = [&](int W, int n) { return n * stage + threads(W) * W * 4; };
+  // Two CTAs an SM where both have two stages, else one with as many as fit.  Eight
+  // columns a thread keep a row's warps many; 16 fit bf16 rows that would need
+  // more than 80 registers in two CTAs (8192 rows of 4096: 72.0 us, with eight 82.6;
+  // not for a few rows, 300: 12.8 against 10.7, and not with a gate row for every
+  // row, 96.4 against 92.2) or more than 64 in one (4096 rows of 8192: 70.2 us, with
+  // eight 100.5).  Rows that do not fit (fp32 above 8192) go straight to registers
+  // (bf16 rows of 16384 did: 1024 of them 119.6 us, staged 88.3).
+  if (const int n = stages(8, 2); n >= 2) {
+    if (threads(8) <= 256) return launch_staged<F32, TOKEN, 8, 256, 2>(job, threads(8), n, smem(8, n), st);
+    if (threads(8) <= 384) return launch_staged<F32, TOKEN, 8, 384, 2>(job, threads(8), n, smem(8, n), st);
+    if constexpr (!F32 && !TOKEN)
+      if (threads(16) <= 256 && a.rows > 8 * num_sms())
+        return launch_staged<F32, TOKEN, 16, 256, 2>(job, threads(16), n, smem(16, n), st);
+  }
+  if (const int n = stages(8, 1); n >= 1) {
+    if (threads(8) <= 640) return launch_staged<F32, TOKEN, 8, 640, 1>(job, threads(8), n, smem(8, n), st);
+    if constexpr (!F32) {
+      if (threads(16) <= 512) return launch_staged<F32, TOKEN, 16, 512, 1>(job, threads(16), n, smem(16, n), st);
+      if (const int m = stages(16, 1); m >= 1)
+        return launch_staged<F32, TOKEN, 16, 1024, 1>(job, threads(16), m, smem(16, m), st);
+    } else {
+      if (threads(8) <= 1024) return launch_staged<F32, TOKEN, 8, 1024, 1>(job, threads(8), n, smem(8, n), st);
+    }
+  }
   const int wide = (a.H / 16 + 31) / 32 * 32;  // 16 columns a thread
-  return wide <= 512 ? launch_direct<F32, 512>(job, wide, st) : launch_direct<F32, 1024>(job, wide, st);
+  return launch_direct<F32>(job, wide, st);
 }
 
 }  // namespace

@@ -11,6 +11,8 @@
 // memory and issues the products, four warps bring the result out.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "block.h"
 #include "mx4.cuh"
 
@@ -110,11 +112,11 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t smem) {
 __device__ __forceinline__ uint64_t desc_scales(uint32_t smem) {
   return static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
 }
-// Instruction descriptor: e2m1 by e2m1, both along k, e8m0 scales, N columns,
-// 128 rows; sf: which half (0 or 2) of a scale word's four bytes.
-__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf) {
+// Instruction descriptor: e2m1 by e2m1, both along k, e8m0 scales, M rows, N
+// columns; sf: which half (0 or 2) of a scale word's four bytes.
+__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(kM >> 4) << 24) | (sf << 29);
+         (static_cast<uint32_t>(M >> 4) << 24) | (sf << 29);
 }
 
 __device__ __forceinline__ void store_out(const Job& j, int64_t t, int f, float v) {
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 64 elements: 32 bytes further along the row
           if (k < steps)
-            tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(BN, (k & 1) * 2), sf + 4 * (k >> 1),
+            tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(kM, BN, (k & 1) * 2), sf + 4 * (k >> 1),
                         sf + 8 + 4 * (k >> 1), i > i0 || k > 0);
         tc_commit(empty + s);
         if (++s == T::kStages) s = 0, phase ^= 1;
@@ -314,25 +316,75 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------- many tokens: persistent --
-// One CTA an SM takes tile after tile (128 features by BN tokens).  Copies run
+// A pair of CTAs (two SMs) takes tile after tile of 256 features by 256 tokens: each
+// CTA stages 128 features and 128 tokens, and one thread of the first issues
+// products of both (cta_group::2), which read the tokens' codes from both CTAs'
+// shared memory and leave each CTA its 128 features by all 256 tokens.  A pair
+// loads a third less than two CTAs with tiles of their own, which is what
+// bounds a tile: 35 KB a stage and CTA (8192 x 8192 x 8192: 162 us, 6.77 PFLOP/s, against
+// 170; with four stages of the five 169).  Copies run
 // ahead into the next tile; the eight result warps take the accumulator into
-// registers (each 32 features by BN / 2 tokens) and hand it back, so that the
+// registers (each 32 features by 128 tokens) and hand it back, so that the
 // next tile's products start while they round, stage and store this one's, each
 // warp by itself: 16 tokens at a time to shared memory, and from there by bulk
-// tensor stores (a lane's elements are a row of `out` apart).
-template <int BN>
+// tensor stores.  bf16 leaves the tensor memory as 16 x 8 fragments, whose transposed
+// store makes rows of features (4096 tokens, 8192 features, 1024 elements: 20.4 us
+// against 23.1 with a store for each element).
+template <bool OUT32>
 struct Wide {
-  static constexpr int kStages = BN == 256 ? 4 : 5;
+  static constexpr int kTile = 256;     // features and tokens of a pair's tile
+  static constexpr int kHalf = 128;     // of one CTA
+  static constexpr int kStages = 5, kBufs = 2;  // of copies, of results
   static constexpr int kThreads = 320;  // warps 0-7: result; 8: copies; 9: products
-  static constexpr int kSfbTiles = BN / 128;
-  static constexpr int kABytes = kM * 128, kBBytes = BN * 128, kSfBytes = 1024;
-  static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes * (1 + kSfbTiles);
-  static constexpr int kOutBytes = 2048;  // of a result warp: 32 features by 16 tokens fp32, or 2 x 16 bf16
-  static constexpr int kSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
-  static constexpr int kSfCols = 8 * (1 + kSfbTiles);
-  static constexpr int kColsUsed = BN + kStages * kSfCols;
-  static constexpr int kCols = kColsUsed <= 256 ? 256 : 512;
+  static constexpr int kCodeBytes = kHalf * 128, kSfBytes = 1024;
+  static constexpr int kStageBytes = 2 * kCodeBytes + 3 * kSfBytes;
+  static constexpr int kOutBytes = OUT32 ? 2048 : 1024;  // of a result warp: 32 features by 16 tokens, kBufs times
+  static constexpr int kSmem = kStages * kStageBytes + 8 * kBufs * kOutBytes + 1024 + 256;
+  static constexpr int kSfCols = 24;    // [half of k] features; [half of k][128 tokens]
+  static constexpr int kCols = 512;     // the accumulator's 256, then each stage's scales
+  static_assert(kTile + kStages * kSfCols <= kCols && kSmem <= 227 * 1024, "fits");
 };
+
+// The same as above for a pair of CTAs.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* where, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t at, int cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+// Arrives on bar of both CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Each CTA's shared memory to its own tensor memory.
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                                 uint32_t sfb, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+// Into this CTA's shared memory, counted on a barrier of the pair (a cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
 template <int N>  // N * 32 neighbouring columns of this warp's 32 lanes
 __device__ __forceinline__ void tc_load_all(uint32_t tmem, uint32_t (&v)[N * 32]) {
@@ -378,9 +430,6 @@ __device__ __forceinline__ void store_transposed(uint32_t row, uint32_t a, uint3
                : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
                "r"(y), "r"(smem_u32(src))
@@ -388,39 +437,42 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-template <int BN, bool OUT32>
-__global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
+template <bool OUT32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThreads, 1)
     k_mx4_matmul_wide(const Job j, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_wsf, const __grid_constant__ CUtensorMap map_xsf,
                       const __grid_constant__ CUtensorMap map_out) {
-  using T = Wide<BN>;
+  using T = Wide<OUT32>;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sa = base;
-  uint8_t* sb = sa + T::kStages * T::kABytes;
-  uint8_t* ssa = sb + T::kStages * T::kBBytes;
-  uint8_t* ssb = ssa + T::kStages * T::kSfBytes;
-  uint8_t* so = ssb + T::kStages * T::kSfBytes * T::kSfbTiles;
-  uint64_t* full = reinterpret_cast<uint64_t*>(so + 8 * T::kOutBytes);
+  uint8_t* sa = base;                               // [stage] 128 features' codes
+  uint8_t* sb = sa + T::kStages * T::kCodeBytes;    // [stage] 128 tokens' codes
+  uint8_t* ssa = sb + T::kStages * T::kCodeBytes;   // [stage] this CTA's features' scales
+  uint8_t* ssb = ssa + T::kStages * T::kSfBytes;    // [stage][2] all 256 tokens' scales
+  uint8_t* so = ssb + 2 * T::kStages * T::kSfBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(so + 8 * T::kBufs * T::kOutBytes);  // the first CTA's: both CTAs' copies
   uint64_t* empty = full + T::kStages;
   uint64_t* acc_full = empty + T::kStages;   // the accumulator holds a tile
-  uint64_t* acc_free = acc_full + 1;         // it is in the result warps' registers
+  uint64_t* acc_free = acc_full + 1;         // the first CTA's: it is in both CTAs' result warps' registers
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 1);
   volatile uint32_t* failed = tmem_at + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1;
   const int stages_k = (j.H + kStageK - 1) / kStageK;
-  const int tiles_n = static_cast<int>((j.features + kM - 1) / kM);
-  const int tiles = tiles_n * static_cast<int>((j.rows + BN - 1) / BN);
+  const int tiles_n = static_cast<int>((j.features + T::kTile - 1) / T::kTile);
+  const int tiles = tiles_n * static_cast<int>((j.rows + T::kTile - 1) / T::kTile);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
     mbar_init(acc_full, 1);
-    mbar_init(acc_free, 8);
+    mbar_init(acc_free, 16);
     *failed = 0;
     mbar_init_fence();
   }
-  if (warp == 9) tmem_alloc(tmem_at, T::kCols);
+  if (warp == 9) tmem_alloc_pair(tmem_at, T::kCols);
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
   pdl_begin();
@@ -430,43 +482,41 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
       int s = 0, used = 0;
       uint32_t phase = 1;  // a first pass over the stages waits for nothing
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int nt = tile % tiles_n;
-        const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * BN;
-        const int sfb_tiles = T::kSfbTiles == 2 && t0 + 128 < j.rows ? 2 : 1;
-        const uint8_t* wsf = j.w_scales + static_cast<int64_t>(nt) * j.KT * 512;
-        const uint8_t* xsf = j.x_scales + t0 / 128 * j.KT * 512;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
+        const int nt = tile % tiles_n * 2, tt = tile / tiles_n * 2;  // in steps of 128
         for (int i = 0; i < stages_k; ++i) {
           if (!mbar_wait_bounded(empty + s, phase)) {
             ok = false;
             break;
           }
-          const uint32_t sf = j.KT - 2 * i >= 2 ? 1024u : 512u;  // the last stage may hold one scale tile of k
-          mbar_expect_tx(full + s, T::kABytes + T::kBBytes + sf * (1 + sfb_tiles));
-          tma_load_2d(sa + s * T::kABytes, &map_w, i * 128, nt * kM, full + s);
-          tma_load_2d(sb + s * T::kBBytes, &map_x, i * 128, static_cast<int>(t0), full + s);
-          bulk_load(ssa + s * T::kSfBytes, wsf + i * 1024, sf, full + s);
-          for (int q = 0; q < sfb_tiles; ++q)
-            bulk_load(ssb + (s * T::kSfbTiles + q) * T::kSfBytes,
-                      xsf + static_cast<int64_t>(q) * j.KT * 512 + i * 1024, sf, full + s);
+          if (rank == 0) mbar_expect_tx(full + s, 2 * T::kStageBytes);
+          const uint32_t bar = cluster_addr(full + s, 0);
+          // what lies past the end of a tensor reads as 0; a stage's second scale tile of k
+          // may be the next row's first, and is not used then
+          tma_load_2d_pair(sa + s * T::kCodeBytes, &map_w, i * 128, (nt + rank) * 128, bar);
+          tma_load_2d_pair(sb + s * T::kCodeBytes, &map_x, i * 128, (tt + rank) * 128, bar);
+          tma_load_2d_pair(ssa + s * T::kSfBytes, &map_wsf, 0, ((nt + rank) * j.KT + 2 * i) * 4, bar);
+          tma_load_2d_pair(ssb + 2 * s * T::kSfBytes, &map_xsf, 0, (tt * j.KT + 2 * i) * 4, bar);
+          tma_load_2d_pair(ssb + (2 * s + 1) * T::kSfBytes, &map_xsf, 0, ((tt + 1) * j.KT + 2 * i) * 4, bar);
           used = min(used + 1, T::kStages);
           if (++s == T::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!ok) {  // the copies in flight land before the CTA ends
+      if (!ok) {
         *failed = 1;
-        for (int q = 0; q < used; ++q) {
+        // the copies in flight, both CTAs', land before either ends
+        for (int q = 0; rank == 0 && q < used; ++q) {
           if (--s < 0) s = T::kStages - 1, phase ^= 1;
           mbar_wait_bounded(full + s, phase ^ 1);
         }
       }
     }
   } else if (warp == 9) {
-    if (elect_one()) {
+    if (rank == 0 && elect_one()) {
       int s = 0;
       uint32_t phase = 0, acc_phase = 1;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
         if (!mbar_wait_bounded(acc_free, acc_phase)) {
           ok = false;
           break;
@@ -478,41 +528,42 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sf = tmem + BN + s * T::kSfCols;
-          const int halves = j.KT - 2 * i >= 2 ? 2 : 1;
+          const uint32_t sf = tmem + T::kTile + s * T::kSfCols;
+          const int halves = j.KT - 2 * i >= 2 ? 2 : 1;  // scale tiles of k in this stage
           for (int q = 0; q < halves; ++q) {
-            tc_copy_scales(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
-            for (int r = 0; r < T::kSfbTiles; ++r)
-              tc_copy_scales(sf + 8 + 4 * (q * T::kSfbTiles + r),
-                             desc_scales(smem_u32(ssb + (s * T::kSfbTiles + r) * T::kSfBytes + q * 512)));
+            tc_copy_scales_pair(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
+            for (int r = 0; r < 2; ++r)
+              tc_copy_scales_pair(sf + 8 + 4 * (2 * q + r),
+                                  desc_scales(smem_u32(ssb + (2 * s + r) * T::kSfBytes + q * 512)));
           }
-          const uint64_t da = desc_codes(smem_u32(sa + s * T::kABytes));
-          const uint64_t db = desc_codes(smem_u32(sb + s * T::kBBytes));
+          const uint64_t da = desc_codes(smem_u32(sa + s * T::kCodeBytes));
+          const uint64_t db = desc_codes(smem_u32(sb + s * T::kCodeBytes));
           const int steps = min(4, (j.H - i * kStageK + 63) / 64);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (k < steps)
-              tc_mma_mxf4(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(BN, (k & 1) * 2), sf + 4 * (k >> 1),
-                          sf + 8 + 4 * (k >> 1) * T::kSfbTiles, i > 0 || k > 0);
-          tc_commit(empty + s);
+              tc_mma_mxf4_pair(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(T::kTile, T::kTile, (k & 1) * 2),
+                               sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1), i > 0 || k > 0);
+          tc_commit_pair(empty + s);
           if (++s == T::kStages) s = 0, phase ^= 1;
         }
-        if (ok) tc_commit(acc_full);
+        if (ok) tc_commit_pair(acc_full);
       }
       if (!ok) {  // what was issued ends before the memory it uses is given back
         *failed = 1;
-        tc_commit(acc_full);
+        tc_commit_pair(acc_full);
         mbar_wait_bounded(acc_full, 0);
         mbar_wait_bounded(acc_full, 1);
       }
     }
   } else {
-    constexpr int kCols = BN / 2, kBufs = OUT32 ? 1 : 2;
+    constexpr int kCols = T::kTile / 2;
     const int half = warp >> 2;
-    uint8_t* buf0 = so + warp * T::kOutBytes;
-    uint32_t phase = 0;
+    uint8_t* buf0 = so + warp * T::kBufs * T::kOutBytes;
     int turn = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const uint32_t freed = cluster_addr(acc_free, 0);
+    uint32_t phase = 0;
+    for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs) {
       const bool there = mbar_wait_bounded(acc_full, phase);
       phase ^= 1;
       if (__any_sync(kFull, !there || *failed)) {
@@ -530,17 +581,17 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
       }
       tc_fence_before();
-      if (lane == 0) mbar_arrive(acc_free);
-      const int n0 = tile % tiles_n * kM + (warp & 3) * 32;
-      const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * BN + half * kCols;
+      if (lane == 0) mbar_arrive_cluster(freed);
+      const int n0 = tile % tiles_n * T::kTile + rank * T::kHalf + (warp & 3) * 32;
+      const int64_t t0 = static_cast<int64_t>(tile / tiles_n) * T::kTile + half * kCols;
       if (n0 >= j.features) continue;
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         if (t0 + c >= j.rows) break;
-        uint8_t* buf = buf0 + (turn & (kBufs - 1)) * (T::kOutBytes / kBufs);
-        ++turn;
+        uint8_t* buf = buf0 + turn * T::kOutBytes;
+        turn = turn + 1 == T::kBufs ? 0 : turn + 1;
         // the buffer's last store has read it
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBufs - 1) : "memory");
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(T::kBufs - 1) : "memory");
         __syncwarp();
         if constexpr (OUT32) {
 #pragma unroll
@@ -564,12 +615,12 @@ __global__ void __launch_bounds__(Wide<BN>::kThreads, 1)
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
-  __syncthreads();
+  cluster_sync_all();  // neither CTA ends while the other's products or barriers use its memory
   if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
-    tmem_free(tmem, T::kCols);
+    tmem_free_pair(tmem, T::kCols);
   }
 }
 
@@ -622,18 +673,35 @@ cudaError_t out_map(CUtensorMap* m, const Mx4MatmulArgs& a) {
              : cudaErrorInvalidValue;
 }
 
-template <int BN, bool OUT32>
+// Scale tiles as rows of 128 bytes, two neighbouring tiles (1024 bytes) a box.
+cudaError_t scales_map(CUtensorMap* m, const uint8_t* scales, int64_t rows, int KT) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>((rows + 127) / 128) * KT * 4};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, 8}, step[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(scales), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <bool OUT32>
 cudaError_t launch_wide(const Mx4MatmulArgs& a, const Job& j, cudaStream_t st) {
-  auto* kern = k_mx4_matmul_wide<BN, OUT32>;
-  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Wide<BN>::kSmem)) return e;
-  CUtensorMap mw, mx, mo;
-  if (cudaError_t e = codes_map(&mw, a.w_codes, a.features, a.H, kM)) return e;
-  if (cudaError_t e = codes_map(&mx, a.x_codes, a.rows, a.H, BN)) return e;
+  using T = Wide<OUT32>;
+  auto* kern = k_mx4_matmul_wide<OUT32>;
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), T::kSmem)) return e;
+  CUtensorMap mw, mx, mws, mxs, mo;
+  if (cudaError_t e = codes_map(&mw, a.w_codes, a.features, a.H, T::kHalf)) return e;
+  if (cudaError_t e = codes_map(&mx, a.x_codes, a.rows, a.H, T::kHalf)) return e;
+  if (cudaError_t e = scales_map(&mws, a.w_scales, a.features, j.KT)) return e;
+  if (cudaError_t e = scales_map(&mxs, a.x_scales, a.rows, j.KT)) return e;
   if (cudaError_t e = out_map(&mo, a)) return e;
-  const int64_t tiles = ((a.features + kM - 1) / kM) * ((a.rows + BN - 1) / BN);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()));
-  return launch_pdl(kern, grid, dim3(Wide<BN>::kThreads), Wide<BN>::kSmem, st, j, mw, mx, mo);
+  const int64_t tiles = ((a.features + T::kTile - 1) / T::kTile) * ((a.rows + T::kTile - 1) / T::kTile);
+  const int64_t pairs = std::min<int64_t>(tiles, num_sms() / 2);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(T::kThreads), T::kSmem, st, j, mw, mx, mws, mxs,
+                    mo);
 }
 
 template <int BN>
@@ -678,7 +746,7 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, cudaStream_t st) {
   int parts = 1;
   while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
   if (a.rows > 128 && parts == 1)
-    return a.out_f32 ? launch_wide<256, true>(a, j, st) : launch_wide<256, false>(a, j, st);
+    return a.out_f32 ? launch_wide<true>(a, j, st) : launch_wide<false>(a, j, st);
   if (bn == 16) return launch<16>(a, j, parts, st);
   if (bn == 32) return launch<32>(a, j, parts, st);
   if (bn == 64) return launch<64>(a, j, parts, st);

@@ -11,6 +11,11 @@ standing in as P slabs in one GPU's HBM:
   fresh epoch (one launch for all slabs), then the consumer validates and reduces
   them.
 
+With a ``projection`` weight the step goes on into the next layer: y is
+quantized to microscaled 4-bit floating point and multiplied with the weight,
+which is quantized once, at construction; the product is one rank's partial
+sums of the next boundary.
+
 With ``splits`` > 1 (BF16_TAGGED, INT8, INT4) the token rows are split into
 that many subsets whose fused calls run on their own streams (TokenWeave's
 token splitting), at even or wave-aware boundaries.
@@ -20,6 +25,8 @@ only launches libfcomm kernels.  ``alg_bytes()`` gives the bytes the method
 must move per step (intermediates kept on chip are not counted).
 """
 from __future__ import annotations
+
+from typing import Optional
 
 import numpy as np
 import torch
@@ -47,7 +54,8 @@ def qs_bytes(w: Workload, E: int) -> int:
 
 class Pipeline:
     def __init__(self, w: Workload, inputs: dict, device="cuda", with_payload=True,
-                 split: str = "even"):
+                 split: str = "even", projection: Optional[torch.Tensor] = None):
+        """projection: bf16 or fp32 [features, H] weight of the next projection, or None."""
         self.w = w
         self.device = device
         self.spec = fc.QSpec(w.fmt, w.group)
@@ -85,6 +93,16 @@ class Pipeline:
         else:
             self.wave_rows = None
             self.bounds = [w.T * i // n for i in range(n + 1)]
+        self.weight = None
+        if projection is not None:
+            if projection.dim() != 2 or projection.shape[1] != H:
+                raise ValueError(f"projection must be [features, {H}] (got {tuple(projection.shape)})")
+            features = projection.shape[0]
+            self.weight = fc.alloc_mx4(features, H, device)
+            fc.mx4_quantize(projection.to(device).contiguous(), self.weight)
+            self.y_mx4 = fc.alloc_mx4(T, H, device)
+            self.out = torch.empty(T, features, dtype=torch.bfloat16, device=device)
+            self.projection_status = torch.zeros(2, dtype=torch.int32, device=device)
         self.launches_per_step = self._launches()
         self.graph = None
         self._bind()
@@ -94,6 +112,9 @@ class Pipeline:
         spends no host time converting arguments."""
         w = self.w
         self._send, self._fuse, self._split = None, None, []
+        self._project = [] if self.weight is None else [
+            fc.bind_mx4_quantize(self.y, self.y_mx4),
+            fc.bind_mx4_matmul(self.y_mx4, self.weight, self.out, d_status=self.projection_status)]
         if w.fmt in (FMT_INT8_SYM, FMT_INT4_ASYM):
             self._send = fc.bind_group_quantize_multi(self.x, self.spec, self.codes)
             if max(1, w.splits) == 1:
@@ -138,15 +159,17 @@ class Pipeline:
     def _launches(self) -> int:
         """Kernels launched per step: the sender, the consumer call(s), and for
         each consumer call that takes a status word the one-thread kernel
-        that resets it."""
+        that resets it; with a projection the quantization, the product and the
+        reset of its status."""
         w = self.w
+        n = 0 if self.weight is None else 3
         if w.fmt in (FMT_INT8_SYM, FMT_INT4_ASYM):
-            return 1 + max(1, w.splits)
+            return n + 1 + max(1, w.splits)
         if w.fmt in QTAGGED:
-            return 1 + 2
+            return n + 1 + 2
         if w.fmt == FMT_BF16:
-            return 1
-        return 1 + 2 * max(1, w.splits)
+            return n + 1
+        return n + 1 + 2 * max(1, w.splits)
 
     def step(self, stream=None):
         """Launch one pass of the hot path on `stream` (default: current)."""
@@ -209,6 +232,8 @@ class Pipeline:
             self._fuse(st)
         else:
             self._split_consume(st)
+        for call in self._project:
+            call(st)
 
     def _split_consume(self, st):
         fork = torch.cuda.Event()
@@ -227,7 +252,16 @@ class Pipeline:
 
     # ------------------------------------------------------------------
     def alg_bytes(self) -> dict:
-        """Algorithmic bytes per step, by stage: {'sender': .., 'fused': ..}."""
+        """Algorithmic bytes per step, by stage: {'sender': .., 'fused': ..}, and
+        {'projection': ..} with one (y and the weight in, the product out)."""
+        w = self.w
+        b = self._boundary_bytes()
+        if self.weight is not None:
+            features = self.out.shape[1]
+            b["projection"] = 2 * w.T * w.H + features * w.H // 2 + features * w.H // 32 + 2 * w.T * features
+        return b
+
+    def _boundary_bytes(self) -> dict:
         w = self.w
         E, H, P = w.T * w.H, w.H, w.P
         if w.fmt in (FMT_INT8_SYM, FMT_INT4_ASYM):
@@ -257,4 +291,7 @@ class Pipeline:
                        zeros=None if self.payload[2] is None else self.payload[2].cpu().numpy())
         if self.status is not None:
             out["status"] = self.status.cpu().numpy()
+        if self.weight is not None:
+            out["out"] = self.out.view(torch.int16).cpu().numpy().view(np.uint16)
+            out["projection_status"] = self.projection_status.cpu().numpy()
         return out

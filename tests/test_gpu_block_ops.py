@@ -384,7 +384,137 @@ def test_nan_scales_spoil_their_own_rows_and_columns():
     assert torch.equal(out[~bad].double(), (xv @ wv.T)[~bad])
 
 
+@pytest.mark.parametrize("rows,features,hidden", [(2100, 4368, 288), (1100, 9232, 1568), (4099, 1552, 96)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_product_over_many_tiles(rows, features, hidden, dtype):
+    """More tiles than the GPU holds at once, the last of them ragged; exact as above."""
+    g = gen_of("tiles", rows, features, hidden)
+    x, xv = mx4_random(g, rows, hidden)
+    w, wv = mx4_random(g, features, hidden)
+    out = torch.full((rows, features), float("nan"), dtype=DT[dtype], device="cuda")
+    fc.mx4_matmul(x, w, out)
+    assert torch.equal(out, (xv.cuda() @ wv.cuda().T).to(DT[dtype]))
+
+
+# ------------------------------------------ sizes that take other kernels --
+@pytest.mark.parametrize("rows,hidden", [(1300, 1040), (700, 8192)])
+def test_block_norm_of_many_rows(rows, hidden):
+    i = norm_inputs(rows, hidden, "bf16", "gate-seq")
+    h, y = torch.empty_like(i["x"]), torch.empty_like(i["x"])
+    fc.block_norm(i["x"], i["r"], h, y, **spec_of(i))
+    check_norm(i, h, y, torch.bfloat16)
+
+
+@pytest.mark.parametrize("form", ["sandwich", "gate-seq", "gate-token", "pre", "post"])
+@pytest.mark.parametrize("rows,hidden,dtype", [(1260, 3600, "bf16"), (330, 6160, "bf16"), (315, 5136, "f32"),
+                                               (40, 12304, "bf16"), (20, 12304, "f32"), (700, 2576, "f32")])
+def test_gradient_of_every_plan(rows, hidden, dtype, form):
+    i = grad_inputs(rows, hidden, dtype, form)
+    out = grad_outputs(i)
+    status = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    ws = fc.alloc_block_norm_workspace(rows, hidden, 0 if i["gate"] is None else i["gate"].shape[0])
+    fc.block_norm_backward(i["x"], i["h"], i["dy"], i["dh"], workspace=ws, d_status=status, **out, **spec_of(i))
+    check_grad(i, out)
+    assert status.tolist() == [0, fc.STATUS_NO_INDEX]
+
+
+# ------------------------------------------------- offsets past 32 bits ----
+def test_rows_past_the_32_bit_offsets():
+    """More than 2^32 elements: the first and the last rows as when they are alone."""
+    rows, hidden, k = 66000, 65536, 3
+    x = torch.randn(rows, hidden, device="cuda", dtype=torch.bfloat16)
+    q = fc.alloc_mx4(rows, hidden)
+    fc.mx4_quantize(x, q)
+    for r in (slice(0, k), slice(rows - k, rows)):
+        code, byte = ref.mx4_reference(x[r].cpu())
+        assert torch.equal(ref.unpack(q[0][r].cpu()), code)
+        off = ref.scale_offsets(rows, hidden)[r].cuda()
+        assert torch.equal(q[1][off.flatten()].cpu().long(), byte.flatten())
+    want = x[rows - k:].clone()
+    fc.mx4_dequantize(q, x)
+    assert torch.equal(x[rows - k:].cpu().double(), ref.mx4_values(*ref.mx4_reference(want.cpu())))
+
+
+def test_norm_and_gradient_past_the_32_bit_offsets():
+    rows, hidden, k = 530000, 8192, 5
+    w = torch.ones(hidden, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(rows, hidden, device="cuda", dtype=torch.bfloat16)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    fc.block_norm(x, x, h, y, post_weight=w, pre_weight=w)
+    small = x[rows - k:].contiguous()
+    h2, y2 = torch.empty_like(small), torch.empty_like(small)
+    fc.block_norm(small, small, h2, y2, post_weight=w, pre_weight=w)
+    assert torch.equal(h[rows - k:], h2) and torch.equal(y[rows - k:], y2)
+    dx, dx2 = torch.empty_like(x), torch.empty_like(small)
+    dw = torch.empty(hidden, device="cuda")
+    for a, b, c, n in ((x, h, dx, rows), (small, h2, dx2, k)):
+        fc.block_norm_backward(a, b, a, b, c, fc.alloc_block_norm_workspace(n, hidden), dpost_weight=dw,
+                               post_weight=w, pre_weight=w)
+    assert torch.equal(dx[rows - k:], dx2)
+
+
+@pytest.mark.parametrize("rows,features", [(140000, 16384), (100, 4190000)])
+def test_product_past_the_32_bit_offsets(rows, features):
+    hidden = 64
+    x, xv = mx4_random(gen_of("far", rows), rows, hidden)
+    w, wv = mx4_random(gen_of("wide", features), features, hidden)
+    out = torch.empty(rows, features, dtype=torch.bfloat16 if rows > 100 else torch.float32, device="cuda")
+    fc.mx4_matmul(x, w, out)
+    for r, c in ((slice(0, 3), slice(0, 40)), (slice(rows - 3, rows), slice(features - 40, features))):
+        assert torch.equal(out[r, c].cpu(), (xv[r] @ wv[c].T).to(out.dtype))
+
+
 # ------------------------------------------------------- used together -----
+def test_two_gradients_at_once():
+    """Two calls on two streams, each with a workspace of its own, as one after the other."""
+    jobs = []
+    for k, (rows, hidden) in enumerate([(900, 2064), (700, 4096)]):
+        i = grad_inputs(rows, hidden, "bf16", "gate-seq")
+        want, out = grad_outputs(i), grad_outputs(i)
+        run_grad(i, want)
+        ws = fc.alloc_block_norm_workspace(rows, hidden, i["gate"].shape[0])
+        jobs.append((i, want, out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, _, out, ws, st in jobs:
+            run_grad(i, out, ws, st)
+    torch.cuda.synchronize()
+    for _, want, out, _, _ in jobs:
+        for name in want:
+            assert torch.equal(want[name], out[name]), name
+
+
+@pytest.mark.parametrize("name", ["decode", "prefill", "token-split", "decode-qtagged"])
+def test_pipeline_into_the_next_projection(name):
+    """The boundary's step with a projection: h, y and the payload as without it, and
+    the product of the quantised y with the quantised weight."""
+    from quantized_reduce_rmsnorm_gb300 import synth
+    from quantized_reduce_rmsnorm_gb300.pipeline import Pipeline
+    w = synth.Workload(**{**synth.WORKLOADS[name].__dict__, "T": 48})
+    inp = synth.make_inputs(w, seed=3)
+    weight = randn(gen_of("projection", name), 1040, w.H, std=w.H ** -0.5, dtype=torch.bfloat16)
+    plain, pipe = Pipeline(w, inp), Pipeline(w, inp, projection=weight)
+    assert pipe.launches_per_step == plain.launches_per_step + 3
+    assert set(pipe.alg_bytes()) == set(plain.alg_bytes()) | {"projection"}
+    plain.step()
+    pipe.step()
+    want, got = plain.outputs(), pipe.outputs()
+    for k in want:
+        assert want[k] is None and got[k] is None or (want[k] == got[k]).all(), k
+    assert got["projection_status"].tolist() == [0, fc.STATUS_NO_INDEX]
+    xv = ref.mx4_values(*ref.mx4_reference(pipe.y.cpu()))
+    wv = ref.mx4_values(*ref.mx4_reference(weight.cpu()))
+    value, size = xv @ wv.T, xv.abs() @ wv.abs().T
+    within(pipe.out.cpu(), value, HALF[torch.bfloat16] * value.abs() + w.H * 2.0 ** -23 * size, "out")
+    if name in ("decode", "prefill"):
+        pipe.capture()
+        pipe.out.zero_()
+        pipe.replay()
+        assert (pipe.outputs()["out"] == got["out"]).all()
+    with pytest.raises(ValueError, match="projection"):
+        Pipeline(w, inp, projection=weight[:, :64])
+
+
 def test_norm_quantise_project_streams_and_graph():
     """Norms to four bits and through a projection: launched on a side stream, and
     captured and replayed on new inputs, the same bits as one call after another."""
