@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   }
 }
 
-constexpr int kSumWarps = 16, kSumCols = 64;
+constexpr int kSumWarps = 16, kSumCols = 64, kSumBatch = 10;
 // Adds the CTAs' sums: 64 columns a CTA (a lane has two), 16 warps over the
 // addends, in a fixed order.  blockIdx.y: 0 the norm before, 1 the norm after, 2 +
 // s gate row s (segs is below kNormGradMaxCtas where their sums are in pieces).
@@ -534,10 +534,19 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_block_norm_grad_sum(const Gr
   const float* src = y == 0 ? job.ws_pre : y == 1 ? job.ws_post : job.ws_gate + (y - 2) * static_cast<int64_t>(job.p.cuts) * H;
   const int n = y < 2 ? job.p.grid : job.p.cuts;
   if ((y == 0 && !job.a.dpre_w) || (y == 1 && !job.a.dpost_w)) return;
-  float2 s = make_float2(0.0f, 0.0f);
+  const float2 zero = make_float2(0.0f, 0.0f);
+  float2 s = zero;
   if (col < H)
-#pragma unroll 8
-    for (int i = w; i < n; i += kSumWarps) s = padd(s, *reinterpret_cast<const float2*>(src + static_cast<int64_t>(i) * H + col));
+    for (int i0 = w; i0 < n; i0 += kSumWarps * kSumBatch) {  // loads that do not wait for one another
+      float2 v[kSumBatch];
+#pragma unroll
+      for (int k = 0; k < kSumBatch; ++k) {
+        const int i = i0 + k * kSumWarps;
+        v[k] = i < n ? *reinterpret_cast<const float2*>(src + static_cast<int64_t>(i) * H + col) : zero;
+      }
+#pragma unroll
+      for (int k = 0; k < kSumBatch; ++k) s = padd(s, v[k]);
+    }
   red[w][l] = s;
   __syncthreads();
   if (w != 0 || col >= H) return;

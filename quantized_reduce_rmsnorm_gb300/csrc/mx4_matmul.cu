@@ -522,30 +522,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
           break;
         }
         acc_phase ^= 1;
-        for (int i = 0; i < stages_k; ++i) {
-          if (!mbar_wait_bounded(full + s, phase)) {
-            ok = false;
-            break;
-          }
+        // Scales of 128 elements of k go to the tensor core's memory while the products
+        // before them run: the second half's behind the stage's first product, the
+        // next stage's first half's before its last.
+        auto copy_scales = [&](int st, int q) {
+          const uint32_t sf = tmem + T::kTile + st * T::kSfCols;
+          tc_copy_scales_pair(sf + 4 * q, desc_scales(smem_u32(ssa + st * T::kSfBytes + q * 512)));
+          for (int r = 0; r < 2; ++r)
+            tc_copy_scales_pair(sf + 8 + 4 * (2 * q + r), desc_scales(smem_u32(ssb + (2 * st + r) * T::kSfBytes + q * 512)));
+        };
+        auto ready = [&](int st, uint32_t ph) {  // the stage's copies have landed
+          ok = mbar_wait_bounded(full + st, ph);
           tc_fence_after();
+          return ok;
+        };
+        if (!ready(s, phase)) break;
+        copy_scales(s, 0);
+        for (int i = 0; i < stages_k; ++i) {
           const uint32_t sf = tmem + T::kTile + s * T::kSfCols;
-          const int halves = j.KT - 2 * i >= 2 ? 2 : 1;  // scale tiles of k in this stage
-          for (int q = 0; q < halves; ++q) {
-            tc_copy_scales_pair(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
-            for (int r = 0; r < 2; ++r)
-              tc_copy_scales_pair(sf + 8 + 4 * (2 * q + r),
-                                  desc_scales(smem_u32(ssb + (2 * s + r) * T::kSfBytes + q * 512)));
-          }
           const uint64_t da = desc_codes(smem_u32(sa + s * T::kCodeBytes));
           const uint64_t db = desc_codes(smem_u32(sb + s * T::kCodeBytes));
           const int steps = min(4, (j.H - i * kStageK + 63) / 64);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
+          auto product = [&](int k) {
             if (k < steps)
               tc_mma_mxf4_pair(tmem, da + 2 * k, db + 2 * k, idesc_mxf4(T::kTile, T::kTile, (k & 1) * 2),
                                sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1), i > 0 || k > 0);
+          };
+          product(0);
+          if (j.KT - 2 * i >= 2) copy_scales(s, 1);  // the last stage may hold one scale tile of k
+          product(1);
+          product(2);
+          const int s1 = s + 1 == T::kStages ? 0 : s + 1;
+          const uint32_t phase1 = s1 == 0 ? phase ^ 1 : phase;
+          if (i + 1 < stages_k) {
+            if (!ready(s1, phase1)) break;
+            copy_scales(s1, 0);
+          }
+          product(3);
           tc_commit_pair(empty + s);
-          if (++s == T::kStages) s = 0, phase ^= 1;
+          s = s1, phase = phase1;
         }
         if (ok) tc_commit_pair(acc_full);
       }
