@@ -474,10 +474,12 @@ def _mx4(q, rows: int, hidden: int, name: str) -> Mx4:
     if q is None:
         return Mx4(None, None)
     codes, scales = q
-    for t, n, what in ((codes, mx4_codes_bytes(rows, hidden), "codes"),
-                       (scales, mx4_scales_bytes(rows, hidden), "scales")):
-        if t.dtype != torch.uint8 or t.numel() < n:
-            raise ValueError(f"{name}'s {what} must be {n} uint8 (got {t.numel()} {t.dtype})")
+    n = mx4_scales_bytes(rows, hidden)
+    if codes.dtype != torch.uint8 or tuple(codes.shape) != (rows, hidden // 2):
+        raise ValueError(f"{name}'s codes must be [{rows}, {hidden // 2}] uint8 "
+                         f"(got {tuple(codes.shape)} {codes.dtype})")
+    if scales.dtype != torch.uint8 or scales.numel() != n:
+        raise ValueError(f"{name}'s scales must be {n} uint8 (got {scales.numel()} {scales.dtype})")
     return Mx4(_ptr(codes), _ptr(scales))
 
 

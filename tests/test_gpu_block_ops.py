@@ -203,6 +203,29 @@ def test_block_norm_rows_of_zeros_and_non_finite_rows_stay_their_own():
     assert not torch.isfinite(y[8]).any()
 
 
+def test_what_the_binding_refuses():
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    h, q = torch.empty_like(x), fc.alloc_mx4(8, 64)
+    with pytest.raises(ValueError, match="contiguous"):
+        fc.block_norm(torch.zeros(64, 8, dtype=torch.bfloat16, device="cuda").t(), None, h)
+    with pytest.raises(ValueError, match="residual_out"):
+        fc.block_norm(x, None, h.float())
+    with pytest.raises(ValueError, match="pre_weight"):
+        fc.block_norm(x, x, h, h, pre_weight=torch.ones(63, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(fc.FcommError, match="gate_rows"):
+        fc.block_norm(x, x, h, gate=torch.ones(3, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(fc.FcommError, match="overlaps"):
+        fc.block_norm(x, x, h, h, pre_weight=torch.ones(64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="codes"):
+        fc.mx4_quantize(x, fc.alloc_mx4(4, 128))
+    with pytest.raises(ValueError, match="workspace"):
+        fc.block_norm_backward(x, x, x, x, h, torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="x's codes"):
+        fc.mx4_matmul(fc.alloc_mx4(8, 32), fc.alloc_mx4(16, 64), torch.empty(8, 16, device="cuda"))
+    with pytest.raises(fc.FcommError, match="features"):
+        fc.mx4_matmul(q, fc.alloc_mx4(8, 64), torch.empty(8, 8, device="cuda"))
+
+
 # ------------------------------------------------------------ gradient -----
 def grad_inputs(rows, hidden, dtype, form):
     i = norm_inputs(rows, hidden, dtype, form)
@@ -328,7 +351,8 @@ def mx4_random(g, rows, hidden, scales=(127, 128)):
 
 SHAPES = [(1, 16, 32), (1, 128, 64), (2, 144, 96), (3, 256, 128), (16, 128, 160), (17, 272, 224), (31, 128, 256),
           (33, 400, 288), (64, 512, 1024), (65, 128, 512), (127, 144, 320), (129, 272, 2080), (200, 1040, 544),
-          (256, 256, 4096), (257, 400, 352), (300, 2064, 1056), (513, 640, 8192), (1, 8192, 4096), (64, 4096, 8192)]
+          (256, 256, 4096), (257, 400, 352), (300, 2064, 1056), (513, 640, 8192), (1, 8192, 4096), (64, 4096, 8192),
+          (3, 32, 65536), (5000, 16, 64), (130, 48, 8192), (1, 16, 16384)]
 
 
 @pytest.mark.parametrize("rows,features,hidden", SHAPES)
@@ -356,6 +380,25 @@ def test_product_with_scales(rows, features, hidden):
     out = torch.full((rows, features), float("nan"), device="cuda")
     fc.mx4_matmul(x, w, out)
     within(out.cpu(), want, hidden * 2.0 ** -23 * size, "out")
+
+
+@pytest.mark.parametrize("rows", [5, 200])
+@pytest.mark.parametrize("ex,ew", [(-120, 110), (120, -110), (100, 20), (-127, 127), (-60, -60)])
+def test_product_with_far_scales(rows, ex, ew):
+    """The blocks' scales multiply exactly over their whole range.  Every partial sum,
+    in any order, is at most the sum of the terms' sizes: where that is below
+    binary32's largest number nothing overflows, and the result is exact; at 2^120
+    it reaches 160 * 36 * 2^120 = 7.7e39, past 3.4e38, and there a sum on the way may
+    overflow although the last one does not."""
+    g = gen_of("far scales", rows, ex, ew)
+    x, xv = mx4_random(g, rows, 160, (127 + ex, 128 + ex))
+    w, wv = mx4_random(g, 272, 160, (127 + ew, 128 + ew))
+    out = torch.empty(rows, 272, device="cuda")
+    fc.mx4_matmul(x, w, out)
+    safe = xv.abs() @ wv.abs().T < torch.finfo(torch.float32).max
+    assert safe.all() or ex + ew == 120
+    out, want = out.cpu(), (xv @ wv.T).float()
+    assert ((out == want) | (~safe & ~torch.isfinite(out))).all()
 
 
 def test_product_leaves_what_is_behind_the_output_alone():
