@@ -71,6 +71,7 @@ __device__ __forceinline__ void store16(void* base, int64_t elem, const float v[
 struct GradPlan {
   int64_t segs, seg_rows;
   int cuts, grid;
+  int cut_rows, cut_more;  // rows of a piece; the first cut_more of a run have one more
   bool gate_direct;   // a gate row for every row: its gradient is written row by row
   bool gate_final;    // one piece per gate row: its sum is final
 };
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(1024) k_block_norm_grad(const GradJob job) {
   }
   for (int64_t piece = blockIdx.x; piece < p.segs * p.cuts; piece += gridDim.x) {
     const int64_t seg = piece / p.cuts, cut = piece - seg * p.cuts;
-    const int64_t r0 = seg * p.seg_rows + p.seg_rows * cut / p.cuts;
-    const int64_t r1 = seg * p.seg_rows + p.seg_rows * (cut + 1) / p.cuts;
+    const int64_t r0 = seg * p.seg_rows + cut * p.cut_rows + min(static_cast<int>(cut), p.cut_more);
+    const int64_t r1 = r0 + p.cut_rows + (cut < p.cut_more);
     for (int64_t row = r0; row < r1; ++row) {
       const int64_t at = row * a.H + e;
       float x[16] = {}, h[16] = {}, dy[16] = {}, dh[16] = {}, g[16];
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   __shared__ __align__(16) float red[2][8 * kRedStride];  // neighbouring rows take turns
   __shared__ uint64_t full[kMostStages];
   __shared__ volatile int late[2];  // a copy did not land in time, by turns as red
-  __shared__ struct { int piece, row, end, count; } next;
+  __shared__ struct { int piece, row, end, stage, count; } next;
   constexpr int es = F32 ? 4 : 2, kP = W / 2;
   const BlockNormGradArgs& a = job.a;
   const GradPlan& p = job.p;
@@ -341,34 +342,46 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   const int pieces = static_cast<int>(p.segs) * p.cuts;  // at most the rows
   auto piece_rows = [&](int piece, int& r0, int& r1) {
     const int seg = piece / p.cuts, cut = piece - seg * p.cuts;
-    r0 = static_cast<int>(seg * p.seg_rows + p.seg_rows * cut / p.cuts);
-    r1 = static_cast<int>(seg * p.seg_rows + p.seg_rows * (cut + 1) / p.cuts);
+    r0 = seg * static_cast<int>(p.seg_rows) + cut * p.cut_rows + min(cut, p.cut_more);
+    r1 = r0 + p.cut_rows + (cut < p.cut_more);
   };
-  // Stages the next row (thread 0; `next` keeps its place out of the registers).
-  auto stage_next = [&] {
-    if (next.piece >= pieces) return;
-    const int s = next.count++ % stages, row = next.row++;
-    fence_proxy_async_smem();
-    uint8_t* dst = ring + static_cast<size_t>(s) * slots * row_bytes;
-    const int64_t off = static_cast<int64_t>(row) * row_bytes;
-    auto copy = [&](int slot, const void* src) {
-      bulk_load(dst + slot * row_bytes, static_cast<const char*>(src) + off, row_bytes, full + s);
+  // Stages the next row (the first warp): each of a row's tensors is one lane's
+  // copy.  `next` keeps the place out of the registers.
+  const char* from = nullptr;
+  {
+    int k = 0;
+    auto slot = [&](bool there, const void* base) {
+      if (there && t == k++) from = static_cast<const char*>(base);
     };
-    mbar_expect_tx(full + s, slots * row_bytes);
-    copy(0, a.x);
-    if (pre) copy(slot_h, a.h), copy(slot_dy, a.dy);
-    if (a.dh) copy(slot_dh, a.dh);
-    if (TOKEN) copy(slot_g, a.gate);
-    if (row + 1 == next.end) {
-      next.piece += gridDim.x;
+    slot(true, a.x), slot(pre, a.h), slot(pre, a.dy), slot(a.dh != nullptr, a.dh), slot(TOKEN, a.gate);
+  }
+  auto stage_next = [&] {
+    const int piece = next.piece, row = next.row, st = next.stage;
+    __syncwarp();
+    if (piece >= pieces) return;
+    if (t == 0) {
+      fence_proxy_async_smem();
+      mbar_expect_tx(full + st, slots * row_bytes);
+      ++next.count;
+      next.stage = st + 1 == stages ? 0 : st + 1;
+      next.row = row + 1;
+      if (row + 1 == next.end) {
+        next.piece = piece + gridDim.x;
+        if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
+      }
+    }
+    __syncwarp();
+    if (t < slots)
+      bulk_load(ring + (st * slots + t) * row_bytes, from + static_cast<int64_t>(row) * row_bytes, row_bytes, full + st);
+  };
+  if (t < 32) {
+    if (t == 0) {
+      next.piece = blockIdx.x;
+      next.count = next.stage = 0;
       if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
     }
-  };
-  if (t == 0) {
-    next.piece = blockIdx.x;
-    next.count = 0;
-    if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
-    for (int s = 0; s < stages; ++s) stage_next();
+    __syncwarp();
+    for (int k = 0; k < stages; ++k) stage_next();
   }
 
   const float inv_n = 1.0f / static_cast<float>(H);
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
         stop = true;
         break;
       }
-      if (t == 0) stage_next();
+      if (t < 32) stage_next();
       if (++s == stages) s = 0, phase ^= 1;
       const float inv = pre ? inv_sqrt(__fadd_rn(r[0] * inv_n, a.eps_pre)) : 0.0f;
       const float k = inv * inv * inv * (r[1] * inv_n);
@@ -572,6 +585,8 @@ void plan(GradJob& job, int64_t most) {
   p.seg_rows = a.rows / p.segs;
   // one piece a CTA where there are fewer gate rows than CTAs, else one piece a gate row
   p.cuts = static_cast<int>(std::max<int64_t>(1, std::min(most / p.segs, p.seg_rows)));
+  p.cut_rows = static_cast<int>(p.seg_rows / p.cuts);
+  p.cut_more = static_cast<int>(p.seg_rows % p.cuts);
   p.gate_final = p.cuts == 1;
   p.grid = static_cast<int>(std::min(most, p.segs * p.cuts));
   job.ws_pre = a.ws;
