@@ -166,8 +166,6 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream.__class__ is int:
-        return stream
     if stream is None:  # the handle alone: a torch Stream object costs more than a launch
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
@@ -192,14 +190,12 @@ class Bound:
     itself.  The object holds a reference to every tensor it was bound to,
     so their memory cannot be freed and handed to another tensor while the
     bound call exists.  For the calls that carry an epoch (tagged formats),
-    `epoch` may be changed between calls.  A call bound to a `device` runs on
-    that device's current stream whichever device is current."""
-    __slots__ = ("_fn", "_args", "_si", "_ei", "_keep", "_dev")
+    `epoch` may be changed between calls."""
+    __slots__ = ("_fn", "_args", "_si", "_ei", "_keep")
 
-    def __init__(self, fn, args, stream_index, epoch_index=None, keep=(), device=None):
+    def __init__(self, fn, args, stream_index, epoch_index=None, keep=()):
         self._fn, self._args, self._si, self._ei, self._keep = fn, list(args), stream_index, \
             epoch_index, keep
-        self._dev = device
 
     @property
     def epoch(self) -> int:
@@ -211,14 +207,37 @@ class Bound:
 
     def __call__(self, stream=None):
         a = self._args
-        if self._dev is not None:
-            if torch._C._cuda_getDevice() != self._dev:
-                with torch.cuda.device(self._dev):
-                    return self(stream)
-            if stream is None:
-                stream = torch._C._cuda_getCurrentRawStream(self._dev)
         a[self._si] = _stream(stream)
         st = self._fn(*a)
+        if st != FC_OK:
+            _check(st)
+
+
+class DeviceBound(Bound):
+    """A Bound call that belongs to the device of its tensors: it runs there, on
+    that device's current stream by default, whichever device is current.
+
+    Its arguments are ctypes objects of the entry point's own types from the
+    start and go through a function object without argtypes, so that a call
+    converts none of them (2.6 us a launch on GB300's host, 3.1 with)."""
+    __slots__ = ("_dev", "_last")
+
+    def __init__(self, fn, args, stream_index, keep, device: int):
+        def exact(a, t):
+            return a if isinstance(a, t) or type(a).__name__ == "CArgObject" else t(a)
+        super().__init__(_lib[fn.__name__], [exact(a, t) for a, t in zip(args, fn.argtypes)],
+                         stream_index, keep=keep)
+        self._dev, self._last = device, None
+
+    def __call__(self, stream=None):
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self(stream)
+        s = torch._C._cuda_getCurrentRawStream(self._dev) if stream is None else _stream(stream)
+        if s != self._last:
+            self._args[self._si] = ctypes.c_void_p(s)
+            self._last = s
+        st = self._fn(*self._args)
         if st != FC_OK:
             _check(st)
 
@@ -490,7 +509,7 @@ def _one_device(*tensors) -> int:
     return devices.pop().index
 
 
-def _once(call: Bound, stream):
+def _once(call: DeviceBound, stream):
     """Run a call bound for this one time.  On a stream other than the current
     one, its tensors' memory is kept from reuse until that stream is done."""
     call(stream)
@@ -516,9 +535,9 @@ def alloc_mx4(rows: int, hidden: int, device="cuda"):
             torch.empty(mx4_scales_bytes(rows, hidden), dtype=torch.uint8, device=device))
 
 
-def bind_mx4_quantize(x: torch.Tensor, out) -> Bound:
+def bind_mx4_quantize(x: torch.Tensor, out) -> DeviceBound:
     rows, hidden = _rows_hidden(x)
-    return Bound(load().fc_mx4_quantize,
+    return DeviceBound(load().fc_mx4_quantize,
                  [ctypes.c_void_p(_ptr(x)), _dtype(x, "x"), rows, hidden,
                   _mx4(out, rows, hidden, "out"), None], 5,
                  keep=(x, *out), device=_one_device(x, *out))
@@ -529,9 +548,9 @@ def mx4_quantize(x: torch.Tensor, out, stream=None):
     _once(bind_mx4_quantize(x, out), stream)
 
 
-def bind_mx4_dequantize(q, out: torch.Tensor) -> Bound:
+def bind_mx4_dequantize(q, out: torch.Tensor) -> DeviceBound:
     rows, hidden = _rows_hidden(out)
-    return Bound(load().fc_mx4_dequantize,
+    return DeviceBound(load().fc_mx4_dequantize,
                  [_mx4(q, rows, hidden, "q"), rows, hidden, ctypes.c_void_p(_ptr(out)),
                   _dtype(out, "out"), None], 5,
                  keep=(*q, out), device=_one_device(*q, out))
@@ -542,12 +561,12 @@ def mx4_dequantize(q, out: torch.Tensor, stream=None):
     _once(bind_mx4_dequantize(q, out), stream)
 
 
-def bind_mx4_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None) -> Bound:
+def bind_mx4_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None) -> DeviceBound:
     rows, features = _rows_hidden(out)
     if w[0].dim() != 2 or w[0].shape[0] != features:
         raise ValueError(f"w's codes must be [{features}, hidden / 2] (got {tuple(w[0].shape)})")
     hidden = 2 * w[0].shape[1]
-    return Bound(load().fc_mx4_matmul,
+    return DeviceBound(load().fc_mx4_matmul,
                  [_mx4(x, rows, hidden, "x"), _mx4(w, features, hidden, "w"), rows, features,
                   hidden, ctypes.c_void_p(_ptr(out)), _dtype(out, "out"),
                   ctypes.c_void_p(_want(d_status, (2,), torch.int32, "d_status")), None], 8,
@@ -580,7 +599,7 @@ def bind_block_norm(x: torch.Tensor, residual_in: Optional[torch.Tensor],
                     gate: Optional[torch.Tensor] = None,
                     pre_weight: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
                     block_scale: float = 1.0, post_eps: float = 1e-5, pre_eps: float = 1e-5,
-                    y_mx4=None) -> Bound:
+                    y_mx4=None) -> DeviceBound:
     rows, hidden = _rows_hidden(x)
     spec = _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
                             pre_eps)
@@ -590,7 +609,7 @@ def bind_block_norm(x: torch.Tensor, residual_in: Optional[torch.Tensor],
             P(_want(residual_out, x.shape, x.dtype, "residual_out")),
             P(_want(y, x.shape, x.dtype, "y")), _mx4(y_mx4, rows, hidden, "y_mx4"), None]
     keep = (x, residual_in, residual_out, y, post_weight, gate, pre_weight, *(y_mx4 or ()))
-    return Bound(load().fc_block_norm, args, 9, keep=(*keep, spec), device=_one_device(*keep))
+    return DeviceBound(load().fc_block_norm, args, 9, keep=(*keep, spec), device=_one_device(*keep))
 
 
 def block_norm(x: torch.Tensor, residual_in: Optional[torch.Tensor], residual_out: torch.Tensor,
@@ -626,7 +645,7 @@ def bind_block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor],
                              pre_weight: Optional[torch.Tensor] = None,
                              residual_scale: float = 1.0, block_scale: float = 1.0,
                              post_eps: float = 1e-5, pre_eps: float = 1e-5,
-                             d_status: Optional[torch.Tensor] = None) -> Bound:
+                             d_status: Optional[torch.Tensor] = None) -> DeviceBound:
     rows, hidden = _rows_hidden(x)
     spec = _block_norm_spec(x, post_weight, gate, pre_weight, residual_scale, block_scale, post_eps,
                             pre_eps)
@@ -645,7 +664,7 @@ def bind_block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor],
             P(_want(d_status, (2,), torch.int32, "d_status")), None]
     keep = (x, h, dy, dh, dx, workspace, dresidual, dpost_weight, dgate, dpre_weight, post_weight,
             gate, pre_weight, d_status)
-    return Bound(load().fc_block_norm_backward, args, 11, keep=(*keep, spec, grads),
+    return DeviceBound(load().fc_block_norm_backward, args, 11, keep=(*keep, spec, grads),
                  device=_one_device(*keep))
 
 

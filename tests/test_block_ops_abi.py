@@ -171,3 +171,23 @@ def test_binding_checks_shapes_and_types():
         fc.alloc_mx4(4, 48, device="cpu")
     with pytest.raises(ValueError, match="one device"):
         fc._one_device(x, torch.zeros(1, device="meta"))
+
+
+def test_device_bound_call_passes_exact_arguments(monkeypatch):
+    """A device-bound call hands the entry point the values it was bound to, in its
+    own types, on the stream asked for or the device's current one."""
+    seen = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d, raising=False)
+    L = fc.load()
+    q = fc.Mx4(A[1], A[2])
+    b = fc.DeviceBound(L.fc_mx4_quantize, [A[0], BF16, 0, 1 << 33, q, None], 5, keep=(), device=0)
+    assert b._fn.argtypes is None and b._fn(*b._args) == fc.FC_ERR_UNSUPPORTED  # hidden 2^33 arrives whole
+    b._fn = lambda *a: seen.append([v.value if hasattr(v, "value") else v for v in a]) or 0
+    for stream in (None, 5, None, 5):
+        b(stream)
+    assert [a[5] for a in seen] == [70, 5, 70, 5]
+    assert all(a[:4] == [A[0], BF16, 0, 1 << 33] and a[4] is q for a in seen)
+    b._fn = lambda *a: fc.FC_ERR_INVALID
+    with pytest.raises(fc.FcommError):
+        b()
