@@ -9,8 +9,14 @@
 //
 // Bound by memory: x and r in, h and y out.  One CTA holds one row in
 // registers (32 neighbouring bytes a thread, so a warp's loads and stores
-// cover 1 KB), and each row is read once.  Rows that fit one warp take one each.  The quantised y (mx4.cuh) leaves from the registers that
-// hold it.
+// cover 1 KB), and each row is read once.  Rows that fit one warp take one each.
+// The weights come where they are used, from L1: fewer registers, more rows in
+// flight, which is what a row's two sums are hidden behind.  The quantised y
+// (mx4.cuh) leaves from the registers that hold it.  Measured on GB300: 8192 x
+// 8192 bf16, both norms and a gate, 88.2 us, 6.09 TB/s (0.90 of the measured copy
+// rate; 99.5 us with the weights loaded first and two CTAs an SM); 1037 x 5120
+// fp32 with a gate for every row 16.6 us, 6.4 TB/s; one row of 4096 1.9 us in a
+// graph.
 #include "block.h"
 #include "mx4.cuh"
 

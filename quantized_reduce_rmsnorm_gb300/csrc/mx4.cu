@@ -4,7 +4,9 @@
 // Bound by memory: 2 (bf16) or 4 bytes read and 0.53 written per element, and
 // the reverse.  A lane takes 16 elements (one or two 256-bit loads, 8 bytes of
 // codes); eight lanes make one word of four scales, so every scale is written
-// once, in words, with the bytes past a row's end set to 0.
+// once, in words, with the bytes past a row's end set to 0.  Measured on GB300, 8192
+// x 8192 bf16: to four bits 28.9 us (5.9 TB/s, 0.87 of the measured copy rate; 33.2
+// with one load in flight and 64-bit indexes), back 26.3 us (6.5 TB/s, 0.95).
 #include "block.h"
 #include "mx4.cuh"
 
