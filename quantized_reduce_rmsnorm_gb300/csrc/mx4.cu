@@ -5,19 +5,18 @@
 // the reverse.  A lane takes 16 elements (one or two 256-bit loads, 8 bytes of
 // codes); eight lanes make one word of four scales, so every scale is written
 // once, in words, with the bytes past a row's end set to 0.  Measured on GB300, 8192
-// x 8192 bf16: to four bits 28.9 us (5.9 TB/s, 0.87 of the measured copy rate; 33.2
-// with one load in flight and 64-bit indexes), back 26.3 us (6.5 TB/s, 0.95).
+// x 8192 bf16: to four bits 26.3 us (6.5 TB/s, 0.95 of the measured copy rate; with
+// one load in flight 34.2), back 26.4 us; 8192 x 8192 fp32 43.8 and 44.8 us.
 #include "block.h"
 #include "mx4.cuh"
 
 namespace fc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWords = kThreads / 8;  // scale words of a CTA's turn
-constexpr int kTurns = 2;             // turns whose loads are in flight together
 
-template <bool F32>
+template <bool F32, int kTurns>  // turns whose loads are in flight together
 __global__ void __launch_bounds__(kThreads)
     k_mx4_quantize(const void* x, uint32_t words, int H, uint32_t KT, uint8_t* codes, uint8_t* scales) {
   pdl_begin();
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <bool F32>
+template <bool F32, int kTurns>  // turns whose loads are in flight together
 __global__ void __launch_bounds__(kThreads)
     k_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, uint32_t words, int H, uint32_t KT, void* out) {
   pdl_begin();
@@ -83,7 +82,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-dim3 grid_for(int64_t words) { return dim3(static_cast<unsigned>((words + kWords * kTurns - 1) / (kWords * kTurns))); }
+template <int kTurns>
+dim3 grid_for(uint32_t words) {
+  return dim3((words + kWords * kTurns - 1) / (kWords * kTurns));
+}
+// Three turns a lane where there are CTAs enough, one where more of them start
+// sooner (us, one / three turns, bf16 to four bits: 512 x 8192 2.9 / 3.3, 1024 x 8192
+// 4.9 / 3.9, 8192 x 8192 34.2 / 26.4).  Reading back to fp32 writes eight bytes for
+// each it reads: one turn (1024 x 8192 6.0 / 7.7, 8192 x 8192 44.8 / 45.7).
+bool many(uint32_t words) { return words >= 3u << 14; }
 
 }  // namespace
 
@@ -92,10 +99,11 @@ cudaError_t launch_mx4_quantize(bool f32, const void* x, int64_t rows, int H, vo
   const uint32_t KT = static_cast<uint32_t>(mx4_tiles_k(H));
   const uint32_t words = static_cast<uint32_t>(rows * KT);  // below 2^31: the caller's check
   auto* c = static_cast<uint8_t*>(codes);
-  return f32 ? launch_pdl(k_mx4_quantize<true>, grid_for(words), dim3(kThreads), 0, st, x, words, H,
-                          KT, c, scales)
-             : launch_pdl(k_mx4_quantize<false>, grid_for(words), dim3(kThreads), 0, st, x, words, H,
-                          KT, c, scales);
+  if (many(words))
+    return launch_pdl(f32 ? k_mx4_quantize<true, 3> : k_mx4_quantize<false, 3>, grid_for<3>(words), dim3(kThreads), 0,
+                      st, x, words, H, KT, c, scales);
+  return launch_pdl(f32 ? k_mx4_quantize<true, 1> : k_mx4_quantize<false, 1>, grid_for<1>(words), dim3(kThreads), 0,
+                    st, x, words, H, KT, c, scales);
 }
 
 cudaError_t launch_mx4_dequantize(bool f32, const void* codes, const uint8_t* scales, int64_t rows,
@@ -103,10 +111,11 @@ cudaError_t launch_mx4_dequantize(bool f32, const void* codes, const uint8_t* sc
   const uint32_t KT = static_cast<uint32_t>(mx4_tiles_k(H));
   const uint32_t words = static_cast<uint32_t>(rows * KT);  // below 2^31: the caller's check
   auto* c = static_cast<const uint8_t*>(codes);
-  return f32 ? launch_pdl(k_mx4_dequantize<true>, grid_for(words), dim3(kThreads), 0, st, c, scales,
-                          words, H, KT, out)
-             : launch_pdl(k_mx4_dequantize<false>, grid_for(words), dim3(kThreads), 0, st, c, scales,
-                          words, H, KT, out);
+  if (f32)
+    return launch_pdl(k_mx4_dequantize<true, 1>, grid_for<1>(words), dim3(kThreads), 0, st, c, scales, words, H, KT, out);
+  if (many(words))
+    return launch_pdl(k_mx4_dequantize<false, 3>, grid_for<3>(words), dim3(kThreads), 0, st, c, scales, words, H, KT, out);
+  return launch_pdl(k_mx4_dequantize<false, 1>, grid_for<1>(words), dim3(kThreads), 0, st, c, scales, words, H, KT, out);
 }
 
 }  // namespace fc
