@@ -26,10 +26,11 @@ struct BlockNormArgs {
   int64_t rows;
   int64_t gate_seg;     // neighbouring rows that share one row of gate
   int H;
+  int ahead;            // set at the launch
   float alpha, beta;    // residual scale, block scale
   float eps_post, eps_pre;
 };
-cudaError_t launch_block_norm(bool f32, const BlockNormArgs& a, cudaStream_t st);
+cudaError_t launch_block_norm(bool f32, BlockNormArgs a, cudaStream_t st);
 
 // CTAs of the gradient kernel at most (152 SMs, up to 4 on each); its
 // workspace is sized by this and not by the device, so that a caller can ask

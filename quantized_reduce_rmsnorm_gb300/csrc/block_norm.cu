@@ -11,12 +11,12 @@
 // registers (32 neighbouring bytes a thread, so a warp's loads and stores
 // cover 1 KB), and each row is read once.  Rows that fit one warp take one each.
 // The weights come where they are used, from L1: fewer registers, more rows in
-// flight, which is what a row's two sums are hidden behind.  The quantised y
-// (mx4.cuh) leaves from the registers that hold it.  Measured on GB300: 8192 x
-// 8192 bf16, both norms and a gate, 88.2 us, 6.09 TB/s (0.90 of the measured copy
-// rate; 99.5 us with the weights loaded first and two CTAs an SM); 1037 x 5120
-// fp32 with a gate for every row 16.6 us, 6.4 TB/s; one row of 4096 1.9 us in a
-// graph.
+// flight, which is what a row's two sums are hidden behind; and rows start for L2
+// before a CTA takes them.  The quantised y (mx4.cuh) leaves from the registers that
+// hold it.  Measured on GB300: 8192 x 8192 bf16, both norms and a gate, 85.0 us, 6.3
+// TB/s (0.93 of the measured copy rate; without rows sent for 90.7, with 304 rows
+// ahead 86.4, with 456 86.9, and with the weights loaded first and two CTAs an SM
+// 99.5); 4096 x 8192 fp32 88.6 us (102.6 without); one row of 4096 1.9 us in a graph.
 #include "block.h"
 #include "mx4.cuh"
 
@@ -47,6 +47,15 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const BlockNormArgs a
   const bool live = e < a.H;
   const int64_t at = static_cast<int64_t>(row) * a.H + e;
   const float inv_n = 1.0f / static_cast<float>(a.H);
+  // The row that the CTAs of the next turn or so will take starts on its way to L2
+  // (`ahead` rows on, the SMs' number; whole rows are multiples of 32 bytes).
+  if (!TEAM && threadIdx.x == 0 && row + a.ahead < a.rows) {
+    const uint32_t bytes = a.H * (F32 ? 4 : 2);
+    const int64_t off = static_cast<int64_t>(row + a.ahead) * bytes;
+    prefetch_l2(static_cast<const char*>(a.x) + off, bytes);
+    if (a.res_in) prefetch_l2(static_cast<const char*>(a.res_in) + off, bytes);
+    if (a.gate && a.gate_seg == 1) prefetch_l2(static_cast<const char*>(a.gate) + off, bytes);
+  }
   Raw<F32, W> xr, rr, gr;
   if (live) {
     xr = load_raw<F32, W>(a.x, at);
@@ -115,6 +124,19 @@ cudaError_t launch_rows(const BlockNormArgs& a, cudaStream_t st) {
   return launch_pdl(k_block_norm<F32, W, false, MAXT, MINB>, dim3(static_cast<unsigned>(a.rows)),
                     dim3(static_cast<unsigned>((a.H / W + 31) / 32 * 32)), 0, st, a);
 }
+// Turns of the whole GPU that the rows take.
+template <bool F32, int W, int MAXT, int MINB>
+int64_t turns(const BlockNormArgs& a) {
+  auto* kern = k_block_norm<F32, W, false, MAXT, MINB>;
+  const int threads = (a.H / W + 31) / 32 * 32;
+  const int occ = occupancy_memo(reinterpret_cast<const void*>(kern), threads, 0, 1, [&] {
+    int v = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, 0);
+    return v;
+  });
+  const int64_t slots = static_cast<int64_t>(num_sms()) * (occ > 0 ? occ : 1);
+  return (a.rows + slots - 1) / slots;
+}
 template <bool F32, int W>
 cudaError_t launch_teams(const BlockNormArgs& a, cudaStream_t st) {
   return launch_pdl(k_block_norm<F32, W, true, 128, 1>, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st,
@@ -123,15 +145,17 @@ cudaError_t launch_teams(const BlockNormArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_block_norm(bool f32, const BlockNormArgs& a, cudaStream_t st) {
-  // Registers for three CTAs of 512 threads an SM spill a little: worth it where
-  // rows come in waves (8192 x 8192: 88.2 us, with two 93.4), not for a few (64 x
-  // 8192: 3.6 us against 3.1).  fp32 rows: two CTAs of 640 threads (1037 x 5120:
-  // 16.6 us, with one 22.0, with three 21.0).
+cudaError_t launch_block_norm(bool f32, BlockNormArgs a, cudaStream_t st) {
+  a.ahead = num_sms();
+  // Registers for three CTAs of 512 threads an SM spill a little: they are taken where
+  // the rows then go in fewer turns of the whole GPU (us, three / two CTAs, rows of
+  // 8192: 300 7.2 / 6.1, 456 8.4 / 10.4, 600 12.1 / 11.4, 8192 88.2 / 93.4).  fp32 rows:
+  // two CTAs of 640 threads (1037 x 5120: 16.6 us, with one 22.0, with three 21.0).
   if (!f32) {
     if (a.H <= 512) return launch_teams<false, 16>(a, st);
     if (a.H > 8192) return launch_rows<false, 16, 1024, 1>(a, st);
-    return a.rows > 4 * num_sms() ? launch_rows<false, 16, 512, 3>(a, st) : launch_rows<false, 16, 512, 2>(a, st);
+    return turns<false, 16, 512, 3>(a) < turns<false, 16, 512, 2>(a) ? launch_rows<false, 16, 512, 3>(a, st)
+                                                                     : launch_rows<false, 16, 512, 2>(a, st);
   }
   if (a.H <= 256) return launch_teams<true, 8>(a, st);
   if (a.H <= 5120) return launch_rows<true, 8, 640, 2>(a, st);
