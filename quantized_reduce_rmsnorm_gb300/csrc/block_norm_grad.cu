@@ -12,9 +12,9 @@
 //
 // Bound by memory: four rows in, two out.  The sums over rows stay on chip:
 // a CTA takes one run of neighbouring rows (within one gate row's rows) and
-// adds its columns up in shared memory, each thread its own 16 columns, so
-// there is no atomic and the order of every sum is fixed.  A CTA writes its sums
-// once, to the workspace, and a second kernel adds the CTAs' sums in order.
+// adds its columns up in registers, each thread its own, so there is no atomic
+// and the order of every sum is fixed.  A CTA writes its sums once, to the
+// workspace, and a second kernel adds the CTAs' sums in order.
 // Measured on GB300, 8192 x 5120 bf16 with everything asked for: 84.9 us, 5.9 TB/s
 // (0.88 of the measured copy rate), of which the second kernel is about 4; rows
 // straight to registers with two barriers a row took 233.
@@ -27,47 +27,6 @@ namespace fc {
 namespace {
 
 constexpr int kErrCuda = 2;  // FC_ERR_CUDA
-
-// Sums over the row's threads of N values at once; red: N * 32 floats.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* red) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  const int n = blockDim.x >> 5, l = threadIdx.x & 31;
-  if (l == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 32 + (threadIdx.x >> 5)] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(l < n ? red[i * 32 + l] : 0.0f);
-}
-
-// A thread's 16 running column sums of one kind, in shared memory as four
-// planes of float4 (lanes 16 bytes apart: no bank conflict).
-__device__ __forceinline__ void acc_add(float4* acc, const float v[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float4 s = acc[j * blockDim.x + threadIdx.x];
-    s.x += v[4 * j], s.y += v[4 * j + 1], s.z += v[4 * j + 2], s.w += v[4 * j + 3];
-    acc[j * blockDim.x + threadIdx.x] = s;
-  }
-}
-__device__ __forceinline__ void acc_take(float4* acc, float v[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 s = acc[j * blockDim.x + threadIdx.x];
-    v[4 * j] = s.x, v[4 * j + 1] = s.y, v[4 * j + 2] = s.z, v[4 * j + 3] = s.w;
-    acc[j * blockDim.x + threadIdx.x] = make_float4(0, 0, 0, 0);
-  }
-}
-
-template <bool F32>
-__device__ __forceinline__ void store16(void* base, int64_t elem, const float v[16]) {
-  float2 p[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = make_float2(v[2 * i], v[2 * i + 1]);
-  store_raw<F32, 16>(base, elem, pack_raw<F32, 16>(p));
-}
 
 // How the rows are cut: `segs` runs of seg_rows rows that share a gate row,
 // each into `cuts` pieces; piece i of the segs * cuts is CTA i, i + grid, ...
@@ -87,132 +46,8 @@ struct GradJob {
   float* ws_gate;     // [segs * cuts, H]
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(1024) k_block_norm_grad(const GradJob job) {
-  extern __shared__ float4 acc[];
-  // a row's three sums and one more, each its own floats; neighbouring rows take
-  // turns, so a row's first barrier frees what the row before it read
-  __shared__ float red[2][4 * 32];
-  int turn = 0;
-  const BlockNormGradArgs& a = job.a;
-  const GradPlan& p = job.p;
-  pdl_begin();
-  const int e = threadIdx.x * 16;
-  const bool live = e < a.H;
-  const bool w_pre = a.dpre_w != nullptr, w_post = a.dpost_w != nullptr;
-  const bool g_sum = a.dgate != nullptr && !p.gate_direct;
-  float4* acc_pre = acc;
-  float4* acc_post = acc + 4 * blockDim.x;
-  float4* acc_gate = acc + 8 * blockDim.x;
-#pragma unroll
-  for (int j = 0; j < 12; ++j) acc[j * blockDim.x + threadIdx.x] = make_float4(0, 0, 0, 0);
-  const float inv_n = 1.0f / static_cast<float>(a.H);
-  float w1[16], w2[16];
-  {
-    Raw<F32, 16> r{};
-    if (live && a.post_w) r = load_weight<F32, 16>(a.post_w, e);
-    unpack_raw<F32, 16>(r, w1);
-    if (live && a.pre_w) r = load_weight<F32, 16>(a.pre_w, e);
-    unpack_raw<F32, 16>(r, w2);
-  }
-  for (int64_t piece = blockIdx.x; piece < p.segs * p.cuts; piece += gridDim.x) {
-    const int64_t seg = piece / p.cuts, cut = piece - seg * p.cuts;
-    const int64_t r0 = seg * p.seg_rows + cut * p.cut_rows + min(static_cast<int>(cut), p.cut_more);
-    const int64_t r1 = r0 + p.cut_rows + (cut < p.cut_more);
-    for (int64_t row = r0; row < r1; ++row) {
-      const int64_t at = row * a.H + e;
-      float x[16] = {}, h[16] = {}, dy[16] = {}, dh[16] = {}, g[16];
-      if (live) {
-        unpack_raw<F32, 16>(load_raw<F32, 16>(a.x, at), x);
-        if (a.dy) {
-          unpack_raw<F32, 16>(load_raw<F32, 16>(a.h, at), h);
-          unpack_raw<F32, 16>(load_raw<F32, 16>(a.dy, at), dy);
-        }
-        if (a.dh) unpack_raw<F32, 16>(load_raw<F32, 16>(a.dh, at), dh);
-        if (a.gate)
-          unpack_raw<F32, 16>(load_weight<F32, 16>(a.gate, (p.gate_direct ? row : seg) * a.H + e), g);
-      }
-      float s[3] = {0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[0] = __fmaf_rn(h[i], h[i], s[0]);
-        s[1] = __fmaf_rn(dy[i] * w2[i], h[i], s[1]);
-        s[2] = __fmaf_rn(x[i], x[i], s[2]);
-      }
-      turn ^= 1;
-      row_sums<3>(s, red[turn]);
-      if (a.dy) {
-        const float inv = __frsqrt_rn(__fadd_rn(s[0] * inv_n, a.eps_pre));
-        const float c = inv * inv * s[1] * inv_n;  // mean(dn * hh) * inv_h
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float hh = h[i] * inv;
-          dh[i] += __fmaf_rn(inv, dy[i] * w2[i], -(hh * c));
-          t[i] = dy[i] * hh;
-        }
-        if (w_pre) acc_add(acc_pre, t);
-      }
-      if (live && a.dres) {
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = a.alpha * dh[i];
-        store16<F32>(a.dres, at, t);
-      }
-      const float inv_x = a.post_w ? __frsqrt_rn(__fadd_rn(s[2] * inv_n, a.eps_post)) : 1.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        dh[i] *= a.beta;  // now the gradient of gate * u
-        x[i] *= inv_x;    // now xh (x where there is no norm)
-      }
-      if (a.gate) {
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = dh[i] * (a.post_w ? x[i] * w1[i] : x[i]);
-        if (g_sum) acc_add(acc_gate, t);
-        if (live && a.dgate && p.gate_direct) store16<F32>(a.dgate, at, t);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dh[i] = live ? dh[i] * g[i] : 0.0f;  // now du
-      }
-      if (a.post_w) {
-        float t[16], q[1] = {0};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = dh[i] * x[i];
-        if (w_post) acc_add(acc_post, t);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) q[0] = __fmaf_rn(t[i], w1[i], q[0]);
-        row_sums<1>(q, red[turn] + 96);
-        const float c = q[0] * inv_n;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dh[i] = inv_x * __fmaf_rn(dh[i], w1[i], -(x[i] * c));
-      }
-      if (live) store16<F32>(a.dx, at, dh);
-    }
-    if (g_sum) {
-      float t[16];
-      acc_take(acc_gate, t);
-      if (live) {
-        if (p.gate_final)
-          store16<F32>(a.dgate, seg * a.H + e, t);
-        else
-          store16<true>(job.ws_gate, piece * a.H + e, t);
-      }
-    }
-  }
-  float t[16];
-  if (w_pre) {
-    acc_take(acc_pre, t);
-    if (live) store16<true>(job.ws_pre, static_cast<int64_t>(blockIdx.x) * a.H + e, t);
-  }
-  if (w_post) {
-    acc_take(acc_post, t);
-    if (live) store16<true>(job.ws_post, static_cast<int64_t>(blockIdx.x) * a.H + e, t);
-  }
-}
-
-// ------------------------------------------------------ staged rows -----
-// The same gradient with the rows staged in shared memory by bulk copies, and
-// all of a row's sums taken at once.  With a = dy * pre_weight, gw = beta * gate *
+// The rows are staged in shared memory by bulk copies, a few rows ahead, and all of
+// a row's sums are taken at once.  With a = dy * pre_weight, gw = beta * gate *
 // post_weight (one factor a column) and k = inv_h^3 * mean(a * h):
 //   dh' = dh + inv_h * a - k * h
 //   sum(e * x) = sum gw x dh + inv_h * sum gw x a - k * sum gw x h
@@ -223,7 +58,9 @@ __global__ void __launch_bounds__(1024) k_block_norm_grad(const GradJob job) {
 // beta * post_weight * r and, for a gate that the piece's rows share,
 // dpost_weight = beta * gate * r: one running sum serves both.  It and
 // dpre_weight's are in registers.  A thread has W columns, in groups of 16
-// bytes, the live threads side by side: no bank conflicts.
+// bytes, the live threads side by side: no bank conflicts.  Rows too wide for one
+// CTA's registers are cut over the CTAs of a cluster, which exchange each row's
+// sums through distributed shared memory.
 template <bool F32, int W>
 struct Cols {
   static constexpr int kPer = F32 ? 4 : 8;  // columns of a group
@@ -279,14 +116,22 @@ __device__ __forceinline__ void store_sums(float* row, int t, int live, const fl
   }
 }
 
-// Sums of eight values over the CTA, each thread ending with all eight.  Within a
-// warp the values are folded onto one another (lanes give away the half that
-// the other lanes keep), so that eight sums take 9 shuffles and not 40; lane l
-// ends with value l / 4.  red: 8 rows of kRedStride floats (an odd number of
-// 16-byte groups apart: no bank conflicts), one for each warp, those past the
-// CTA's warps 0.
-constexpr int kRedStride = 36;
+// Sums of eight values over the CTA, or the CL CTAs of the cluster, each thread
+// ending with all eight, in the same order everywhere.  Within a warp the values are
+// folded onto one another (lanes give away the half that the other lanes keep), so
+// that eight sums take 9 shuffles and not 40; lane l ends with value l / 4.
+// red: 8 rows of Red<CL>::kStride floats (an odd number of 16-byte groups: no bank
+// conflicts), one for each warp of each CTA, those past them 0.
+__device__ __forceinline__ void st_cluster(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+template <int CL>
+struct Red {
+  static constexpr int kEntries = CL == 1 ? 32 : 64, kStride = kEntries + 4;
+};
+template <int CL>
 __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
+  using R = Red<CL>;
   const int l = threadIdx.x & 31;
 #pragma unroll
   for (int m = 16, n = 4; m >= 4; m >>= 1, n >>= 1)
@@ -299,12 +144,26 @@ __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
   float s = v[0];
   s += __shfl_xor_sync(kFull, s, 2);
   s += __shfl_xor_sync(kFull, s, 1);
-  float* mine = red + (l >> 2) * kRedStride;
-  if ((l & 3) == 0) mine[threadIdx.x >> 5] = s;
-  __syncthreads();
-  const float4 a = *reinterpret_cast<const float4*>(mine + (l & 3) * 8);
-  const float4 b = *reinterpret_cast<const float4*>(mine + (l & 3) * 8 + 4);
-  s = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  float* mine = red + (l >> 2) * R::kStride;
+  const int warp = threadIdx.x >> 5;
+  if constexpr (CL == 1) {
+    if ((l & 3) == 0) mine[warp] = s;
+    __syncthreads();
+  } else {
+    // a value's four lanes each tell one CTA of the cluster (its rank is the block's)
+    const int at = static_cast<int>(blockIdx.x % CL) * (blockDim.x >> 5) + warp;
+    if ((l & 3) < CL) st_cluster(cluster_addr(mine + at, l & 3), s);
+    __syncwarp();
+    cluster_sync_all();
+  }
+  const float* part = mine + (l & 3) * (R::kEntries / 4);
+#pragma unroll
+  for (int k = 0; k < R::kEntries / 32; ++k) {
+    const float4 a = *reinterpret_cast<const float4*>(part + 8 * k);
+    const float4 b = *reinterpret_cast<const float4*>(part + 8 * k + 4);
+    const float sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+    s = k == 0 ? sum : s + sum;
+  }
   s += __shfl_xor_sync(kFull, s, 2);
   s += __shfl_xor_sync(kFull, s, 1);
 #pragma unroll
@@ -313,19 +172,25 @@ __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
 
 constexpr int kMostStages = 4;
 
-// TOKEN: a gate row for every row, staged with the row.
-template <bool F32, bool TOKEN, int W, int MAXT, int MINB>
+// TOKEN: a gate row for every row, staged with the row.  CL: CTAs of a cluster, a
+// team, that share a row's columns.
+template <bool F32, bool TOKEN, int W, int CL, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const GradJob job, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(16) float red[2][8 * kRedStride];  // neighbouring rows take turns
+  __shared__ __align__(16) float red[2][8 * Red<CL>::kStride];  // neighbouring rows take turns
   __shared__ uint64_t full[kMostStages];
-  __shared__ volatile int late[2];  // a copy did not land in time, by turns as red
+  __shared__ volatile uint32_t late[2];  // not 0: a copy did not land in time, by turns as red
   __shared__ struct { int piece, row, end, stage, count; } next;
   constexpr int es = F32 ? 4 : 2, kP = W / 2;
   const BlockNormGradArgs& a = job.a;
   const GradPlan& p = job.p;
-  const int t = threadIdx.x, live = a.H / W;
-  const int H = a.H, row_bytes = H * es;
+  const int t = threadIdx.x, H = a.H;
+  // this CTA's columns: runs of 16, shared out over the team
+  const int team = blockIdx.x / CL, teams = gridDim.x / CL, rank = blockIdx.x % CL;
+  const int col0 = CL == 1 ? 0 : H / 16 * rank / CL * 16;
+  const int cols = CL == 1 ? H : H / 16 * (rank + 1) / CL * 16 - col0;
+  const int live = cols / W, row_bytes = cols * es;          // of this CTA
+  const int stride = H * es, shift = CL == 1 ? 0 : col0 * es;  // of a row in memory
   const bool on = t < live;
   const bool pre = a.dy != nullptr, post = a.post_w != nullptr;
   // slots of a stage: x, h, dy, dh, gate row; absent tensors take none
@@ -337,9 +202,13 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
     late[0] = late[1] = 0;
     mbar_init_fence();
   }
-  for (int i = t; i < 2 * 8 * kRedStride; i += blockDim.x) red[0][i] = 0.0f;
+  for (int i = t; i < 2 * 8 * Red<CL>::kStride; i += blockDim.x) red[0][i] = 0.0f;
   for (int j = 0; j < W / 4; ++j) acc_post[j * blockDim.x + t] = make_float4(0, 0, 0, 0);
-  __syncthreads();
+  __syncwarp();
+  if constexpr (CL == 1)
+    __syncthreads();
+  else
+    cluster_sync_all();
   pdl_begin();
 
   const int pieces = static_cast<int>(p.segs) * p.cuts;  // at most the rows
@@ -354,7 +223,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   {
     int k = 0;
     auto slot = [&](bool there, const void* base) {
-      if (there && t == k++) from = static_cast<const char*>(base);
+      if (there && t == k++) from = static_cast<const char*>(base) + shift;
     };
     slot(true, a.x), slot(pre, a.h), slot(pre, a.dy), slot(a.dh != nullptr, a.dh), slot(TOKEN, a.gate);
   }
@@ -369,17 +238,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       next.stage = st + 1 == stages ? 0 : st + 1;
       next.row = row + 1;
       if (row + 1 == next.end) {
-        next.piece = piece + gridDim.x;
+        next.piece = piece + teams;
         if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
       }
     }
     __syncwarp();
     if (t < slots)
-      bulk_load(ring + (st * slots + t) * row_bytes, from + static_cast<int64_t>(row) * row_bytes, row_bytes, full + st);
+      bulk_load(ring + (st * slots + t) * row_bytes, from + static_cast<int64_t>(row) * stride, row_bytes, full + st);
   };
   if (t < 32) {
     if (t == 0) {
-      next.piece = blockIdx.x;
+      next.piece = team;
       next.count = next.stage = 0;
       if (next.piece < pieces) piece_rows(next.piece, next.row, next.end);
     }
@@ -391,20 +260,20 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   const float2 zero = make_float2(0.0f, 0.0f);
   float2 gw[kP], acc_pre[kP], acc_r[kP];
   RawCols<F32, W> w2{};
-  if (on && a.pre_w) w2 = load_cols<F32, W>(a.pre_w, t, live);
+  if (on && a.pre_w) w2 = load_cols<F32, W>(static_cast<const char*>(a.pre_w) + shift, t, live);
 #pragma unroll
   for (int i = 0; i < kP; ++i) acc_pre[i] = acc_r[i] = zero;
   int count = 0, s = 0;  // rows done; the row's stage
   uint32_t phase = 0;
   bool stop = false;
-  for (int piece = blockIdx.x; piece < pieces && !stop; piece += gridDim.x) {
+  for (int piece = team; piece < pieces && !stop; piece += teams) {
     int r0, r1;
     piece_rows(piece, r0, r1);
-    const int64_t seg_off = static_cast<int64_t>(piece / p.cuts) * row_bytes;  // its gate row
+    const int64_t seg_off = static_cast<int64_t>(piece / p.cuts) * stride + shift;  // its gate row
 #pragma unroll
     for (int i = 0; i < kP; ++i) gw[i] = dup2(a.beta);
     if (on && post) {
-      const RawCols<F32, W> w = load_cols<F32, W>(a.post_w, t, live);
+      const RawCols<F32, W> w = load_cols<F32, W>(static_cast<const char*>(a.post_w) + shift, t, live);
 #pragma unroll
       for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32, W>(w, i));
     }
@@ -414,9 +283,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       for (int i = 0; i < kP; ++i) gw[i] = pmul(gw[i], pair<F32, W>(w, i));
     }
     for (int row = r0; row < r1; ++row, ++count) {
-      const int64_t off = static_cast<int64_t>(row) * row_bytes;
+      const int64_t off = static_cast<int64_t>(row) * stride + shift;
       const uint8_t* src = ring + s * slots * row_bytes;
-      if (!mbar_wait_bounded(full + s, phase)) late[count & 1] = 1;
+      if (!mbar_wait_bounded(full + s, phase)) {
+        if constexpr (CL == 1)
+          late[count & 1] = 1;
+        else
+          for (int c = 0; c < CL; ++c) st_cluster(cluster_addr(const_cast<const uint32_t*>(late + (count & 1)), c), 1.0f);
+      }
       RawCols<F32, W> x, h{}, dy{}, dh{}, g;
       float r[8] = {};
       if (on) {
@@ -441,7 +315,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
         r[0] = s0.x + s0.y, r[1] = s1.x + s1.y, r[2] = s2.x + s2.y;
         r[3] = s3.x + s3.y, r[4] = s4.x + s4.y, r[5] = s5.x + s5.y;
       }
-      row_sums8(r, red[count & 1]);
+      row_sums8<CL>(r, red[count & 1]);
       if (late[count & 1]) {  // set before this row's barrier only, so all read the same
         stop = true;
         break;
@@ -491,14 +365,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
 #pragma unroll
         for (int i = 0; i < kP; ++i) o[i] = pmul(acc_r[i], dup2(a.beta));
         if (post) {
-          const RawCols<F32, W> w = load_cols<F32, W>(a.post_w, t, live);
+          const RawCols<F32, W> w = load_cols<F32, W>(static_cast<const char*>(a.post_w) + shift, t, live);
 #pragma unroll
           for (int i = 0; i < kP; ++i) o[i] = pmul(o[i], pair<F32, W>(w, i));
         }
         if (p.gate_final)
           store_cols<F32, W>(static_cast<char*>(a.dgate) + seg_off, t, live, o);
         else
-          store_sums<F32, W>(job.ws_gate + static_cast<int64_t>(piece) * H, t, live, o);
+          store_sums<F32, W>(job.ws_gate + static_cast<int64_t>(piece) * H + col0, t, live, o);
       }
       if (a.dpost_w) {
 #pragma unroll
@@ -520,7 +394,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
     }
   }
   if (on && !stop) {
-    if (a.dpre_w) store_sums<F32, W>(job.ws_pre + static_cast<int64_t>(blockIdx.x) * H, t, live, acc_pre);
+    if (a.dpre_w) store_sums<F32, W>(job.ws_pre + static_cast<int64_t>(team) * H + col0, t, live, acc_pre);
     if (a.dpost_w) {
       float2 o[kP];
 #pragma unroll
@@ -528,12 +402,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
         const float4 x = acc_post[j * blockDim.x + t];
         o[2 * j] = make_float2(x.x, x.y), o[2 * j + 1] = make_float2(x.z, x.w);
       }
-      store_sums<F32, W>(job.ws_post + static_cast<int64_t>(blockIdx.x) * H, t, live, o);
+      store_sums<F32, W>(job.ws_post + static_cast<int64_t>(team) * H + col0, t, live, o);
     }
   }
   if (stop && t == 0) {  // a copy never landed: say so, and let those in flight land
     if (a.status) *a.status = kErrCuda;
     for (int i = count; i < next.count; ++i) mbar_wait_bounded(full + i % stages, (i / stages) & 1);
+  }
+  if constexpr (CL > 1) {  // no CTA's memory goes while another may write to it
+    __syncwarp();
+    cluster_sync_all();
   }
 }
 
@@ -597,35 +475,40 @@ void plan(GradJob& job, int64_t most) {
   job.ws_gate = a.dgate && !p.gate_direct && !p.gate_final ? a.ws + 2 * static_cast<int64_t>(p.grid) * a.H : nullptr;
 }
 
-// CTAs that the GPU holds at once, 0 if none fits.
-template <class K>
-int64_t resident(K* kern, int threads, int smem) {
-  if (raise_smem_limit(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return 0;
-  const int occ = occupancy_memo(reinterpret_cast<const void*>(kern), threads, smem, 1, [&] {
+template <bool F32, bool TOKEN, int W, int CL, int MAXT, int MINB>
+cudaError_t launch_staged(GradJob& job, int threads, int stages, int smem, cudaStream_t st) {
+  auto* kern = k_block_norm_grad_staged<F32, TOKEN, W, CL, MAXT, MINB>;
+  const void* fn = reinterpret_cast<const void*>(kern);
+  if (cudaError_t e = raise_smem_limit(fn, smem)) return e;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CL;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = CL == 1 ? 1 : 2;
+  // teams that the GPU holds at once
+  const int held = occupancy_memo(fn, threads, smem, CL, [&] {
     int v = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem);
+    if (CL == 1) {
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem);
+      return v * num_sms();
+    }
+    cfg.attrs = at + 1, cfg.numAttrs = 1;
+    cudaOccupancyMaxActiveClusters(&v, kern, &cfg);
+    cfg.attrs = at, cfg.numAttrs = 2;
     return v;
   });
-  return std::min<int64_t>(kNormGradMaxCtas, static_cast<int64_t>(num_sms()) * occ);
-}
-
-template <bool F32>
-cudaError_t launch_direct(GradJob& job, int threads, cudaStream_t st) {
-  auto* kern = k_block_norm_grad<F32>;
-  const int smem = threads * 12 * static_cast<int>(sizeof(float4));
-  const int64_t most = resident(kern, threads, smem);
-  if (most < 1) return cudaErrorInvalidConfiguration;
-  plan(job, most);
-  return launch_pdl(kern, dim3(job.p.grid), dim3(threads), smem, st, job);
-}
-
-template <bool F32, bool TOKEN, int W, int MAXT, int MINB>
-cudaError_t launch_staged(GradJob& job, int threads, int stages, int smem, cudaStream_t st) {
-  auto* kern = k_block_norm_grad_staged<F32, TOKEN, W, MAXT, MINB>;
-  const int64_t most = resident(kern, threads, smem);
-  if (most < 1) return cudaErrorInvalidConfiguration;
-  plan(job, most);
-  return launch_pdl(kern, dim3(job.p.grid), dim3(threads), smem, st, job, stages);
+  if (held < 1) return cudaErrorInvalidConfiguration;
+  plan(job, std::min(held, kNormGradMaxCtas));
+  cfg.gridDim = dim3(static_cast<unsigned>(job.p.grid * CL));
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const GradJob&>(job), stages);
 }
 
 template <bool F32, bool TOKEN>
@@ -633,37 +516,50 @@ cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
   const BlockNormGradArgs& a = job.a;
   const int slots = 1 + (a.dy ? 2 : 0) + (a.dh ? 1 : 0) + (TOKEN ? 1 : 0);
   constexpr int kMost = 220 * 1024;
-  // W columns a thread; `ctas` CTAs share an SM's memory; the stages that fit
-  const int stage = slots * a.H * (F32 ? 4 : 2);
-  auto threads = [&](int W) { return (a.H / W + 31) / 32 * 32; };
-  auto stages = [&](int W, int ctas) { return std::min(kMostStages, (kMost / ctas - threads(W) * W * 4) / stage); };
-  auto smem = [&](int W, int n) { return n * stage + threads(W) * W * 4; };
+  // A CTA's columns in a team of CL (the widest), its threads at W columns each, the
+  // stages that fit where `ctas` CTAs share an SM's memory, and what they take.
+  auto cols = [&](int CL) { return (a.H / 16 + CL - 1) / CL * 16; };
+  auto threads = [&](int W, int CL) { return (cols(CL) / W + 31) / 32 * 32; };
+  auto stage = [&](int CL) { return slots * cols(CL) * (F32 ? 4 : 2); };
+  auto stages = [&](int W, int CL, int ctas) {
+    return std::min(kMostStages, (kMost / ctas - threads(W, CL) * W * 4) / stage(CL));
+  };
+  auto smem = [&](int W, int CL, int n) { return n * stage(CL) + threads(W, CL) * W * 4; };
   // Two CTAs an SM where both have two stages, else one with as many as fit.  Eight
   // columns a thread keep a row's warps many; 16 fit bf16 rows that would need
   // more than 80 registers in two CTAs (8192 rows of 4096: 72.0 us, with eight 82.6;
   // not for a few rows, 300: 12.8 against 10.7, and not with a gate row for every
   // row, 96.4 against 92.2) or more than 64 in one (4096 rows of 8192: 70.2 us, with
-  // eight 100.5).  Rows that do not fit (fp32 above 8192) go straight to registers
-  // (bf16 rows of 16384 did: 1024 of them 119.6 us, staged 88.3).
-  if (const int n = stages(8, 2); n >= 2) {
-    if (threads(8) <= 256) return launch_staged<F32, TOKEN, 8, 256, 2>(job, threads(8), n, smem(8, n), st);
-    if (threads(8) <= 384) return launch_staged<F32, TOKEN, 8, 384, 2>(job, threads(8), n, smem(8, n), st);
+  // eight 100.5).  Wider rows take a cluster (1024 rows of 16384 bf16 53.1 us, in one
+  // CTA of 1024 threads 88.3; 1024 of 8192 fp32 50.6, in one 61.5; 600 of 12288 fp32
+  // 50.4, with every row straight to registers 76.9).
+  if (const int n = stages(8, 1, 2); n >= 2) {
+    const int t = threads(8, 1);
+    if (t <= 256) return launch_staged<F32, TOKEN, 8, 1, 256, 2>(job, t, n, smem(8, 1, n), st);
+    if (t <= 384) return launch_staged<F32, TOKEN, 8, 1, 384, 2>(job, t, n, smem(8, 1, n), st);
     if constexpr (!F32 && !TOKEN)
-      if (threads(16) <= 256 && a.rows > 8 * num_sms())
-        return launch_staged<F32, TOKEN, 16, 256, 2>(job, threads(16), n, smem(16, n), st);
+      if (threads(16, 1) <= 256 && a.rows > 8 * num_sms())
+        return launch_staged<F32, TOKEN, 16, 1, 256, 2>(job, threads(16, 1), n, smem(16, 1, n), st);
   }
-  if (const int n = stages(8, 1); n >= 1) {
-    if (threads(8) <= 640) return launch_staged<F32, TOKEN, 8, 640, 1>(job, threads(8), n, smem(8, n), st);
-    if constexpr (!F32) {
-      if (threads(16) <= 512) return launch_staged<F32, TOKEN, 16, 512, 1>(job, threads(16), n, smem(16, n), st);
-      if (const int m = stages(16, 1); m >= 1)
-        return launch_staged<F32, TOKEN, 16, 1024, 1>(job, threads(16), m, smem(16, m), st);
-    } else {
-      if (threads(8) <= 1024) return launch_staged<F32, TOKEN, 8, 1024, 1>(job, threads(8), n, smem(8, n), st);
+  if (threads(8, 1) <= 640) {
+    const int n = stages(8, 1, 1);
+    return launch_staged<F32, TOKEN, 8, 1, 640, 1>(job, threads(8, 1), n, smem(8, 1, n), st);
+  }
+  if constexpr (!F32) {
+    if (threads(16, 1) <= 512) {
+      const int n = stages(16, 1, 1);
+      return launch_staged<F32, TOKEN, 16, 1, 512, 1>(job, threads(16, 1), n, smem(16, 1, n), st);
     }
+    const int n = stages(16, 2, 1);  // at most 8192 columns a CTA
+    return launch_staged<F32, TOKEN, 16, 2, 512, 1>(job, threads(16, 2), n, smem(16, 2, n), st);
+  } else {
+    if (threads(8, 2) <= 640) {
+      const int n = stages(8, 2, 1);
+      return launch_staged<F32, TOKEN, 8, 2, 640, 1>(job, threads(8, 2), n, smem(8, 2, n), st);
+    }
+    const int n = stages(8, 4, 1);  // at most 4096 columns a CTA
+    return launch_staged<F32, TOKEN, 8, 4, 512, 1>(job, threads(8, 4), n, smem(8, 4, n), st);
   }
-  const int wide = (a.H / 16 + 31) / 32 * 32;  // 16 columns a thread
-  return launch_direct<F32>(job, wide, st);
 }
 
 }  // namespace

@@ -191,4 +191,16 @@ __device__ __forceinline__ void unpack_raw(const Raw<F32, W>& r, float* f) {
   }
 }
 
+// ------------------------------------------------------- thread-block clusters --
+// Barrier of all CTAs of the cluster (whole, converged warps), and the cluster
+// address of a CTA's shared memory.
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
 }  // namespace fc
