@@ -13,9 +13,9 @@
 // The weights come where they are used, from L1: fewer registers, more rows in
 // flight, which is what a row's two sums are hidden behind; and rows start for L2
 // before a CTA takes them.  The quantised y (mx4.cuh) leaves from the registers that
-// hold it.  Measured on GB300: 8192 x 8192 bf16, both norms and a gate, 85.0 us, 6.3
-// TB/s (0.93 of the measured copy rate; without rows sent for 90.7, with 304 rows
-// ahead 86.4, with 456 86.9, and with the weights loaded first and two CTAs an SM
+// hold it.  Measured on GB300: 8192 x 8192 bf16, both norms and a gate, 83.9 us, 6.4
+// TB/s (0.94 of the measured copy rate; without rows sent for 88.9, with twice as
+// far ahead 1.3 more, with three times 1.7, and with the weights loaded first and two CTAs an SM
 // 99.5); 4096 x 8192 fp32 88.6 us (102.6 without); one row of 4096 1.9 us in a graph.
 #include "block.h"
 #include "mx4.cuh"
