@@ -600,6 +600,26 @@ def test_norm_quantise_project_streams_and_graph():
         assert torch.equal(h, want[0]) and torch.equal(out, want[1])
 
 
+def test_products_on_two_streams():
+    """Both kernels of the product at once, many times over: the bits of one after the other."""
+    jobs = []
+    for k, (rows, features, hidden) in enumerate([(700, 2064, 4096), (9, 4096, 4096), (64, 2048, 8192)]):
+        g = gen_of("streams", k)
+        x, _ = mx4_random(g, rows, hidden, (117, 137))
+        w, _ = mx4_random(g, features, hidden, (112, 133))
+        want, out = (torch.empty(rows, features, device="cuda") for _ in range(2))
+        fc.mx4_matmul(x, w, want)
+        status = torch.zeros(2, dtype=torch.int32, device="cuda")
+        jobs.append((fc.bind_mx4_matmul(x, w, out, status), torch.cuda.Stream(), want, out, status))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, st, _, _, _ in jobs:
+            call(st)
+    torch.cuda.synchronize()
+    for _, _, want, out, status in jobs:
+        assert torch.equal(want, out) and status.tolist() == [0, fc.STATUS_NO_INDEX]
+
+
 def test_training_step_captured():
     """Forward and gradient captured into one graph and replayed: the bits of the calls."""
     i = grad_inputs(150, 2064, "bf16", "gate-seq")
