@@ -364,7 +364,8 @@ fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int6
  *   u = x, or x * inv(x, post_eps) * post_weight       (the norm after the block)
  *   h = T(residual_scale * residual_in + block_scale * gate * u)   -> residual_out
  *   y = T(h * inv(h, pre_eps) * pre_weight)            (the norm before the next)
- *   inv(v, eps) = 1 / sqrt(mean(v^2) + eps), binary32
+ *   inv(v, eps) = 1 / sqrt(mean(v^2) + eps), binary32 (a row's squares have to
+ *   add up to less than binary32's largest number: |v| below 1e17)
  * x: [rows, hidden], the block's output.  residual_in: [rows, hidden], or NULL
  * for none.  post_weight, pre_weight: [hidden]; NULL leaves the norm out (no y
  * without pre_weight).  gate: [gate_rows, hidden], NULL (gate_rows 0) for none;
@@ -400,9 +401,9 @@ fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, in
  * over rows run in a fixed order: the same call gives the same bits.
  * workspace: fc_block_norm_backward_workspace bytes, 32-byte aligned, this
  * call's own until it has run.  rows == 0 sets the weights' gradients that are
- * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual may be x, h, dy or dh itself;
- * outputs overlap nothing else.  d_status: optional, as for fc_group_quantize (a
- * staged row that never lands). */
+ * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual
+ * may be x, h, dy or dh itself; outputs overlap nothing else.  d_status:
+ * optional, as for fc_group_quantize (a staged row that never lands). */
 typedef struct {
   void* dx;
   void* dresidual;

@@ -331,6 +331,23 @@ def test_gradient_matches_differences():
         assert abs(got - want) <= 1e-5 * size, (name, got, want, size)
 
 
+def test_gradient_of_rows_of_zeros_with_a_small_eps():
+    """x = h = 0: xh = hh = 0 and inv = eps^-1/2, so dh' = dh + inv dy pre_weight and dx = inv beta post_weight dh';
+    inv^3 = 1e45 is past binary32."""
+    rows, hidden, eps = 3, 1040, 1e-30
+    g = gen_of("zeros")
+    x = torch.zeros(rows, hidden, device="cuda")
+    dy, dh = randn(g, rows, hidden, std=1e-15), randn(g, rows, hidden)
+    w1, w2 = randn(g, hidden, mean=1.0, std=0.1), randn(g, hidden, mean=1.0, std=0.1)
+    dx, dr = torch.empty_like(x), torch.empty_like(x)
+    fc.block_norm_backward(x, x, dy, dh, dx, fc.alloc_block_norm_workspace(rows, hidden), dresidual=dr,
+                           post_weight=w1, pre_weight=w2, post_eps=eps, pre_eps=eps)
+    inv = float(torch.tensor(eps, dtype=torch.float32)) ** -0.5
+    d, size = dh.double() + inv * dy.double() * w2.double(), dh.double().abs() + inv * (dy.double() * w2.double()).abs()
+    within(dr, d, 128 * U * size, "dresidual")
+    within(dx, inv * w1.double() * d, 128 * U * inv * w1.double().abs() * size, "dx")
+
+
 def test_gradient_of_no_rows_is_zero():
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
