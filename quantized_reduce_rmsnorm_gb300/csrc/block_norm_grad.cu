@@ -323,10 +323,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       if (t < 32) stage_next();
       if (++s == stages) s = 0, phase ^= 1;
       const float inv = pre ? inv_sqrt(__fadd_rn(r[0] * inv_n, a.eps_pre)) : 0.0f;
-      // from the sums outwards: a row of zeros has a finite product even where inv^3 has none
-      const float k = inv * (inv * (inv * (r[1] * inv_n)));
+      // inv^2 times the rest, which for a row of zeros is 0: inv^3 may be past binary32
+      const float k = (inv * inv) * (inv * (r[1] * inv_n));
       const float inv_x = post ? inv_sqrt(__fadd_rn(r[2] * inv_n, a.eps_post)) : 1.0f;
-      const float c = inv_x * (inv_x * (inv_x * ((__fmaf_rn(inv, r[4], r[3]) - k * r[5]) * inv_n)));
+      const float c = (inv_x * inv_x) * (inv_x * ((__fmaf_rn(inv, r[4], r[3]) - k * r[5]) * inv_n));
       if (!on) continue;
       const float2 vi = dup2(inv), vk = dup2(-k), vx = dup2(inv_x), vc = dup2(-c);
       float2 d[kP], o[kP];
