@@ -365,7 +365,8 @@ fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int6
  *   h = T(residual_scale * residual_in + block_scale * gate * u)   -> residual_out
  *   y = T(h * inv(h, pre_eps) * pre_weight)            (the norm before the next)
  *   inv(v, eps) = 1 / sqrt(mean(v^2) + eps), binary32 (a row's squares have to
- *   add up to less than binary32's largest number: |v| below 1e17)
+ *   add up to less than binary32's largest number: |v| below 1e17; where their
+ *   mean plus eps is below its smallest normal number, 1.2e-38, it has fewer bits)
  * x: [rows, hidden], the block's output.  residual_in: [rows, hidden], or NULL
  * for none.  post_weight, pre_weight: [hidden]; NULL leaves the norm out (no y
  * without pre_weight).  gate: [gate_rows, hidden], NULL (gate_rows 0) for none;

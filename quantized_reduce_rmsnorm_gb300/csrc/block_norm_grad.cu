@@ -48,9 +48,9 @@ struct GradJob {
 
 // The rows are staged in shared memory by bulk copies, a few rows ahead, and all of
 // a row's sums are taken at once.  With a = dy * pre_weight, gw = beta * gate *
-// post_weight (one factor a column) and k = inv_h^3 * mean(a * h):
-//   dh' = dh + inv_h * a - k * h
-//   sum(e * x) = sum gw x dh + inv_h * sum gw x a - k * sum gw x h
+// post_weight (one factor a column) and k = inv_h^2 * mean(a * h):
+//   dh' = dh + inv_h * (a - k * h)
+//   sum(e * x) = sum gw x dh + inv_h * (sum gw x a - k * sum gw x h)
 // so the six sums h^2, a h, x^2, gw x dh, gw x a and gw x h, which need nothing of
 // the row before them, give every factor of the row: one barrier a row, and the
 // row goes from shared memory to registers once.  Its stage is free again at
@@ -323,18 +323,20 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       if (t < 32) stage_next();
       if (++s == stages) s = 0, phase ^= 1;
       const float inv = pre ? inv_sqrt(__fadd_rn(r[0] * inv_n, a.eps_pre)) : 0.0f;
-      // inv^2 times the rest, which for a row of zeros is 0: inv^3 may be past binary32
-      const float k = (inv * inv) * (inv * (r[1] * inv_n));
+      // Each inverse root multiplies the sum with one h (x) before the next does, and the
+      // third the row's values: nothing here is the square or the cube of an inverse root,
+      // which for rows near 0 with a small eps is past binary32 where the gradient is not.
+      const float k = inv * (inv * (r[1] * inv_n));
       const float inv_x = post ? inv_sqrt(__fadd_rn(r[2] * inv_n, a.eps_post)) : 1.0f;
-      const float c = (inv_x * inv_x) * (inv_x * ((__fmaf_rn(inv, r[4], r[3]) - k * r[5]) * inv_n));
+      const float c = inv_x * (inv_x * (__fmaf_rn(inv, __fmaf_rn(-k, r[5], r[4]), r[3]) * inv_n));
       if (!on) continue;
       const float2 vi = dup2(inv), vk = dup2(-k), vx = dup2(inv_x), vc = dup2(-c);
       float2 d[kP], o[kP];
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
-        const float2 hi = pair<F32, W>(h, i), e = pmul(pair<F32, W>(dy, i), vi);
-        acc_pre[i] = pfma(e, hi, acc_pre[i]);
-        d[i] = padd(pair<F32, W>(dh, i), pfma(e, pair<F32, W>(w2, i), pmul(vk, hi)));
+        const float2 hi = pair<F32, W>(h, i), e = pair<F32, W>(dy, i);
+        acc_pre[i] = pfma(pmul(e, vi), hi, acc_pre[i]);
+        d[i] = pfma(vi, pfma(vk, hi, pmul(e, pair<F32, W>(w2, i))), pair<F32, W>(dh, i));
       }
       if (a.dres) {
 #pragma unroll
@@ -355,8 +357,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
       for (int i = 0; i < kP; ++i) {
         const float2 xi = pair<F32, W>(x, i);
         acc_r[i] = pfma(pmul(d[i], xi), vx, acc_r[i]);
-        o[i] = pmul(pmul(d[i], gw[i]), vx);
-        if (post) o[i] = pfma(xi, vc, o[i]);
+        o[i] = pmul(d[i], gw[i]);
+        if (post) o[i] = pmul(pfma(vc, xi, o[i]), vx);
       }
       store_cols<F32, W>(static_cast<char*>(a.dx) + off, t, live, o);
     }

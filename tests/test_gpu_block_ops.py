@@ -658,3 +658,55 @@ def test_training_step_captured():
         torch.cuda.synchronize()
         for k in out:
             assert torch.equal(out[k], want[k]), k
+
+
+# ------------------------------------------------------- ends of the range --
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hidden", [272, 1040, 8208])
+@pytest.mark.parametrize("eps", [1e-36, 1e-39, 1e-42, 1.4e-45])
+def test_gradient_of_rows_of_zeros_with_the_smallest_eps(eps, hidden, dtype):
+    """As above for the smallest eps: inv = eps^-1/2 is up to 2.7e22, its square past
+    binary32, and the result 0 times neither."""
+    rows, d = 3, DT[dtype]
+    g = gen_of("zeros", eps, hidden, dtype)
+    x = torch.zeros(rows, hidden, dtype=d, device="cuda")
+    dy, dh = randn(g, rows, hidden, std=1e-15, dtype=d), randn(g, rows, hidden, dtype=d)
+    w1, w2 = (randn(g, hidden, mean=1.0, std=0.1, dtype=d) for _ in range(2))
+    gate = randn(g, 1, hidden, dtype=d)
+    dx, dr, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gate)
+    dw1, dw2 = (torch.full((hidden,), float("nan"), device="cuda") for _ in range(2))
+    fc.block_norm_backward(x, x, dy, dh, dx, fc.alloc_block_norm_workspace(rows, hidden, 1), dresidual=dr,
+                           dpost_weight=dw1, dpre_weight=dw2, dgate=dg, post_weight=w1, gate=gate, pre_weight=w2,
+                           post_eps=eps, pre_eps=eps)
+    inv = float(torch.tensor(eps, dtype=torch.float32)) ** -0.5
+    a = inv * dy.double() * w2.double()
+    want, size = dh.double() + a, dh.double().abs() + a.abs()
+    f = inv * w1.double() * gate.double()
+    within(dr, want, HALF[d] * want.abs() + 128 * U * size, "dresidual")
+    within(dx, f * want, HALF[d] * (f * want).abs() + 128 * U * f.abs() * size, "dx")
+    assert all((t == 0).all() for t in (dw1, dw2, dg))
+
+
+@pytest.mark.parametrize("hidden", [272, 1040, 8208])
+@pytest.mark.parametrize("std", [3e-19, 3e-20])
+def test_gradient_of_very_small_rows_without_eps(std, hidden):
+    """Rows whose mean of squares nears the end of binary32, or is past its normal
+    numbers (3e-20: 9e-40, held to half a step of 2^-149, 13 u of it).  That error is
+    in each row's two sums of squares (6.5 u in each inverse root) and, as x h, in
+    the last of the row's sums (13 u): with at most four inverse roots in a term, 40 u
+    beside the 128."""
+    rows = 5
+    g = gen_of("small rows", std, hidden)
+    i = dict(x=randn(g, rows, hidden, std=std), h=randn(g, rows, hidden, std=std), gate=randn(g, 1, hidden),
+             dy=randn(g, rows, hidden, std=1e-3), dh=randn(g, rows, hidden),
+             post_weight=randn(g, hidden, mean=1.0, std=0.1), pre_weight=randn(g, hidden, mean=1.0, std=0.1))
+    out = grad_outputs(i)
+    fc.block_norm_backward(i["x"], i["h"], i["dy"], i["dh"], workspace=fc.alloc_block_norm_workspace(rows, hidden, 1),
+                           post_weight=i["post_weight"], gate=i["gate"], pre_weight=i["pre_weight"], post_eps=0.0,
+                           pre_eps=0.0, **out)
+    want = ref.grad_reference(i["x"], i["h"], i["dy"], i["dh"], i["post_weight"], i["gate"], i["pre_weight"], 1.0, 1.0,
+                              0.0)
+    for name, got in out.items():
+        value, size = want[name]
+        summed = rows if name not in ("dx", "dresidual") else 0
+        within(got, value, U * value.abs() + (summed + 168) * U * size, name)
