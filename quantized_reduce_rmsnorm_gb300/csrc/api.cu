@@ -13,6 +13,10 @@
 #include "fcomm.h"
 #include "internal.h"
 
+namespace fc {
+int64_t wait_cycles = int64_t(1) << 31;
+}
+
 namespace {
 
 thread_local char g_msg[512] = "";

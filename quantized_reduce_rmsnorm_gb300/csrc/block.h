@@ -13,6 +13,11 @@ namespace fc {
 // 1024 threads of 16 elements each.
 constexpr int kBlockNormMaxHidden = 16384;
 
+// Clock cycles after which a kernel gives up waiting for a copy or a product and
+// reports FC_ERR_CUDA: 2^31, about a second.  Read at a launch.  Waits that let work in
+// flight end before the memory it uses goes always have the whole 2^31.
+extern int64_t wait_cycles;
+
 struct BlockNormArgs {
   const void* x;
   const void* res_in;

@@ -191,6 +191,30 @@ __device__ __forceinline__ void unpack_raw(const Raw<F32, W>& r, float* f) {
   }
 }
 
+// ------------------------------------------------------------ bounded waits --
+// Waits for phase `parity` of the barrier for at most about `cycles` clock cycles;
+// false: not complete by then.  A suspended wait may last longer than a short limit,
+// which is polled for instead.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, int64_t cycles) {
+  if (cycles >= 1 << 20) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+      if (clock64() - t0 > cycles) return false;
+    return true;
+  }
+  const long long t0 = clock64();
+  uint32_t ok;
+  do {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  } while (!ok && clock64() - t0 < cycles);
+  return ok != 0;
+}
+
 // ------------------------------------------------------- thread-block clusters --
 // Barrier of all CTAs of the cluster (whole, converged warps), and the cluster
 // address of a CTA's shared memory.

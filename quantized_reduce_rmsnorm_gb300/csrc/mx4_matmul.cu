@@ -46,6 +46,7 @@ struct Job {
   void* out;
   int32_t* status;
   int64_t rows, features;
+  int64_t wait;     // cycles
   int H, KT;        // elements and scale tiles of k
   int out_f32;
 };
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads)
       int s = 0, used = 0;
       uint32_t phase = 1;  // a first pass over the stages waits for nothing
       for (int i = i0; i < i1; ++i) {
-        if (!mbar_wait_bounded(empty + s, phase)) {
+        if (!mbar_wait_for(empty + s, phase, j.wait)) {
           *failed = 1;
           break;
         }
@@ -216,18 +217,18 @@ __global__ void __launch_bounds__(kThreads)
         used = min(used + 1, T::kStages);
         if (++s == T::kStages) s = 0, phase ^= 1;
       }
-      if (*failed)  // the copies in flight land before the CTA ends
-        for (int q = 0; q < used; ++q) {
-          if (--s < 0) s = T::kStages - 1, phase ^= 1;
-          mbar_wait_bounded(full + s, phase ^ 1);
-        }
+      // the last copies land before the CTA ends, also where the products gave up on them
+      for (int q = 0; q < used; ++q) {
+        if (--s < 0) s = T::kStages - 1, phase ^= 1;
+        mbar_wait_bounded(full + s, phase ^ 1);
+      }
     }
   } else if (warp == 5) {
     if (elect_one()) {
       int s = 0;
       uint32_t phase = 0;
       for (int i = i0; i < i1; ++i) {
-        if (!mbar_wait_bounded(full + s, phase)) {
+        if (!mbar_wait_for(full + s, phase, j.wait)) {
           *failed = 1;
           break;
         }
@@ -250,9 +251,10 @@ __global__ void __launch_bounds__(kThreads)
         if (++s == T::kStages) s = 0, phase ^= 1;
       }
       tc_commit(done);
+      mbar_wait_bounded(done, 0);  // and the products end before the memory they use goes
     }
   } else {
-    if (!mbar_wait_bounded(done, 0)) *failed = 1;
+    if (!mbar_wait_for(done, 0, j.wait)) *failed = 1;
     tc_fence_after();
     __syncwarp();
     const int f = warp * 32 + lane;
@@ -742,8 +744,8 @@ cudaError_t launch(const Mx4MatmulArgs& a, const Job& j, int parts, cudaStream_t
 }  // namespace
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, cudaStream_t st) {
-  const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, a.H,
-              static_cast<int>(mx4_tiles_k(a.H)), a.out_f32 ? 1 : 0};
+  const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, wait_cycles,
+              a.H, static_cast<int>(mx4_tiles_k(a.H)), a.out_f32 ? 1 : 0};
   // The kernel that cuts k holds two CTAs an SM.  Its parts: as many as keep all
   // CTAs resident at once, at least four stages each (measured, us, 1 / 2 / 4 / 8
   // parts: 1 token 8192 x 8192 12.6 / 9.8 / 8.3 / -, 64 tokens 4096 x 4096 8.8 / 7.0 /
