@@ -355,7 +355,8 @@ fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, 
  * binary32, one rounding.  features: a multiple of 16.  NaN scales make NaN of
  * the rows (x) or columns (w) of out that they belong to.  For serving: the
  * codes have no gradient.  d_status: optional, as for fc_group_quantize (a
- * staging copy or a product that never completes within its bounded wait). */
+ * staging copy or a product that never completes within its bounded wait: what
+ * was waiting for it in out is then not written, or NaN). */
 fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int64_t hidden, void* out,
                         int32_t out_dtype, int32_t* d_status, fc_stream_t stream);
 

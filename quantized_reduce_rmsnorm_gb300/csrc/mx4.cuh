@@ -193,26 +193,23 @@ __device__ __forceinline__ void unpack_raw(const Raw<F32, W>& r, float* f) {
 
 // ------------------------------------------------------------ bounded waits --
 // Waits for phase `parity` of the barrier for at most about `cycles` clock cycles;
-// false: not complete by then.  A suspended wait may last longer than a short limit,
-// which is polled for instead.
+// false: not complete by then.  One loop, its tries suspended for at most a part of the
+// limit: with a loop of polls beside it for short limits, the instructions that a launch
+// has to fetch made the product of 64 tokens by 4096 x 4096 7.0 us instead of 6.4.
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, int64_t cycles) {
-  if (cycles >= 1 << 20) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity))
-      if (clock64() - t0 > cycles) return false;
-    return true;
-  }
   const long long t0 = clock64();
   uint32_t ok;
   do {
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(static_cast<uint32_t>(cycles >> 11))  // ns
         : "memory");
   } while (!ok && clock64() - t0 < cycles);
   return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // ------------------------------------------------------- thread-block clusters --

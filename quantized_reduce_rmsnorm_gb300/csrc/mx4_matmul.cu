@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* ssb = ssa + T::kStages * T::kSfBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(ssb + T::kStages * T::kSfBytes);
   uint64_t* empty = full + T::kStages;
-  uint64_t* done = empty + T::kStages;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* done = empty + T::kStages;       // the accumulator holds this part's sums
+  uint64_t* ended = done + 1;                // all copies and products issued have ended
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
   volatile uint32_t* failed = tmem_at + 1;
   float* part = reinterpret_cast<float*>(base);          // [BN][128] sums, when the stages are done with
   static_assert(BN * kM * 4 <= T::kStages * T::kStageBytes, "the sums fit where the stages were");
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-    mbar_init(done, 1);
+    mbar_init(done, 1), mbar_init(ended, 2);
     *failed = 0;
     mbar_init_fence();
   }
@@ -222,14 +223,17 @@ __global__ void __launch_bounds__(kThreads)
         if (--s < 0) s = T::kStages - 1, phase ^= 1;
         mbar_wait_bounded(full + s, phase ^ 1);
       }
+      mbar_arrive(ended);
     }
   } else if (warp == 5) {
     if (elect_one()) {
       int s = 0;
       uint32_t phase = 0;
+      bool ok = true;
       for (int i = i0; i < i1; ++i) {
         if (!mbar_wait_for(full + s, phase, j.wait)) {
           *failed = 1;
+          ok = false;
           break;
         }
         tc_fence_after();
@@ -250,11 +254,16 @@ __global__ void __launch_bounds__(kThreads)
         tc_commit(empty + s);
         if (++s == T::kStages) s = 0, phase ^= 1;
       }
-      tc_commit(done);
-      mbar_wait_bounded(done, 0);  // and the products end before the memory they use goes
+      if (ok) tc_commit(done);
+      tc_commit(ended);
+      mbar_wait_bounded(ended, 0);  // before the memory that they use goes
     }
   } else {
-    if (!mbar_wait_for(done, 0, j.wait)) *failed = 1;
+    const bool there = __all_sync(kFull, mbar_wait_for(done, 0, j.wait));
+    if (!there) {
+      *failed = 1;
+      mbar_wait_bounded(ended, 0);
+    }
     tc_fence_after();
     __syncwarp();
     const int f = warp * 32 + lane;
@@ -264,9 +273,10 @@ __global__ void __launch_bounds__(kThreads)
       uint32_t v[16];
       tc_load16(mine + c, v);
       if (parts > 1) {
+        // a part without its sums makes NaN of the tile
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kM + f] = __uint_as_float(v[i]);
-      } else if (n0 + f < j.features && !*failed) {
+        for (int i = 0; i < 16; ++i) part[(c + i) * kM + f] = __uint_as_float(there ? v[i] : 0x7FC00000u);
+      } else if (n0 + f < j.features && there) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (c + i < tokens) store_out(j, t0 + c + i, n0 + f, __uint_as_float(v[i]));
@@ -279,26 +289,25 @@ __global__ void __launch_bounds__(kThreads)
     cluster_sync_all();  // every part's sums are in its shared memory
     const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
     const int shift = 5 - (31 - __clz(parts));  // log2 of the slice's groups of four features
-    if (!*failed)
-      for (int k = threadIdx.x; k < tokens << shift; k += kThreads) {
-        const int t = k >> shift, f = ((part_id << shift) + (k & ((1 << shift) - 1))) * 4;
-        const float* p = part + t * kM + f;
-        float4 v[kMostParts], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = threadIdx.x; k < tokens << shift; k += kThreads) {
+      const int t = k >> shift, f = ((part_id << shift) + (k & ((1 << shift) - 1))) * 4;
+      const float* p = part + t * kM + f;
+      float4 v[kMostParts], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int r = 0; r < kMostParts; ++r)
-          if (r < parts) v[r] = ld_cluster(cluster_addr(p, r));
+      for (int r = 0; r < kMostParts; ++r)
+        if (r < parts) v[r] = ld_cluster(cluster_addr(p, r));
 #pragma unroll
-        for (int r = 0; r < kMostParts; ++r)
-          if (r < parts) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-        if (n0 + f < j.features) {  // a multiple of 16: all four or none
-          const int64_t at = (t0 + t) * j.features + n0 + f;
-          if (j.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = s;
-          else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.out) + at) =
-                make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
-        }
+      for (int r = 0; r < kMostParts; ++r)
+        if (r < parts) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+      if (n0 + f < j.features) {  // a multiple of 16: all four or none
+        const int64_t at = (t0 + t) * j.features + n0 + f;
+        if (j.out_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(j.out) + at) = s;
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.out) + at) =
+              make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
       }
+    }
     __syncwarp();
     cluster_sync_all();  // no part's memory goes before the others have read it
   } else {
