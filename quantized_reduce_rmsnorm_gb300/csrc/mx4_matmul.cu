@@ -389,6 +389,11 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Arrives on bar of this CTA alone.
+__device__ __forceinline__ void tc_commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -461,8 +466,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
   uint64_t* empty = full + T::kStages;
   uint64_t* acc_full = empty + T::kStages;   // the accumulator holds a tile
   uint64_t* acc_free = acc_full + 1;         // the first CTA's: it is in both CTAs' result warps' registers
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_free + 1);
-  volatile uint32_t* failed = tmem_at + 1;
+  uint64_t* ended = acc_free + 1;            // the first CTA's: all products issued have ended
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
+  volatile uint32_t* failed = tmem_at + 1;   // a role of either CTA gave up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1;
   const int stages_k = (j.H + kStageK - 1) / kStageK;
@@ -472,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
     mbar_init(acc_full, 1);
-    mbar_init(acc_free, 16);
+    mbar_init(acc_free, 16), mbar_init(ended, 1);
     *failed = 0;
     mbar_init_fence();
   }
@@ -482,17 +488,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  const uint32_t peer_failed = cluster_addr(const_cast<const uint32_t*>(failed), rank ^ 1);
+  auto give_up = [&] {
+    *failed = 1;
+    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(peer_failed) : "memory");
+  };
   pdl_begin();
 
   if (warp == 8) {
     if (elect_one()) {
-      int s = 0, used = 0;
+      int s = 0;
       uint32_t phase = 1;  // a first pass over the stages waits for nothing
       bool ok = true;
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
         const int nt = tile % tiles_n * 2, tt = tile / tiles_n * 2;  // in steps of 128
         for (int i = 0; i < stages_k; ++i) {
-          if (!mbar_wait_bounded(empty + s, phase)) {
+          if (!mbar_wait_for(empty + s, phase, j.wait)) {
             ok = false;
             break;
           }
@@ -505,18 +516,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
           tma_load_2d_pair(ssa + s * T::kSfBytes, &map_wsf, 0, ((nt + rank) * j.KT + 2 * i) * 4, bar);
           tma_load_2d_pair(ssb + 2 * s * T::kSfBytes, &map_xsf, 0, (tt * j.KT + 2 * i) * 4, bar);
           tma_load_2d_pair(ssb + (2 * s + 1) * T::kSfBytes, &map_xsf, 0, ((tt + 1) * j.KT + 2 * i) * 4, bar);
-          used = min(used + 1, T::kStages);
           if (++s == T::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!ok) {
-        *failed = 1;
-        // the copies in flight, both CTAs', land before either ends
-        for (int q = 0; rank == 0 && q < used; ++q) {
-          if (--s < 0) s = T::kStages - 1, phase ^= 1;
-          mbar_wait_bounded(full + s, phase ^ 1);
-        }
-      }
+      if (!ok) give_up();
     }
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
@@ -524,7 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
       uint32_t phase = 0, acc_phase = 1;
       bool ok = true;
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
-        if (!mbar_wait_bounded(acc_free, acc_phase)) {
+        if (!mbar_wait_for(acc_free, acc_phase, j.wait)) {
           ok = false;
           break;
         }
@@ -539,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
             tc_copy_scales_pair(sf + 8 + 4 * (2 * q + r), desc_scales(smem_u32(ssb + (2 * st + r) * T::kSfBytes + q * 512)));
         };
         auto ready = [&](int st, uint32_t ph) {  // the stage's copies have landed
-          ok = mbar_wait_bounded(full + st, ph);
+          ok = mbar_wait_for(full + st, ph, j.wait);
           tc_fence_after();
           return ok;
         };
@@ -571,12 +574,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
         }
         if (ok) tc_commit_pair(acc_full);
       }
-      if (!ok) {  // what was issued ends before the memory it uses is given back
-        *failed = 1;
+      if (!ok) {
+        give_up();
         tc_commit_pair(acc_full);
-        mbar_wait_bounded(acc_full, 0);
-        mbar_wait_bounded(acc_full, 1);
       }
+      tc_commit_own(ended);
+      mbar_wait_bounded(ended, 0);  // before the memory that they use goes
     }
   } else {
     constexpr int kCols = T::kTile / 2;
@@ -586,10 +589,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
     const uint32_t freed = cluster_addr(acc_free, 0);
     uint32_t phase = 0;
     for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs) {
-      const bool there = mbar_wait_bounded(acc_full, phase);
+      const bool there = mbar_wait_for(acc_full, phase, j.wait);
       phase ^= 1;
       if (__any_sync(kFull, !there || *failed)) {
-        *failed = 1;
+        give_up();
         break;
       }
       tc_fence_after();
@@ -638,6 +641,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
   }
   __syncwarp();
   cluster_sync_all();  // neither CTA ends while the other's products or barriers use its memory
+  if (*failed) {
+    // Copies may be in flight that neither CTA can wait for: the second CTA's count on
+    // the first's barriers, and the CTAs may have given up at different stages.  No more
+    // are issued; they have the time of a wait to land in.
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1ll << 31) __nanosleep(10000);
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
   if (warp == 9) {
     __syncwarp();

@@ -80,3 +80,18 @@ def test_product_that_gives_up(rows, features, hidden):
         assert torch.equal(out[there], want[there])
 
     run_out(run, status, check, check_rest)
+
+
+# fewer tiles than pairs of CTAs, and several tiles a pair; a call that gives up takes a second
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,features,hidden", [(200, 1040, 544), (2100, 4368, 288)])
+def test_wide_product_that_gives_up(rows, features, hidden, dtype):
+    (x, w), want = product_case(rows, features, hidden)
+    out = torch.empty(rows, features, dtype=dtype, device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def check():
+        assert torch.equal(out, want.to(dtype))
+
+    run_out(fc.bind_mx4_matmul(x, w, out, d_status=status), status, check, lambda: None,
+            limits=[0, 600, 1500, 3000, 7000, 20000, 1 << 19], times=1)
