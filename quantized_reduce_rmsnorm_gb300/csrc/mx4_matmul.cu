@@ -574,10 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
         }
         if (ok) tc_commit_pair(acc_full);
       }
-      if (!ok) {
-        give_up();
-        tc_commit_pair(acc_full);
-      }
+      if (!ok) give_up();
       tc_commit_own(ended);
       mbar_wait_bounded(ended, 0);  // before the memory that they use goes
     }
