@@ -405,7 +405,8 @@ fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, in
  * call's own until it has run.  rows == 0 sets the weights' gradients that are
  * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual
  * may be x, h, dy or dh itself; outputs overlap nothing else.  d_status:
- * optional, as for fc_group_quantize (a staged row that never lands). */
+ * optional, as for fc_group_quantize (a staged row that never lands: it and rows
+ * after it are then not written, and the weights' gradients are of no use). */
 typedef struct {
   void* dx;
   void* dresidual;

@@ -13,8 +13,10 @@ namespace fc {
 // 1024 threads of 16 elements each.
 constexpr int kBlockNormMaxHidden = 16384;
 
-// Clock cycles after which a kernel gives up waiting for a copy or a product and
-// reports FC_ERR_CUDA: 2^31, about a second.  Read at a launch.  Waits that let work in
+// Clock cycles after which the product gives up waiting for a copy or a product and
+// reports FC_ERR_CUDA: 2^31, about a second.  Read at a launch.  The gradient's rows have
+// the whole 2^31 whatever it is (a limit of their own, polled for, makes 8192 x 5120 87.4
+// us instead of 85.3), but with 0 they all count as late.  Waits that let work in
 // flight end before the memory it uses goes always have the whole 2^31.
 extern int64_t wait_cycles;
 

@@ -44,6 +44,7 @@ struct GradJob {
   float* ws_pre;      // [grid, H] sums of the CTAs
   float* ws_post;
   float* ws_gate;     // [segs * cuts, H]
+  uint32_t late;      // not 0: every copy counts as late
 };
 
 // The rows are staged in shared memory by bulk copies, a few rows ahead, and all of
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   float4* acc_post = reinterpret_cast<float4*>(ring + static_cast<size_t>(stages) * slots * row_bytes);
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(full + s, 1);
-    late[0] = late[1] = 0;
+    late[0] = late[1] = job.late;
     mbar_init_fence();
   }
   for (int i = t; i < 2 * 8 * Red<CL>::kStride; i += blockDim.x) red[0][i] = 0.0f;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
         r[3] = s3.x + s3.y, r[4] = s4.x + s4.y, r[5] = s5.x + s5.y;
       }
       row_sums8<CL>(r, red[count & 1]);
-      if (late[count & 1]) {  // set before this row's barrier only, so all read the same
+      if (late[count & 1]) {  // set at the start, or before this row's barrier: all read the same
         stop = true;
         break;
       }
@@ -570,6 +571,7 @@ cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
 cudaError_t launch_block_norm_grad(bool f32, const BlockNormGradArgs& a, cudaStream_t st) {
   GradJob job{};
   job.a = a;
+  job.late = wait_cycles <= 0;
   const bool token = a.gate && a.gate_rows == a.rows;
   if (cudaError_t e = f32 ? token ? launch_grad<true, true>(job, st) : launch_grad<true, false>(job, st)
                           : token ? launch_grad<false, true>(job, st)

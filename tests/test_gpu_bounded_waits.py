@@ -105,3 +105,36 @@ def test_wide_product_that_gives_up(rows, features, hidden, dtype):
 
     run_out(run, status, check, check_rest,
             limits=[0, 600, 1500, 3000, 7000, 20000, 1 << 19], times=1)
+
+
+# one CTA a row, and clusters of two and of four
+@pytest.mark.parametrize("rows,hidden,dtype", [(1, 1040, torch.bfloat16), (700, 1040, torch.bfloat16),
+                                               (300, 2064, torch.float32), (300, 16384, torch.bfloat16),
+                                               (200, 12288, torch.float32)])
+def test_gradient_that_gives_up(rows, hidden, dtype):
+    g = torch.Generator(device="cuda").manual_seed(rows + hidden)
+    x, h, dy, dh = (torch.randn(rows, hidden, generator=g, device="cuda").to(dtype) for _ in range(4))
+    w = torch.ones(hidden, dtype=dtype, device="cuda")
+    dx, dr = torch.empty_like(x), torch.empty_like(x)
+    dw1, dw2 = (torch.empty(hidden, device="cuda") for _ in range(2))
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    call = fc.bind_block_norm_backward(x, h, dy, dh, dx, fc.alloc_block_norm_workspace(rows, hidden), dresidual=dr,
+                                       dpost_weight=dw1, dpre_weight=dw2, post_weight=w, pre_weight=w, d_status=status)
+    outs = (dx, dr, dw1, dw2)
+
+    def run():
+        for t in outs:
+            t.fill_(float("nan"))
+        call()
+
+    run()
+    want = [t.clone() for t in outs]
+    assert not any(torch.isnan(t).any() for t in want)
+
+    def check():
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+    def check_rest():  # every row counts as late, none is written; the sums over rows are of no use
+        assert torch.isnan(dx).all() and torch.isnan(dr).all()
+
+    run_out(run, status, check, check_rest, limits=[0, 1 << 19])
