@@ -190,7 +190,8 @@ class Bound:
     itself.  The object holds a reference to every tensor it was bound to,
     so their memory cannot be freed and handed to another tensor while the
     bound call exists.  For the calls that carry an epoch (tagged formats),
-    `epoch` may be changed between calls."""
+    `epoch` may be changed between calls.  Threads may share a bound call: a
+    call changes nothing that another one reads (the epoch is the setter's)."""
     __slots__ = ("_fn", "_args", "_si", "_ei", "_keep")
 
     def __init__(self, fn, args, stream_index, epoch_index=None, keep=()):
@@ -206,7 +207,7 @@ class Bound:
         self._args[self._ei] = ctypes.c_uint32(e & 0xFFFFFFFF)
 
     def __call__(self, stream=None):
-        a = self._args
+        a = self._args.copy()
         a[self._si] = _stream(stream)
         st = self._fn(*a)
         if st != FC_OK:
@@ -227,17 +228,20 @@ class DeviceBound(Bound):
             return a if isinstance(a, t) or type(a).__name__ == "CArgObject" else t(a)
         super().__init__(_lib[fn.__name__], [exact(a, t) for a, t in zip(args, fn.argtypes)],
                          stream_index, keep=keep)
-        self._dev, self._last = device, None
+        self._dev = device
+        self._last = (None, None)  # a stream and the arguments for it, replaced together
 
     def __call__(self, stream=None):
         if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self(stream)
         s = torch._C._cuda_getCurrentRawStream(self._dev) if stream is None else _stream(stream)
-        if s != self._last:
-            self._args[self._si] = ctypes.c_void_p(s)
-            self._last = s
-        st = self._fn(*self._args)
+        last = self._last
+        if s != last[0]:
+            a = self._args.copy()
+            a[self._si] = ctypes.c_void_p(s)
+            self._last = last = (s, a)
+        st = self._fn(*last[1])
         if st != FC_OK:
             _check(st)
 

@@ -191,3 +191,47 @@ def test_device_bound_call_passes_exact_arguments(monkeypatch):
     b._fn = lambda *a: fc.FC_ERR_INVALID
     with pytest.raises(fc.FcommError):
         b()
+
+
+@pytest.mark.parametrize("kind", ["Bound", "DeviceBound"])
+def test_bound_call_shared_by_threads_keeps_each_call_on_its_stream(kind, monkeypatch):
+    """Another thread's whole call on another stream, put between any two lines of a
+    call: both launch on their own streams, and so do the calls after them."""
+    import sys
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    cls = getattr(fc, kind)
+    code = cls.__call__.__code__
+    lines, at = 0, 0
+    while at <= lines:
+        fn, args = fc.load().fc_mx4_quantize, [A[0], BF16, 0, 64, fc.Mx4(A[1], A[2]), None]
+        b = cls(fn, args, 5, keep=(), device=0) if kind == "DeviceBound" else cls(fn, args, 5)
+        launched = []
+        b._fn = lambda *a: launched.append(getattr(a[5], "value", a[5])) or 0
+        seen = 0
+
+        def trace(frame, event, arg):
+            nonlocal seen
+            if frame.f_code is not code:
+                return None
+            if event == "line":
+                seen += 1
+                if seen == at:  # the other thread runs here
+                    sys.settrace(None)
+                    b(22)
+                    sys.settrace(trace)
+            return trace
+
+        b(33)
+        before = sys.gettrace()
+        sys.settrace(trace)
+        try:
+            b(11)
+        finally:
+            sys.settrace(before)
+        lines = max(lines, seen)
+        assert sorted(launched[1:]) == ([11, 22] if at else [11]), (at, launched)
+        for s in (11, 22, 11):
+            b(s)
+            assert launched[-1] == s, (at, launched)
+        at += 1
+    assert lines >= 3
