@@ -354,9 +354,10 @@ fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, 
  * features] of out_dtype FC_FMT_BF16 or FC_FMT_F32: products exact, sums in
  * binary32, one rounding.  features: a multiple of 16.  NaN scales make NaN of
  * the rows (x) or columns (w) of out that they belong to.  For serving: the
- * codes have no gradient.  d_status: optional, as for fc_group_quantize (a
- * staging copy or a product that never completes within its bounded wait: what
- * was waiting for it in out is then not written, or NaN). */
+ * codes have no gradient.  out and d_status share no memory with one another or
+ * an input.  d_status: optional, as for fc_group_quantize (a staging copy or a
+ * product that never completes within its bounded wait: what was waiting for it
+ * in out is then not written, or NaN). */
 fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int64_t hidden, void* out,
                         int32_t out_dtype, int32_t* d_status, fc_stream_t stream);
 
@@ -404,7 +405,7 @@ fc_status fc_block_norm(const void* x, const void* residual_in, int64_t rows, in
  * workspace: fc_block_norm_backward_workspace bytes, 32-byte aligned, this
  * call's own until it has run.  rows == 0 sets the weights' gradients that are
  * asked for to 0 (with no rows, gate_rows may be any count).  dx and dresidual
- * may be x, h, dy or dh itself; outputs overlap nothing else.  d_status:
+ * may be x, h, dy or dh itself; outputs (d_status too) overlap nothing else.  d_status:
  * optional, as for fc_group_quantize (a staged row that never lands: it and rows
  * after it are then not written, and the weights' gradients are of no use). */
 typedef struct {

@@ -625,7 +625,8 @@ fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int6
   if (fc_status s = check_mx4(w, "w")) return s;
   if (fc_status s = check_ptr(out, 32, "out")) return s;
   if (d_status && !aligned(d_status, 4)) return fail(FC_ERR_INVALID, "d_status must be 4-byte aligned");
-  const Span o[] = {{out, rows * features * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false}};
+  const Span o[] = {{out, rows * features * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false},
+                    {d_status, 8, "d_status", false}};
   const Span i[] = {{x.codes, rows * hidden / 2, "x.codes", false},
                     {x.scales, (int64_t)fc_mx4_scales_bytes(rows, hidden), "x.scales", false},
                     {w.codes, features * hidden / 2, "w.codes", false},
@@ -748,7 +749,8 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
       {g.dpost_weight, hidden * 4, "dpost_weight", false},
       {g.dgate, spec->gate_rows * hidden * es, "dgate", false},
       {g.dpre_weight, hidden * 4, "dpre_weight", false},
-      {workspace, (int64_t)fc_block_norm_backward_workspace(rows, hidden, spec->gate_rows), "workspace", false}};
+      {workspace, (int64_t)fc_block_norm_backward_workspace(rows, hidden, spec->gate_rows), "workspace", false},
+      {d_status, 8, "d_status", false}};
   const Span i[] = {{x, n * es, "x", true},
                     {h, n * es, "h", true},
                     {dy, n * es, "dy", true},

@@ -235,3 +235,15 @@ def test_bound_call_shared_by_threads_keeps_each_call_on_its_stream(kind, monkey
             assert launched[-1] == s, (at, launched)
         at += 1
     assert lines >= 3
+
+
+def test_status_word_overlaps_no_tensor_of_its_call():
+    """d_status is an output: reset before the kernel runs, it would spoil an input that holds it."""
+    x, w, E = fc.Mx4(A[1], A[2]), fc.Mx4(A[3], A[4]), A[5]
+    for at in (A[0], A[0] + 4 * 64 * 2 - 4, A[1], A[2] + 508, A[3] + 64, A[4]):
+        refused("fc_mx4_matmul", x, w, 4, 64, 64, A[0], BF16, at, None, says="d_status")
+    full = spec(post=A[5], gate=A[6], pre=A[7], gate_rows=2)
+    g = fc.BlockNormGrads(A[8], A[9], A[10], A[11], A[12])
+    for at in A[:13]:
+        refused("fc_block_norm_backward", *back(full, g, st=at), says="d_status")
+    refused("fc_block_norm_backward", *back(full, g, st=A[0] - 4), says="d_status")
