@@ -117,3 +117,19 @@ def grad_reference(x, h, dy, dh, post_w, gate, pre_w, alpha, beta, eps):
     else:
         out["dx"] = (du, su)
     return out
+
+
+def scaled_pair(g: torch.Generator, rows: int, features: int, hidden: int):
+    """Two microscaled operands whose blocks' scales differ, (code, byte) each, and whose
+    product is exact in binary32 in any order of its sums: values are multiples of
+    0.5, products of 0.25, and the sum of the products' sizes, which bounds every
+    partial sum, is below 2^24 of those.  Scales of 1 to 128 where that leaves room,
+    else of 1 to 8, of 1 or 2."""
+    code = [torch.randint(0, 16, (n, hidden), generator=g) for n in (rows, features)]
+    pick = [torch.randint(0, 8, (n, hidden // 32), generator=g) for n in (rows, features)]
+    for spread in (8, 4, 2):
+        byte = [127 + p % spread for p in pick]
+        xv, wv = (mx4_values(c, b) for c, b in zip(code, byte))
+        if (xv.abs() @ wv.abs().T).max() * 4 < 2 ** 24:
+            return list(zip(code, byte)), xv @ wv.T
+    raise AssertionError("no such scales at this size")

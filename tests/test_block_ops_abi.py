@@ -247,3 +247,23 @@ def test_status_word_overlaps_no_tensor_of_its_call():
     for at in A[:13]:
         refused("fc_block_norm_backward", *back(full, g, st=at), says="d_status")
     refused("fc_block_norm_backward", *back(full, g, st=A[0] - 4), says="d_status")
+
+
+@pytest.mark.parametrize("rows,features,hidden", [(3, 32, 65536), (1, 16, 16384), (1, 512, 4096), (5, 16, 64)])
+def test_exact_product_inputs_show_every_block(rows, features, hidden):
+    """The inputs of the exact test of the product see a block's scale doubled, a stage of
+    256 elements left out and two neighbouring blocks' scales exchanged, at any k."""
+    g = torch.Generator().manual_seed(rows + features + hidden)
+    ((xc, xb), (wc, wb)), want = ref.scaled_pair(g, rows, features, hidden)
+    assert torch.equal(want.float().double(), want) and len(xb.unique()) > 1 and len(wb.unique()) > 1
+    blocks = hidden // 32
+    xv, wv = (ref.mx4_values(c, b).reshape(len(c), blocks, 32) for c, b in ((xc, xb), (wc, wb)))
+    part = torch.einsum("tbk,nbk->btn", xv, wv)  # each block's share of the result
+    assert (part.sum(0) == want).all()
+    assert (part != 0).any(2).float().mean() > 0.99     # a block of x doubled: seen in some feature
+    assert (part != 0).any(1).float().mean() > 0.85     # a block of w: few tokens see it
+    stages = torch.stack([p.sum(0) for p in part.split(8)])
+    assert (stages != 0).flatten(1).any(1).all()
+    f = torch.exp2((xb[:, 1:] - xb[:, :-1]).double()).T[..., None]  # [block, token, 1]
+    moved = part[:-1] * f + part[1:] / f - part[:-1] - part[1:]
+    assert (moved != 0).any(2)[(f != 1)[..., 0]].float().mean() > 0.97

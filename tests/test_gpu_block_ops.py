@@ -710,3 +710,15 @@ def test_gradient_of_very_small_rows_without_eps(std, hidden):
         value, size = want[name]
         summed = rows if name not in ("dx", "dresidual") else 0
         within(got, value, U * value.abs() + (summed + 168) * U * size, name)
+
+
+# ------------------------------------------- blocks of different scales ----
+@pytest.mark.parametrize("rows,features,hidden", SHAPES + [(2100, 4368, 288), (1100, 9232, 1568), (700, 528, 16384)])
+def test_product_with_scales_is_exact(rows, features, hidden):
+    """Every block has its scale and no other's: bit for bit, in fp32 and in bf16."""
+    pair, want = ref.scaled_pair(gen_of("scaled", rows, features, hidden), rows, features, hidden)
+    x, w = (tuple(t.cuda() for t in ref.pack_mx4(*p, fill=0xFF)) for p in pair)
+    for d in (torch.float32, torch.bfloat16):
+        out = torch.full((rows, features), float("nan"), dtype=d, device="cuda")
+        fc.mx4_matmul(x, w, out)
+        assert torch.equal(out.cpu(), want.to(d))
