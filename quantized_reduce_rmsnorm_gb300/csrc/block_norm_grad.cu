@@ -15,8 +15,8 @@
 // adds its columns up in registers, each thread its own, so there is no atomic
 // and the order of every sum is fixed.  A CTA writes its sums once, to the
 // workspace, and a second kernel adds the CTAs' sums in order.
-// Measured on GB300, 8192 x 5120 bf16 with everything asked for: 83.6 us, 6.0 TB/s
-// (0.89 of the measured copy rate), of which the second kernel is about 4; rows
+// Measured on GB300, 8192 x 5120 bf16 with everything asked for: 84.8 us, 5.9 TB/s
+// (0.88 of the measured copy rate), of which the second kernel is about 4; rows
 // straight to registers with two barriers a row took 233.
 #include <algorithm>
 
@@ -468,7 +468,10 @@ void plan(GradJob& job, int64_t most) {
   p.gate_direct = a.gate && a.gate_rows == a.rows;
   p.segs = a.gate && !p.gate_direct ? a.gate_rows : 1;
   p.seg_rows = a.rows / p.segs;
-  // one piece a CTA where there are fewer gate rows than CTAs, else one piece a gate row
+  // One piece a CTA where there are fewer gate rows than CTAs, else one piece a gate
+  // row.  A count of gate rows just above the CTAs, or half of them, leaves many idle
+  // (us, rows of 5120 bf16, 152 CTAs, 50 rows a gate row, by gate rows: 76 57.4, 77 77.3,
+  // 152 79.9, 153 149.1, 304 150.4).
   p.cuts = static_cast<int>(std::max<int64_t>(1, std::min(most / p.segs, p.seg_rows)));
   p.cut_rows = static_cast<int>(p.seg_rows / p.cuts);
   p.cut_more = static_cast<int>(p.seg_rows % p.cuts);
@@ -531,12 +534,13 @@ cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
   auto smem = [&](int W, int CL, int n) { return n * stage(CL) + threads(W, CL) * W * 4; };
   // Two CTAs an SM where both have two stages, else one with as many as fit.  Eight
   // columns a thread keep a row's warps many; 16 fit bf16 rows that would need
-  // more than 80 registers in two CTAs (8192 rows of 4096: 72.0 us, with eight 82.6;
-  // not for a few rows, 300: 12.8 against 10.7, and not with a gate row for every
-  // row, 96.4 against 92.2) or more than 64 in one (4096 rows of 8192: 70.2 us, with
-  // eight 100.5).  Wider rows take a cluster (1024 rows of 16384 bf16 53.1 us, in one
-  // CTA of 1024 threads 88.3; 1024 of 8192 fp32 50.6, in one 61.5; 600 of 12288 fp32
-  // 50.4, with every row straight to registers 76.9).
+  // more than 80 registers in two CTAs (8192 rows of 4096: 72.0 us, with eight 75.3;
+  // not for a few rows, 300: 13.4 against 10.8, and not with a gate row for every
+  // row, 102.8 against 88.3) or more than 64 in one (4096 rows of 8192: 70.8 us, with
+  // eight 109.7).  Wider rows take a cluster (1024 rows of 16384 bf16 56.5 us, in one
+  // CTA of 1024 threads 94.3; 1024 of 8192 fp32 52.7, in one 61.4; 600 of 12288 fp32
+  // 53.0).  fp32 rows of 2064 and wider in two CTAs spill 88 bytes a thread, with a gate
+  // row for every row 172: 2048 rows of 2560 with one each 44.1 us, 0.56 of the copy rate.
   if (const int n = stages(8, 1, 2); n >= 2) {
     const int t = threads(8, 1);
     if (t <= 256) return launch_staged<F32, TOKEN, 8, 1, 256, 2>(job, t, n, smem(8, 1, n), st);

@@ -141,8 +141,8 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 // the CTAs of a cluster take the parts of k of one tile, leave their sums in
 // their shared memory, and each adds up a slice of the features over the parts,
 // in order (no atomics: the same bits every time).  Bound by the weights' bytes:
-// one token by 8192 x 8192 8.2 us, 4.4 TB/s (floor 5.3 us; one CTA a tile 12.6); what is
-// left is a launch, the first copies' latency and the join.
+// one token by 8192 x 8192, weights that are not in L2, 8.5 us, 4.2 TB/s (floor 5.3 us;
+// one CTA a tile 11.5); what is left is a launch, the first copies' latency and the join.
 __device__ __forceinline__ float4 ld_cluster(uint32_t at) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -328,15 +328,17 @@ __global__ void __launch_bounds__(kThreads)
 // shared memory and leave each CTA its 128 features by all 256 tokens.  A pair
 // loads a third less than two CTAs with tiles of their own: 35 KB a stage and CTA
 // (8192 x 8192 x 8192: 162 us against 170, with four stages of the five 169; with the
-// scales' moves between the products 160 us, 6.87 PFLOP/s, the tensor pipe active for
-// three quarters of it; without those moves it would be 149, without the stores 156).  Copies run
+// scales' moves between the products 160 us, with the waits of mbar_wait_for 153, 7.2
+// PFLOP/s, the tensor pipe active for four fifths of it).  An instruction takes 64
+// elements of k; those of 96 that this chip has, at half as much again, are not used.  Copies run
 // ahead into the next tile; the eight result warps take the accumulator into
 // registers (each 32 features by 128 tokens) and hand it back, so that the
 // next tile's products start while they round, stage and store this one's, each
 // warp by itself: 16 tokens at a time to shared memory, and from there by bulk
 // tensor stores.  bf16 leaves the tensor memory as 16 x 8 fragments, whose transposed
-// store makes rows of features (4096 tokens, 8192 features, 1024 elements: 20.4 us
-// against 23.1 with a store for each element).
+// store makes rows of features (4096 tokens, 8192 features, 1024 elements, in tiles of one
+// CTA: 20.4 us against 23.1 with a store for each element; pairs of CTAs 24.2, their loss
+// where k is short).
 template <bool OUT32>
 struct Wide {
   static constexpr int kTile = 256;     // features and tokens of a pair's tile
@@ -765,12 +767,12 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, cudaStream_t st) {
   const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, wait_cycles,
               a.H, static_cast<int>(mx4_tiles_k(a.H)), a.out_f32 ? 1 : 0};
   // The kernel that cuts k holds two CTAs an SM.  Its parts: as many as keep all
-  // CTAs resident at once, at least four stages each (measured, us, 1 / 2 / 4 / 8
-  // parts: 1 token 8192 x 8192 12.6 / 9.8 / 8.3 / -, 64 tokens 4096 x 4096 8.8 / 7.0 /
-  // 5.4 / 7.6 at two stages a part).  Above 128 tokens, and where k is not cut, the
-  // persistent kernel's wider tile wins (512 tokens 8192 x 8192 17.5 against 20.9,
-  // 2048 tokens 4096 x 4096 17.5 against 26.9); with k cut it does not (512 tokens
-  // 2048 x 8192: 15.9 against 11.8).
+  // CTAs resident at once, at least four stages each (us, inputs changing from call to
+  // call, 1 / 2 / 4 / 8 parts: 1 token 8192 x 8192 11.5 / 10.1 / 8.5 / 11.6, 64 tokens 4096
+  // x 4096 8.8 / 8.3 / 6.3 / 7.7 at two stages a part).  Above 128 tokens, and where k
+  // is not cut, the persistent kernel's wider tile wins (512 tokens 8192 x 8192 16.9
+  // against 20.5, 2048 tokens 4096 x 4096 17.1 against 25.9); with k cut it does not (512
+  // tokens 2048 x 8192: 15.0 against 12.2).
   const int64_t stages = (a.H + kStageK - 1) / kStageK;
   const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : 128;
   const int64_t tiles = ((a.features + kM - 1) / kM) * ((a.rows + bn - 1) / bn);
