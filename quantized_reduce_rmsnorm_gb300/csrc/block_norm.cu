@@ -76,9 +76,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const BlockNormArgs a
   float2 ss = zero;
   if (live) {
     float2 u[W / 2];
-    const float2 f = dup2(a.beta * inv);  // of x: the norm's factor and the block's scale
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pair<F32, W>(xr, i), f);
+    for (int i = 0; i < W / 2; ++i) u[i] = pmul(pair<F32, W>(xr, i), dup2(inv));
     if (a.post_w) {
       const Raw<F32, W> w = load_weight<F32, W>(a.post_w, e);
 #pragma unroll
@@ -87,9 +86,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const BlockNormArgs a
     if (a.gate)
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(gr, i));
-    if (a.res_in)
+    // block_scale last: with the inverse root alone it may be past binary32
+    if (a.res_in) {
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) u[i] = pfma(pair<F32, W>(rr, i), dup2(a.alpha), u[i]);
+      for (int i = 0; i < W / 2; ++i) u[i] = pfma(u[i], dup2(a.beta), pmul(pair<F32, W>(rr, i), dup2(a.alpha)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], dup2(a.beta));
+    }
     hr = pack_raw<F32, W>(u);
     store_raw<F32, W>(a.res_out, at, hr);
 #pragma unroll

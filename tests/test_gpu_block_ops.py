@@ -722,3 +722,22 @@ def test_product_with_scales_is_exact(rows, features, hidden):
         out = torch.full((rows, features), float("nan"), dtype=d, device="cuda")
         fc.mx4_matmul(x, w, out)
         assert torch.equal(out.cpu(), want.to(d))
+
+
+@pytest.mark.parametrize("hidden", [272, 4096, 12288])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_block_scale_of_small_rows(dtype, hidden):
+    """block_scale times an inverse root may be past binary32 where block_scale times the
+    normed row is not: rows of zeros with the smallest eps, and rows of 1e-15 without."""
+    d = DT[dtype]
+    g = gen_of("large scale", dtype, hidden)
+    x, r = randn(g, 4, hidden, std=1e-15, dtype=d), randn(g, 4, hidden, dtype=d)
+    w, gate = randn(g, hidden, mean=1.0, std=0.1, dtype=d), randn(g, 1, hidden, dtype=d)
+    h = torch.empty_like(x)
+    fc.block_norm(x, r, h, post_weight=w, gate=gate, block_scale=1e25, post_eps=0.0)
+    beta = float(torch.tensor(1e25))
+    want, size = ref.norm_reference(x, r, w, gate, 1.0, beta, 0.0)
+    within(h, want, HALF[d] * want.abs() + 32 * U * size, "h")
+    for res in (r, None):
+        fc.block_norm(torch.zeros_like(x), res, h, post_weight=w, gate=gate, block_scale=1e25, post_eps=1.4e-45)
+        assert torch.equal(h, torch.zeros_like(h) if res is None else r)
