@@ -14,8 +14,8 @@
 // flight, which is what a row's two sums are hidden behind; and rows start for L2
 // before a CTA takes them.  The quantised y (mx4.cuh) leaves from the registers that
 // hold it.  Measured on GB300, inputs changing from call to call: 8192 x
-// 8192 bf16, both norms and eight gates, 84.1 us, 6.4 TB/s (0.94 of the measured copy
-// rate; without rows sent for 90.2, with twice as far ahead 85.5); 4096 x 8192 fp32 89.5
+// 8192 bf16, both norms and eight gates, 83.2 us, 6.5 TB/s (0.95 of the measured copy
+// rate; without rows sent for 89.0, with twice as far ahead 84.5); 4096 x 8192 fp32 89.5
 // us; one row of 4096 1.9 us in a graph.
 #include "block.h"
 #include "mx4.cuh"
@@ -153,11 +153,11 @@ cudaError_t launch_block_norm(bool f32, BlockNormArgs a, cudaStream_t st) {
   a.ahead = num_sms();
   // Registers for three CTAs of 512 threads an SM spill a little: they are taken where
   // the rows then go in fewer turns of the whole GPU (us, inputs changing from call to
-  // call, three / two CTAs, rows of 8192: 300 7.2 / 6.1, 456 8.3 / 10.4, 600 12.1 / 11.4,
-  // 2048 26.1 / 26.6, 8192 84.2 / 88.1).  fp32 rows up to 5120: CTAs of up to 640 threads,
-  // two an SM (1037 x 5120, a gate a row, 19.7 us; held to three they spill, 23.0); wider
+  // call, three / two CTAs, rows of 8192: 300 7.2 / 6.1, 456 8.3 / 10.3, 600 12.1 / 11.3,
+  // 2048 25.8 / 26.0, 8192 83.2 / 85.8).  fp32 rows up to 5120: CTAs of up to 640 threads,
+  // two an SM (1037 x 5120, a gate a row, 19.6 us; held to three they spill, 23.8); wider
   // ones have an SM to themselves, which costs the narrower of them: 1037 rows of 5120,
-  // 5136, 6144, 7168, one gate, 17.3, 20.6, 23.1, 25.6 us; 4096 rows of 6144 72.5 us, 0.82
+  // 5136, 6144, 7168, one gate, 17.2, 20.6, 23.3, 25.6 us; 4096 rows of 6144 72.9 us, 0.82
   // of the copy rate, of 8192 89.5, 0.89.
   if (!f32) {
     if (a.H <= 512) return launch_teams<false, 16>(a, st);
