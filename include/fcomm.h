@@ -422,6 +422,107 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
                                  const fc_block_norm_spec* spec, const fc_block_norm_grads* grads,
                                  void* workspace, int32_t* d_status, fc_stream_t stream);
 
+/* Residual add and layer norm.  All tensors are of one dtype T, FC_FMT_BF16 or
+ * FC_FMT_F32:
+ *   h = T(x + residual_in)                          -> residual_out
+ *   y = T((h - mean(h)) * inv * weight + bias),  inv = 1 / sqrt(var(h) + eps)
+ * with mean, var (the mean of squared distances to the mean) and inv in binary32
+ * (a row's squared distances have to add up to less than binary32's largest
+ * number).  x, residual_in, residual_out, y: [rows, hidden].  residual_in and
+ * residual_out: both or neither; without them h is x.  weight, bias: [hidden],
+ * each NULL for none.  stats: fp32 [rows, 2], 8-byte aligned, receives each row's
+ * mean and inv for the gradient; NULL if not wanted.  hidden: a multiple of 16,
+ * at most 16384.  rows <= 2^31 - 1.  Every other tensor is 32-byte aligned.
+ * eps in [0, 1].  residual_out and y may be x or residual_in itself; outputs
+ * overlap nothing else. */
+fc_status fc_layer_norm(const void* x, const void* residual_in, int64_t rows, int64_t hidden, int32_t dtype,
+                        const void* weight, const void* bias, float eps, void* residual_out, void* y,
+                        float* stats, fc_stream_t stream);
+
+/* Gradient of fc_layer_norm.  h: what was normed (residual_out, or x without a
+ * residual); stats: what the forward pass wrote; dy: the gradient of y; dh: that
+ * of residual_out by itself, or NULL.  dx: the gradient of h, which is that of x
+ * and of residual_in alike.  dweight, dbias: fp32[hidden], 4-byte aligned, each NULL
+ * if not wanted (also without a weight or a bias); sums over rows run in a fixed
+ * order: the same call gives the same bits.  workspace:
+ * fc_layer_norm_backward_workspace bytes, 32-byte aligned, this call's own until
+ * it has run.  rows == 0 sets dweight and dbias to 0.  dx may be h, dy or dh
+ * itself; outputs (d_status too) overlap nothing else.  d_status: optional, as for
+ * fc_block_norm_backward. */
+size_t fc_layer_norm_backward_workspace(int64_t rows, int64_t hidden);
+fc_status fc_layer_norm_backward(const void* h, const float* stats, const void* dy, const void* dh,
+                                 int64_t rows, int64_t hidden, int32_t dtype, const void* weight, void* dx,
+                                 float* dweight, float* dbias, void* workspace, int32_t* d_status,
+                                 fc_stream_t stream);
+
+/* 8-bit floating point with a scale for each block of 128: one tensor of rows x
+ * hidden elements (hidden a multiple of 16).  codes: uint8[rows*hidden], e4m3.
+ * scales: fp32 [ceil(rows / block_rows), ceil(hidden / 128)], one for each block of
+ * block_rows (1: an activation's; 128: a weight's) by 128 elements; the last of
+ * the rows and of a row may be smaller.  codes 16-byte aligned, scales 4-byte. */
+typedef struct {
+  void* codes;
+  float* scales;
+} fc_fp8;
+
+/* Number of scales; 0 for an invalid size. */
+size_t fc_fp8_scales(int64_t rows, int64_t hidden, int64_t block_rows);
+
+/* Quantize [rows, hidden] of dtype FC_FMT_BF16 or FC_FMT_F32.  Per block: s =
+ * max(max|x| / 448, 2^-60) (binary32), codes x / s (a binary32 quotient) rounded to
+ * the nearest e4m3 value (ties to even, at most 448 in magnitude); a block with an
+ * infinity or a NaN has the scale NaN, so all of it reads back as NaN. */
+fc_status fc_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, int64_t block_rows,
+                          fc_fp8 out, fc_stream_t stream);
+
+/* Read back: out[rows, hidden] = code * scale, rounded once to out_dtype
+ * FC_FMT_BF16 or FC_FMT_F32. */
+fc_status fc_fp8_dequantize(fc_fp8 in, int64_t rows, int64_t hidden, int64_t block_rows, void* out,
+                            int32_t out_dtype, fc_stream_t stream);
+
+/* Product: out[t, n] = sum over blocks b of k of sx[t, b] * sw[n / 128, b] * sum in b
+ * of x[t, k] * w[n, k], x of rows x hidden with block_rows 1 (tokens), w of features
+ * x hidden with block_rows 128 (a projection's weight), out [rows, features] of
+ * out_dtype FC_FMT_BF16 or FC_FMT_F32.  Scales are any binary32 numbers whose
+ * products are too; codes' products are exact, sums in binary32, one rounding.
+ * features: a multiple of 16.  A NaN scale makes NaN of the row (x) or the columns
+ * (w) of out that it belongs to.  For serving: the codes have no gradient.  out and
+ * d_status share no memory with one another or an input.  d_status: optional, as
+ * for fc_mx4_matmul. */
+fc_status fc_fp8_matmul(fc_fp8 x, fc_fp8 w, int64_t rows, int64_t features, int64_t hidden, void* out,
+                        int32_t out_dtype, int32_t* d_status, fc_stream_t stream);
+
+/* The gated feed-forward block's two projections, activation and product:
+ *   g = x w_gate^T,  u = x w_up^T,  out = bf16(act(g) * u)
+ * x: [rows, hidden], w_gate and w_up: [features, hidden], out: [rows, features], all
+ * bf16 and 32-byte aligned; sums, activation and product in binary32.  gate, up:
+ * [rows, features] bf16, receive g and u for the gradient; both or neither.
+ * hidden and features: multiples of 16; hidden at most 65536, rows and features at
+ * most 2^22.  Outputs overlap nothing.  d_status: optional, as for fc_mx4_matmul. */
+typedef enum {
+  FC_ACT_SILU = 0,     /* z / (1 + exp(-z)) */
+  FC_ACT_GELU_TANH = 1 /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+} fc_activation;
+
+fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t features,
+                       int64_t hidden, int32_t activation, void* out, void* gate, void* up, int32_t* d_status,
+                       fc_stream_t stream);
+
+/* Gradient of fc_gated_ffn.  gate, up: what the forward pass kept; dout: the
+ * gradient of out.  With dg = dout * up * act'(gate) and du = dout * act(gate), each
+ * rounded to bf16:
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * in bf16 after a binary32 sum.  dx may be NULL, and both of dw_gate and dw_up, not all
+ * three.  Sums run in a fixed order.  workspace: fc_gated_ffn_backward_workspace
+ * bytes, 32-byte aligned, this call's own until it has run.  rows == 0 sets the
+ * weights' gradients to 0.  Outputs overlap nothing.  d_status: optional, as for
+ * fc_mx4_matmul. */
+size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features);
+fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                const void* up, const void* dout, int64_t rows, int64_t features,
+                                int64_t hidden, int32_t activation, void* dx, void* dw_gate, void* dw_up,
+                                void* workspace, int32_t* d_status, fc_stream_t stream);
+
 /* --------------------------------------------------------------- misc --- */
 const char* fc_status_string(fc_status s);
 /* Message describing the calling thread's last non-OK status ("" if none). */

@@ -197,6 +197,50 @@ fc_status check_mx4(const fc_mx4& t, const char* name) {
   return check_ptr(t.scales, 16, buf);
 }
 
+// Optional tensors.
+fc_status check_optional(const void* p, size_t align, const char* name) {
+  if (p && !aligned(p, align)) return fail(FC_ERR_INVALID, "%s must be %zu-byte aligned", name, align);
+  return FC_OK;
+}
+
+fc_status check_eps(float eps) {
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(FC_ERR_INVALID, "eps must be in [0, 1]");
+  return FC_OK;
+}
+
+fc_status check_fp8_size(int64_t rows, int64_t hidden, int64_t block_rows) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 16, 65536)) return s;
+  if (block_rows != 1 && block_rows != 128)
+    return fail(FC_ERR_INVALID, "block_rows must be 1 or 128 (got %lld)", (long long)block_rows);
+  if (rows * ((hidden + 127) / 128) > INT32_MAX)
+    return fail(FC_ERR_UNSUPPORTED, "rows * ceil(hidden / 128) > 2^31 - 1 is not supported");
+  return FC_OK;
+}
+
+fc_status check_fp8(const fc_fp8& t, const char* name) {
+  char buf[64];
+  snprintf(buf, sizeof buf, "%s.codes", name);
+  if (fc_status s = check_ptr(t.codes, 16, buf)) return s;
+  snprintf(buf, sizeof buf, "%s.scales", name);
+  return check_ptr(t.scales, 4, buf);
+}
+
+// Shape of a product: rows x hidden by features x hidden, hidden a multiple of step.
+fc_status check_product(int64_t rows, int64_t features, int64_t hidden, int step) {
+  if (fc_status s = check_rows_hidden(rows, hidden, step, 65536)) return s;
+  if (rows > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "rows > 2^22 is not supported");
+  if (features <= 0 || features % 16 != 0)
+    return fail(FC_ERR_INVALID, "features must be a positive multiple of 16 (got %lld)", (long long)features);
+  if (features > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "features > 2^22 is not supported");
+  return FC_OK;
+}
+
+fc_status check_activation(int32_t activation) {
+  if (activation != FC_ACT_SILU && activation != FC_ACT_GELU_TANH)
+    return fail(FC_ERR_INVALID, "unknown activation %d", activation);
+  return FC_OK;
+}
+
 // One tensor of a call, for the check of overlaps.
 struct Span {
   const void* p;
@@ -614,11 +658,7 @@ fc_status fc_mx4_dequantize(fc_mx4 in, int64_t rows, int64_t hidden, void* out, 
 
 fc_status fc_mx4_matmul(fc_mx4 x, fc_mx4 w, int64_t rows, int64_t features, int64_t hidden, void* out,
                         int32_t out_dtype, int32_t* d_status, fc_stream_t stream) {
-  if (fc_status s = check_rows_hidden(rows, hidden, 32, 65536)) return s;
-  if (rows > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "rows > 2^22 is not supported");
-  if (features <= 0 || features % 16 != 0)
-    return fail(FC_ERR_INVALID, "features must be a positive multiple of 16 (got %lld)", (long long)features);
-  if (features > (1 << 22)) return fail(FC_ERR_UNSUPPORTED, "features > 2^22 is not supported");
+  if (fc_status s = check_product(rows, features, hidden, 32)) return s;
   if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
   if (rows == 0) return ok();
   if (fc_status s = check_mx4(x, "x")) return s;
@@ -784,6 +824,271 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
   if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
   return cuda_status(fc::launch_block_norm_grad(dtype == FC_FMT_F32, a, (cudaStream_t)stream),
                      "fc_block_norm_backward launch");
+}
+
+fc_status fc_layer_norm(const void* x, const void* residual_in, int64_t rows, int64_t hidden, int32_t dtype,
+                        const void* weight, const void* bias, float eps, void* residual_out, void* y,
+                        float* stats, fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 16, fc::kBlockNormMaxHidden)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (fc_status s = check_eps(eps)) return s;
+  if (!residual_in != !residual_out)
+    return fail(FC_ERR_INVALID, "residual_in and residual_out are given together");
+  if (fc_status s = check_optional(weight, 32, "weight")) return s;
+  if (fc_status s = check_optional(bias, 32, "bias")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (fc_status s = check_optional(residual_in, 32, "residual_in")) return s;
+  if (fc_status s = check_optional(residual_out, 32, "residual_out")) return s;
+  if (fc_status s = check_ptr(y, 32, "y")) return s;
+  if (fc_status s = check_optional(stats, 8, "stats")) return s;
+  const int64_t es = dtype == FC_FMT_F32 ? 4 : 2, n = rows * hidden * es;
+  const Span o[] = {{residual_out, n, "residual_out", false}, {y, n, "y", false}, {stats, rows * 8, "stats", false}};
+  const Span i[] = {{x, n, "x", true},
+                    {residual_in, n, "residual_in", true},
+                    {weight, hidden * es, "weight", false},
+                    {bias, hidden * es, "bias", false}};
+  if (fc_status s = check_overlaps(o, 2, i)) return s;
+  fc::LayerNormArgs a{};
+  a.x = x;
+  a.res_in = residual_in;
+  a.res_out = residual_out;
+  a.y = y;
+  a.weight = weight;
+  a.bias = bias;
+  a.stats = stats;
+  a.rows = rows;
+  a.H = static_cast<int>(hidden);
+  a.eps = eps;
+  return cuda_status(fc::launch_layer_norm(dtype == FC_FMT_F32, a, (cudaStream_t)stream), "fc_layer_norm launch");
+}
+
+size_t fc_layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
+  if (rows <= 0 || hidden <= 0) return 0;
+  return static_cast<size_t>(std::min<int64_t>(rows, fc::kNormGradMaxCtas)) * static_cast<size_t>(hidden) * sizeof(float) * 2u;
+}
+
+fc_status fc_layer_norm_backward(const void* h, const float* stats, const void* dy, const void* dh,
+                                 int64_t rows, int64_t hidden, int32_t dtype, const void* weight, void* dx,
+                                 float* dweight, float* dbias, void* workspace, int32_t* d_status,
+                                 fc_stream_t stream) {
+  if (fc_status s = check_rows_hidden(rows, hidden, 16, fc::kBlockNormMaxHidden)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (fc_status s = check_optional(weight, 32, "weight")) return s;
+  if (fc_status s = check_optional(dweight, 4, "dweight")) return s;
+  if (fc_status s = check_optional(dbias, 4, "dbias")) return s;
+  if (fc_status s = check_optional(d_status, 4, "d_status")) return s;
+  const Span early[] = {{dweight, hidden * 4, "dweight", false},
+                        {dbias, hidden * 4, "dbias", false},
+                        {d_status, 8, "d_status", false}};
+  const int64_t es = dtype == FC_FMT_F32 ? 4 : 2, n = rows * hidden * es;
+  const Span w[] = {{weight, hidden * es, "weight", false}};
+  if (fc_status s = check_overlaps(early, 0, w)) return s;
+  if (rows == 0) {  // sums of nothing
+    if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+    for (float* p : {dweight, dbias})
+      if (p)
+        if (fc_status s = cuda_status(cudaMemsetAsync(p, 0, hidden * 4, (cudaStream_t)stream), "gradient of no rows"))
+          return s;
+    return ok();
+  }
+  if (fc_status s = check_ptr(h, 32, "h")) return s;
+  if (fc_status s = check_ptr(stats, 8, "stats")) return s;
+  if (fc_status s = check_ptr(dy, 32, "dy")) return s;
+  if (fc_status s = check_optional(dh, 32, "dh")) return s;
+  if (fc_status s = check_ptr(dx, 32, "dx")) return s;
+  if (fc_status s = check_ptr(workspace, 32, "workspace")) return s;
+  const Span o[] = {{dx, n, "dx", false},
+                    {dweight, hidden * 4, "dweight", false},
+                    {dbias, hidden * 4, "dbias", false},
+                    {workspace, (int64_t)fc_layer_norm_backward_workspace(rows, hidden), "workspace", false},
+                    {d_status, 8, "d_status", false}};
+  const Span i[] = {{h, n, "h", true},
+                    {dy, n, "dy", true},
+                    {dh, n, "dh", true},
+                    {stats, rows * 8, "stats", false},
+                    {weight, hidden * es, "weight", false}};
+  if (fc_status s = check_overlaps(o, 1, i)) return s;
+  fc::LayerNormGradArgs a{};
+  a.h = h;
+  a.stats = stats;
+  a.dy = dy;
+  a.dh = dh;
+  a.weight = weight;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.ws = static_cast<float*>(workspace);
+  a.status = d_status;
+  a.rows = rows;
+  a.H = static_cast<int>(hidden);
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+  return cuda_status(fc::launch_layer_norm_grad(dtype == FC_FMT_F32, a, (cudaStream_t)stream),
+                     "fc_layer_norm_backward launch");
+}
+
+size_t fc_fp8_scales(int64_t rows, int64_t hidden, int64_t block_rows) {
+  if (rows < 0 || hidden <= 0 || hidden % 16 != 0 || (block_rows != 1 && block_rows != 128)) return 0;
+  return static_cast<size_t>((rows + block_rows - 1) / block_rows) * static_cast<size_t>((hidden + 127) / 128);
+}
+
+fc_status fc_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, int64_t block_rows,
+                          fc_fp8 out, fc_stream_t stream) {
+  if (fc_status s = check_fp8_size(rows, hidden, block_rows)) return s;
+  if (fc_status s = check_dtype(dtype, "dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (fc_status s = check_fp8(out, "out")) return s;
+  const int64_t n = rows * hidden;
+  const Span o[] = {{out.codes, n, "out.codes", false},
+                    {out.scales, (int64_t)fc_fp8_scales(rows, hidden, block_rows) * 4, "out.scales", false}};
+  const Span i[] = {{x, n * (dtype == FC_FMT_F32 ? 4 : 2), "x", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  return cuda_status(fc::launch_fp8_quantize(dtype == FC_FMT_F32, block_rows == 128, x, rows, static_cast<int>(hidden),
+                                             out.codes, out.scales, (cudaStream_t)stream),
+                     "fc_fp8_quantize launch");
+}
+
+fc_status fc_fp8_dequantize(fc_fp8 in, int64_t rows, int64_t hidden, int64_t block_rows, void* out,
+                            int32_t out_dtype, fc_stream_t stream) {
+  if (fc_status s = check_fp8_size(rows, hidden, block_rows)) return s;
+  if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_fp8(in, "in")) return s;
+  if (fc_status s = check_ptr(out, 32, "out")) return s;
+  const int64_t n = rows * hidden;
+  const Span o[] = {{out, n * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false}};
+  const Span i[] = {{in.codes, n, "in.codes", false},
+                    {in.scales, (int64_t)fc_fp8_scales(rows, hidden, block_rows) * 4, "in.scales", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  return cuda_status(fc::launch_fp8_dequantize(out_dtype == FC_FMT_F32, block_rows == 128, in.codes, in.scales, rows,
+                                               static_cast<int>(hidden), out, (cudaStream_t)stream),
+                     "fc_fp8_dequantize launch");
+}
+
+fc_status fc_fp8_matmul(fc_fp8 x, fc_fp8 w, int64_t rows, int64_t features, int64_t hidden, void* out,
+                        int32_t out_dtype, int32_t* d_status, fc_stream_t stream) {
+  if (fc_status s = check_product(rows, features, hidden, 16)) return s;
+  if (fc_status s = check_dtype(out_dtype, "out_dtype")) return s;
+  if (rows == 0) return ok();
+  if (fc_status s = check_fp8(x, "x")) return s;
+  if (fc_status s = check_fp8(w, "w")) return s;
+  if (fc_status s = check_ptr(out, 32, "out")) return s;
+  if (fc_status s = check_optional(d_status, 4, "d_status")) return s;
+  const Span o[] = {{out, rows * features * (out_dtype == FC_FMT_F32 ? 4 : 2), "out", false},
+                    {d_status, 8, "d_status", false}};
+  const Span i[] = {{x.codes, rows * hidden, "x.codes", false},
+                    {x.scales, (int64_t)fc_fp8_scales(rows, hidden, 1) * 4, "x.scales", false},
+                    {w.codes, features * hidden, "w.codes", false},
+                    {w.scales, (int64_t)fc_fp8_scales(features, hidden, 128) * 4, "w.scales", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  fc::Fp8MatmulArgs a{};
+  a.x_codes = x.codes;
+  a.x_scales = x.scales;
+  a.w_codes = w.codes;
+  a.w_scales = w.scales;
+  a.out = out;
+  a.status = d_status;
+  a.rows = rows;
+  a.features = features;
+  a.H = static_cast<int>(hidden);
+  a.out_f32 = out_dtype == FC_FMT_F32;
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+  return cuda_status(fc::launch_fp8_matmul(a, (cudaStream_t)stream), "fc_fp8_matmul launch");
+}
+
+fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t features,
+                       int64_t hidden, int32_t activation, void* out, void* gate, void* up, int32_t* d_status,
+                       fc_stream_t stream) {
+  if (fc_status s = check_product(rows, features, hidden, 16)) return s;
+  if (fc_status s = check_activation(activation)) return s;
+  if (!gate != !up) return fail(FC_ERR_INVALID, "gate and up are given together");
+  if (rows == 0) return ok();
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (fc_status s = check_ptr(w_gate, 32, "w_gate")) return s;
+  if (fc_status s = check_ptr(w_up, 32, "w_up")) return s;
+  if (fc_status s = check_ptr(out, 32, "out")) return s;
+  if (fc_status s = check_optional(gate, 32, "gate")) return s;
+  if (fc_status s = check_optional(up, 32, "up")) return s;
+  if (fc_status s = check_optional(d_status, 4, "d_status")) return s;
+  const int64_t n = rows * features * 2, wn = features * hidden * 2;
+  const Span o[] = {{out, n, "out", false}, {gate, n, "gate", false}, {up, n, "up", false}, {d_status, 8, "d_status", false}};
+  const Span i[] = {{x, rows * hidden * 2, "x", false}, {w_gate, wn, "w_gate", false}, {w_up, wn, "w_up", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  fc::GatedFfnArgs a{};
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.out = out;
+  a.gate = gate;
+  a.up = up;
+  a.status = d_status;
+  a.rows = rows;
+  a.features = features;
+  a.H = static_cast<int>(hidden);
+  a.activation = activation;
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+  return cuda_status(fc::launch_gated_ffn(a, (cudaStream_t)stream), "fc_gated_ffn launch");
+}
+
+size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features) {
+  if (rows <= 0 || features <= 0) return 0;
+  return static_cast<size_t>(rows) * static_cast<size_t>(features) * 4u;
+}
+
+fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                const void* up, const void* dout, int64_t rows, int64_t features,
+                                int64_t hidden, int32_t activation, void* dx, void* dw_gate, void* dw_up,
+                                void* workspace, int32_t* d_status, fc_stream_t stream) {
+  if (fc_status s = check_product(rows, features, hidden, 16)) return s;
+  if (fc_status s = check_activation(activation)) return s;
+  if (!dw_gate != !dw_up) return fail(FC_ERR_INVALID, "dw_gate and dw_up are given together");
+  if (!dx && !dw_gate) return fail(FC_ERR_INVALID, "no gradient is asked for");
+  if (fc_status s = check_optional(dw_gate, 32, "dw_gate")) return s;
+  if (fc_status s = check_optional(dw_up, 32, "dw_up")) return s;
+  if (fc_status s = check_optional(d_status, 4, "d_status")) return s;
+  const int64_t n = rows * features * 2, wn = features * hidden * 2;
+  const Span o[] = {{dx, rows * hidden * 2, "dx", false},
+                    {dw_gate, wn, "dw_gate", false},
+                    {dw_up, wn, "dw_up", false},
+                    {workspace, (int64_t)fc_gated_ffn_backward_workspace(rows, features), "workspace", false},
+                    {d_status, 8, "d_status", false}};
+  const Span i[] = {{x, rows * hidden * 2, "x", false}, {w_gate, wn, "w_gate", false}, {w_up, wn, "w_up", false},
+                    {gate, n, "gate", false},           {up, n, "up", false},          {dout, n, "dout", false}};
+  if (fc_status s = check_overlaps(o, 0, i)) return s;
+  if (rows == 0) {  // sums of nothing
+    if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+    for (void* p : {dw_gate, dw_up})
+      if (p)
+        if (fc_status s = cuda_status(cudaMemsetAsync(p, 0, wn, (cudaStream_t)stream), "gradient of no rows")) return s;
+    return ok();
+  }
+  if (fc_status s = check_ptr(x, 32, "x")) return s;
+  if (fc_status s = check_ptr(w_gate, 32, "w_gate")) return s;
+  if (fc_status s = check_ptr(w_up, 32, "w_up")) return s;
+  if (fc_status s = check_ptr(gate, 32, "gate")) return s;
+  if (fc_status s = check_ptr(up, 32, "up")) return s;
+  if (fc_status s = check_ptr(dout, 32, "dout")) return s;
+  if (fc_status s = check_optional(dx, 32, "dx")) return s;
+  if (fc_status s = check_ptr(workspace, 32, "workspace")) return s;
+  fc::GatedFfnGradArgs a{};
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.gate = gate;
+  a.up = up;
+  a.dout = dout;
+  a.dx = dx;
+  a.dw_gate = dw_gate;
+  a.dw_up = dw_up;
+  a.ws = workspace;
+  a.status = d_status;
+  a.rows = rows;
+  a.features = features;
+  a.H = static_cast<int>(hidden);
+  a.activation = activation;
+  if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
+  return cuda_status(fc::launch_gated_ffn_grad(a, (cudaStream_t)stream), "fc_gated_ffn_backward launch");
 }
 
 fc_status fc_token_split(int P, int64_t rows, int64_t hidden, fc_qspec spec, int64_t* split,

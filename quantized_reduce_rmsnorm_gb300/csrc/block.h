@@ -67,6 +67,37 @@ struct BlockNormGradArgs {
 };
 cudaError_t launch_block_norm_grad(bool f32, const BlockNormGradArgs& a, cudaStream_t st);
 
+struct LayerNormArgs {
+  const void* x;
+  const void* res_in;   // NULL: h is x, and not written
+  void* res_out;
+  void* y;
+  const void* weight;   // NULL: ones
+  const void* bias;     // NULL: none
+  float* stats;         // NULL, or [rows][2]: mean and inverse deviation
+  int64_t rows;
+  int H;
+  int ahead;            // set at the launch
+  float eps;
+};
+cudaError_t launch_layer_norm(bool f32, LayerNormArgs a, cudaStream_t st);
+
+struct LayerNormGradArgs {
+  const void* h;
+  const float* stats;
+  const void* dy;
+  const void* dh;       // NULL: none
+  const void* weight;   // NULL: ones
+  void* dx;
+  float* dweight;       // NULL: not wanted
+  float* dbias;         // NULL: not wanted
+  float* ws;
+  int32_t* status;      // NULL, or word 0 set to FC_ERR_CUDA if a staged row never lands
+  int64_t rows;
+  int H;
+};
+cudaError_t launch_layer_norm_grad(bool f32, const LayerNormGradArgs& a, cudaStream_t st);
+
 cudaError_t launch_mx4_quantize(bool f32, const void* x, int64_t rows, int H, void* codes,
                                 uint8_t* scales, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(bool f32, const void* codes, const uint8_t* scales, int64_t rows,
@@ -85,5 +116,61 @@ struct Mx4MatmulArgs {
   bool out_f32;
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, cudaStream_t st);
+
+// 8-bit floating point with a scale for each block of 128 (square: of 128 by 128).
+cudaError_t launch_fp8_quantize(bool f32, bool square, const void* x, int64_t rows, int H, void* codes, float* scales,
+                                cudaStream_t st);
+cudaError_t launch_fp8_dequantize(bool f32, bool square, const void* codes, const float* scales, int64_t rows, int H,
+                                  void* out, cudaStream_t st);
+
+struct Fp8MatmulArgs {
+  const void* x_codes;
+  const float* x_scales;  // [rows, ceil(H / 128)]
+  const void* w_codes;
+  const float* w_scales;  // [ceil(features / 128), ceil(H / 128)]
+  void* out;
+  int32_t* status;        // NULL, or word 0 set to FC_ERR_CUDA if a bounded wait ran out
+  int64_t rows;           // tokens
+  int64_t features;
+  int H;
+  bool out_f32;
+};
+cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, cudaStream_t st);
+
+enum Activation : int { kSilu = 0, kGeluTanh = 1 };
+
+struct GatedFfnArgs {
+  const void* x;          // [rows, H]
+  const void* w_gate;     // [features, H]
+  const void* w_up;
+  void* out;              // [rows, features]
+  void* gate;             // NULL: not kept
+  void* up;
+  int32_t* status;
+  int64_t rows;
+  int64_t features;
+  int H;
+  int activation;
+};
+cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st);
+
+struct GatedFfnGradArgs {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  const void* gate;
+  const void* up;
+  const void* dout;       // [rows, features]
+  void* dx;               // NULL: not wanted; so for the weights' two
+  void* dw_gate;
+  void* dw_up;
+  void* ws;               // [2][rows, features] bf16
+  int32_t* status;
+  int64_t rows;
+  int64_t features;
+  int H;
+  int activation;
+};
+cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st);
 
 }  // namespace fc

@@ -23,17 +23,6 @@
 namespace fc {
 namespace {
 
-// Sum over the row's threads: one warp, or the CTA (red: 32 floats of its own
-// for each of a row's sums, so that one barrier serves).
-__device__ __forceinline__ float row_sum(float v, float* red, bool one_warp) {
-  v = warp_sum(v);
-  if (one_warp) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int n = (blockDim.x + 31) >> 5, l = threadIdx.x & 31;
-  return warp_sum(l < n ? red[l] : 0.0f);
-}
-
 // TEAM: one warp a row, four rows a CTA; else one row a CTA.  W: columns of a
 // thread, 32 bytes of them or (fp32 rows above 8192) 64.
 template <bool F32, int W, bool TEAM, int MAXT, int MINB>

@@ -21,7 +21,7 @@
 #include <algorithm>
 
 #include "block.h"
-#include "mx4.cuh"
+#include "grad_rows.cuh"
 
 namespace fc {
 namespace {
@@ -62,74 +62,12 @@ struct GradJob {
 // bytes, the live threads side by side: no bank conflicts.  Rows too wide for one
 // CTA's registers are cut over the CTAs of a cluster, which exchange each row's
 // sums through distributed shared memory.
-template <bool F32, int W>
-struct Cols {
-  static constexpr int kPer = F32 ? 4 : 8;  // columns of a group
-  static constexpr int kGroups = W / kPer;
-  // first column of group j of thread t, `live` threads in all
-  static __device__ __forceinline__ int at(int j, int t, int live) { return (j * live + t) * kPer; }
-};
-
-template <bool F32, int W>
-struct RawCols {
-  uint4 g[Cols<F32, W>::kGroups];
-};
-// The thread's columns of a row (or of a weight), from shared or global memory.
-template <bool F32, int W>
-__device__ __forceinline__ RawCols<F32, W> load_cols(const void* row, int t, int live) {
-  constexpr int es = F32 ? 4 : 2;
-  RawCols<F32, W> r;
-#pragma unroll
-  for (int j = 0; j < Cols<F32, W>::kGroups; ++j)
-    r.g[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + Cols<F32, W>::at(j, t, live) * es);
-  return r;
-}
-// Columns 2i and 2i + 1 of them.
-template <bool F32, int W>
-__device__ __forceinline__ float2 pair(const RawCols<F32, W>& r, int i) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.g);
-  if constexpr (F32) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-  return make_float2(bf_lo(w[i]), bf_hi(w[i]));
-}
-template <bool F32, int W>
-__device__ __forceinline__ void store_cols(void* row, int t, int live, const float2 f[W / 2]) {
-  constexpr int es = F32 ? 4 : 2, kPairs = Cols<F32, W>::kPer / 2;
-#pragma unroll
-  for (int j = 0; j < Cols<F32, W>::kGroups; ++j) {
-    const float2* v = f + j * kPairs;
-    uint4 w;
-    if constexpr (F32)
-      w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-    else
-      w = make_uint4(pack_bf2(v[0].x, v[0].y), pack_bf2(v[1].x, v[1].y), pack_bf2(v[2].x, v[2].y),
-                     pack_bf2(v[3].x, v[3].y));
-    st128(static_cast<char*>(row) + Cols<F32, W>::at(j, t, live) * es, w);
-  }
-}
-// The same columns of a row of fp32 sums.
-template <bool F32, int W>
-__device__ __forceinline__ void store_sums(float* row, int t, int live, const float2 f[W / 2]) {
-  constexpr int kPer = Cols<F32, W>::kPer;
-#pragma unroll
-  for (int k = 0; k < W / 4; ++k) {  // four columns at a time
-    const int at = Cols<F32, W>::at(4 * k / kPer, t, live) + 4 * k % kPer;
-    *reinterpret_cast<float4*>(row + at) = make_float4(f[2 * k].x, f[2 * k].y, f[2 * k + 1].x, f[2 * k + 1].y);
-  }
-}
-
 // Sums of eight values over the CTA, or the CL CTAs of the cluster, each thread
 // ending with all eight, in the same order everywhere.  Within a warp the values are
 // folded onto one another (lanes give away the half that the other lanes keep), so
 // that eight sums take 9 shuffles and not 40; lane l ends with value l / 4.
 // red: 8 rows of Red<CL>::kStride floats (an odd number of 16-byte groups: no bank
 // conflicts), one for each warp of each CTA, those past them 0.
-__device__ __forceinline__ void st_cluster(uint32_t at, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-template <int CL>
-struct Red {
-  static constexpr int kEntries = CL == 1 ? 32 : 64, kStride = kEntries + 4;
-};
 template <int CL>
 __device__ __forceinline__ void row_sums8(float (&v)[8], float* red) {
   using R = Red<CL>;
@@ -419,37 +357,19 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_grad_staged(const Gra
   }
 }
 
-constexpr int kSumWarps = 16, kSumCols = 64, kSumBatch = 10;
-// Adds the CTAs' sums: 64 columns a CTA (a lane has two), 16 warps over the
-// addends, in a fixed order.  blockIdx.y: 0 the norm before, 1 the norm after, 2 +
+// Adds the CTAs' sums.  blockIdx.y: 0 the norm before, 1 the norm after, 2 +
 // s gate row s (segs is below kNormGradMaxCtas where their sums are in pieces).
 template <bool F32>
 __global__ void __launch_bounds__(kSumWarps * 32) k_block_norm_grad_sum(const GradJob job) {
   __shared__ float2 red[kSumWarps][32];
   pdl_begin();
-  const int H = job.a.H, l = threadIdx.x & 31, w = threadIdx.x >> 5, y = blockIdx.y;
-  const int col = blockIdx.x * kSumCols + 2 * l;
+  const int H = job.a.H, y = blockIdx.y;
+  const int col = blockIdx.x * kSumCols + 2 * (threadIdx.x & 31);
   const float* src = y == 0 ? job.ws_pre : y == 1 ? job.ws_post : job.ws_gate + (y - 2) * static_cast<int64_t>(job.p.cuts) * H;
   const int n = y < 2 ? job.p.grid : job.p.cuts;
   if ((y == 0 && !job.a.dpre_w) || (y == 1 && !job.a.dpost_w)) return;
-  const float2 zero = make_float2(0.0f, 0.0f);
-  float2 s = zero;
-  if (col < H)
-    for (int i0 = w; i0 < n; i0 += kSumWarps * kSumBatch) {  // loads that do not wait for one another
-      float2 v[kSumBatch];
-#pragma unroll
-      for (int k = 0; k < kSumBatch; ++k) {
-        const int i = i0 + k * kSumWarps;
-        v[k] = i < n ? *reinterpret_cast<const float2*>(src + static_cast<int64_t>(i) * H + col) : zero;
-      }
-#pragma unroll
-      for (int k = 0; k < kSumBatch; ++k) s = padd(s, v[k]);
-    }
-  red[w][l] = s;
-  __syncthreads();
-  if (w != 0 || col >= H) return;
-#pragma unroll
-  for (int i = 1; i < kSumWarps; ++i) s = padd(s, red[i][l]);
+  float2 s;
+  if (!column_sums(src, n, H, col, red, s)) return;
   if (y < 2) {  // 4-byte aligned
     float* out = (y == 0 ? job.a.dpre_w : job.a.dpost_w) + col;
     out[0] = s.x, out[1] = s.y;

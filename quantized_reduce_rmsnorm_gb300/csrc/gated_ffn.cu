@@ -1,0 +1,596 @@
+// gated_ffn.cu -- the gated feed-forward block's first half and its gradient, in bf16:
+//   g = x w_gate^T,  u = x w_up^T,  out = bf16(act(g) * u)
+//   dg = dout * u * act'(g),  du = dout * act(g)
+//   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+// x [rows, H], weights [features, H], out, g and u [rows, features]; act is SiLU, z
+// sigmoid(z), or GELU by its tanh form, z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)).
+//
+// All products are tcgen05.mma kind::f16 with binary32 sums in tensor memory; each result
+// is rounded once.  Both projections share a tile's copies of x, and their sums meet in
+// the thread that has a token's row of both, so g and u leave the chip only where the
+// caller keeps them (in bf16, for the gradient).  dg and du are rounded to bf16, as the
+// tensor core takes them, in the workspace; their rounding, at most 2^-9 of each term, is
+// within that of the results.
+#include <algorithm>
+
+#include "block.h"
+#include "tc.cuh"
+
+namespace fc {
+namespace {
+
+constexpr int kK = 64;           // elements of k a stage: 128 bytes of a row
+constexpr int kMostParts = 8;    // of k, in one cluster
+constexpr int kErrCuda = 2;      // FC_ERR_CUDA
+
+// sigmoid(z): the hardware's exponential and reciprocal, a few units of 2^-22; 0 below
+// about -88.
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + __expf(-z)); }
+constexpr float kGeluScale = 1.5957691216f, kGeluCube = 0.044715f;  // 2 sqrt(2 / pi)
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if (ACT == kSilu) return z * sigmoid(z);
+  return z * sigmoid(kGeluScale * __fmaf_rn(kGeluCube * z * z, z, z));
+}
+// The activation and its slope s + z p' s (1 - s), s = sigmoid(p(z)).
+template <int ACT>
+__device__ __forceinline__ float2 activate_slope(float z) {
+  const float zz = z * z;
+  const float p = ACT == kSilu ? z : kGeluScale * __fmaf_rn(kGeluCube * zz, z, z);
+  const float dp = ACT == kSilu ? 1.0f : kGeluScale * __fmaf_rn(3.0f * kGeluCube, zz, 1.0f);
+  const float s = sigmoid(p), a = z * s;
+  return make_float2(a, __fmaf_rn(a * dp, 1.0f - s, s));
+}
+
+// ------------------------------------------------ few tokens: k in parts --
+// With few tokens the weights' bytes count.  The tile's 128 rows are 64 features of the
+// gate and the same 64 of the other projection, its columns are tokens: one token costs
+// 16 columns, not 128 rows.  The CTAs of a cluster take the parts of k of one tile and
+// leave their sums in their shared memory, where the two projections of a feature meet;
+// each adds up a slice of the features over the parts, in order (no atomics).
+struct FewJob {
+  void* out;
+  void* gate;
+  void* up;
+  int32_t* status;
+  int64_t rows, features;
+  int64_t wait;     // cycles
+  int H;
+};
+
+template <int BN>
+struct Few {
+  static constexpr int kM = 128, kFeatures = 64, kThreads = 192;  // warps 0-3: result; 4: copies; 5: products
+  static constexpr int kStages = BN >= 128 ? 3 : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;  // two CTAs an SM
+  static constexpr int kABytes = kM * 128, kBBytes = BN * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kCols = BN < 32 ? 32 : BN;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+  static_assert(2 * kCols <= 512 && 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+template <int BN, int ACT>
+__global__ void __launch_bounds__(Few<BN>::kThreads, 2)
+    k_gated_ffn(const FewJob j, const __grid_constant__ CUtensorMap map_gate, const __grid_constant__ CUtensorMap map_up,
+                const __grid_constant__ CUtensorMap map_x) {
+  using T = Few<BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sa = base;                                    // [stage][64 rows of the gate, 64 of the other][128 bytes]
+  uint8_t* sb = sa + T::kStages * T::kABytes;            // [stage][BN rows][128 bytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + T::kStages * T::kBBytes);
+  uint64_t* empty = full + T::kStages;
+  uint64_t* done = empty + T::kStages;       // the accumulator holds this part's sums
+  uint64_t* ended = done + 1;                // all copies and products issued have ended
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
+  volatile uint32_t* failed = tmem_at + 1;
+  float* part = reinterpret_cast<float*>(base);          // [BN][128] sums, when the stages are done with
+  static_assert(BN * T::kM * 4 <= T::kStages * T::kStageBytes, "the sums fit where the stages were");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * T::kFeatures;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * BN;
+  const int parts = gridDim.z, part_id = blockIdx.z;     // a cluster is the parts of a tile
+  const int stages_k = (j.H + kK - 1) / kK;
+  const int i0 = stages_k * part_id / parts, i1 = stages_k * (part_id + 1) / parts;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    mbar_init(done, 1), mbar_init(ended, 2);
+    *failed = 0;
+    mbar_init_fence();
+  }
+  // taken before the next kernel may start, so that all of this grid's CTAs have theirs
+  if (warp == 5) tmem_alloc(tmem_at, T::kCols);
+  if (warp == 4 && elect_one())
+    for (int i = i0; i < i1 && i < i0 + T::kStages; ++i) {
+      tma_prefetch_2d(&map_gate, i * kK, n0);
+      tma_prefetch_2d(&map_up, i * kK, n0);
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_begin();
+
+  if (warp == 4) {
+    if (elect_one()) {
+      int s = 0, used = 0;
+      uint32_t phase = 1;  // a first pass over the stages waits for nothing
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_for(empty + s, phase, j.wait)) {
+          *failed = 1;
+          break;
+        }
+        mbar_expect_tx(full + s, T::kStageBytes);
+        tma_load_2d(sa + s * T::kABytes, &map_gate, i * kK, n0, full + s);
+        tma_load_2d(sa + s * T::kABytes + T::kABytes / 2, &map_up, i * kK, n0, full + s);
+        tma_load_2d(sb + s * T::kBBytes, &map_x, i * kK, static_cast<int>(t0), full + s);
+        used = min(used + 1, T::kStages);
+        if (++s == T::kStages) s = 0, phase ^= 1;
+      }
+      // the last copies land before the CTA ends, also where the products gave up on them
+      for (int q = 0; q < used; ++q) {
+        if (--s < 0) s = T::kStages - 1, phase ^= 1;
+        mbar_wait_bounded(full + s, phase ^ 1);
+      }
+      mbar_arrive(ended);
+    }
+  } else if (warp == 5) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_for(full + s, phase, j.wait)) {
+          *failed = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t da = desc_along_k(smem_u32(sa + s * T::kABytes));
+        const uint64_t db = desc_along_k(smem_u32(sb + s * T::kBBytes));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 16 elements
+          tc_mma_bf16(tmem, da + 2 * k, db + 2 * k, idesc_bf16(T::kM, BN, false, false), i > i0 || k > 0);
+        tc_commit(empty + s);
+        if (++s == T::kStages) s = 0, phase ^= 1;
+      }
+      if (ok) tc_commit(done);
+      tc_commit(ended);
+      mbar_wait_bounded(ended, 0);  // before the memory that they use goes
+    }
+  } else {
+    const bool there = __all_sync(kFull, mbar_wait_for(done, 0, j.wait));
+    if (!there) *failed = 1;
+    mbar_wait_bounded(ended, 0);  // the sums go where the copies went
+    tc_fence_after();
+    __syncwarp();
+    const int f = warp * 32 + lane;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
+    for (int c = 0; c < tokens; c += 16) {
+      uint32_t v[16];
+      tc_load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+      // a part without its sums makes NaN of the tile
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[(c + i) * T::kM + f] = __uint_as_float(there ? v[i] : 0x7FC00000u);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();  // every part's sums are in its shared memory
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
+  const int shift = 4 - (31 - __clz(parts));  // log2 of the slice's groups of four features
+  for (int k = threadIdx.x; k < tokens << shift; k += T::kThreads) {
+    const int t = k >> shift, f = ((part_id << shift) + (k & ((1 << shift) - 1))) * 4;
+    const float* p = part + t * T::kM + f;
+    float4 v[kMostParts], w[kMostParts], g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+#pragma unroll
+    for (int r = 0; r < kMostParts; ++r)
+      if (r < parts) v[r] = ld_cluster(cluster_addr(p, r)), w[r] = ld_cluster(cluster_addr(p + T::kFeatures, r));
+#pragma unroll
+    for (int r = 0; r < kMostParts; ++r)
+      if (r < parts) {
+        g.x += v[r].x, g.y += v[r].y, g.z += v[r].z, g.w += v[r].w;
+        u.x += w[r].x, u.y += w[r].y, u.z += w[r].z, u.w += w[r].w;
+      }
+    if (n0 + f < j.features) {  // a multiple of 16: all four or none
+      const int64_t at = (t0 + t) * j.features + n0 + f;
+      auto put = [&](void* to, float a, float b, float c, float d) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at) = make_uint2(pack_bf2(a, b), pack_bf2(c, d));
+      };
+      put(j.out, activate<ACT>(g.x) * u.x, activate<ACT>(g.y) * u.y, activate<ACT>(g.z) * u.z, activate<ACT>(g.w) * u.w);
+      if (j.gate) {
+        put(j.gate, g.x, g.y, g.z, g.w);
+        put(j.up, u.x, u.y, u.z, u.w);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // no part's memory goes before the others have read it
+  if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, T::kCols);
+  }
+}
+
+// ------------------------------------------------- many tokens: persistent --
+// A pair of CTAs (two SMs) takes tile after tile of 256 rows by 256 columns: each CTA stages
+// 128 rows of A and 128 of B, and one thread of the first issues products of both
+// (cta_group::2), which leave each CTA its 128 rows by all 256 columns.  Two accumulators:
+// the eight result warps, each 32 rows by half the columns, round, stage and store one
+// tile while the products of the next run.
+//
+// One kernel for the three kinds of product.  An operand lies along k (its rows are the
+// matrix's rows) or across it (its rows are the matrix's columns, read as they lie):
+//   kForward: A = x, B = the gate's weight (the first CTA's half) and the other's
+//             (the second's), both along k: 256 tokens by 128 features of both.
+//   kInput:   A = dg, then du, along k; B = w_gate, then w_up, across: dx.
+//   kWeights: A = dg, or du, across k; B = x across k: dw_gate, then dw_up.
+enum Kind { kForward, kInput, kWeights };
+
+struct Job {
+  int32_t* status;
+  int64_t rows, cols;  // of one matrix of the output (kForward: of out)
+  int64_t wait;        // cycles
+  int k;               // elements of k (kInput: of one of the two)
+  int keep;            // kForward: g and u are kept
+};
+
+struct Wide {
+  static constexpr int kTile = 256, kHalf = 128;
+  static constexpr int kStages = 6, kBufs = 2;
+  static constexpr int kThreads = 320;  // warps 0-7: result; 8: copies; 9: products
+  static constexpr int kPartBytes = kHalf * 128, kStageBytes = 2 * kPartBytes;
+  static constexpr int kOutBytes = 4096;  // of a result warp: 32 rows by 64 columns
+  static constexpr int kSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
+  static constexpr int kCols = kBufs * kTile;
+  static_assert(kCols <= 512 && kSmem <= 227 * 1024, "fits");
+};
+
+// The maps of A and B (the second of each for the other weight or its gradient) and of the
+// outputs (kForward: out, g, u; kWeights: one for each weight).
+struct Maps {
+  CUtensorMap a[2], b[2], o[3];
+};
+
+template <int KIND, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
+    k_gated_wide(const Job j, const __grid_constant__ Maps maps) {
+  using T = Wide;
+  constexpr bool kAcrossA = KIND == kWeights, kAcrossB = KIND != kForward;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sa = base;                               // [stage] 128 rows of A
+  uint8_t* sb = sa + T::kStages * T::kPartBytes;    // [stage] 128 of B
+  uint8_t* so = sb + T::kStages * T::kPartBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(so + 8 * T::kOutBytes);  // the first CTA's: both CTAs' copies
+  uint64_t* empty = full + T::kStages;
+  uint64_t* acc_full = empty + T::kStages;      // [buffer] holds a tile
+  uint64_t* acc_free = acc_full + T::kBufs;     // the first CTA's: both CTAs' result warps have read it
+  uint64_t* ended = acc_free + T::kBufs;        // the first CTA's: all products issued have ended
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
+  volatile uint32_t* failed = tmem_at + 1;      // a role of either CTA gave up
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1;
+  constexpr int kTileN = KIND == kForward ? T::kHalf : T::kTile;  // columns of the output
+  const int tiles_n = static_cast<int>((j.cols + kTileN - 1) / kTileN);
+  const int tiles_m = static_cast<int>((j.rows + T::kTile - 1) / T::kTile);
+  const int tiles_one = tiles_n * tiles_m, tiles = KIND == kWeights ? 2 * tiles_one : tiles_one;
+  const int stages_one = (j.k + kK - 1) / kK, stages_k = KIND == kInput ? 2 * stages_one : stages_one;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int b = 0; b < T::kBufs; ++b) mbar_init(acc_full + b, 1), mbar_init(acc_free + b, 16);
+    mbar_init(ended, 1);
+    *failed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc_pair(tmem_at, T::kCols);
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  const uint32_t peer_failed = cluster_addr(const_cast<const uint32_t*>(failed), rank ^ 1);
+  auto give_up = [&] {
+    *failed = 1;
+    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(peer_failed) : "memory");
+  };
+  pdl_begin();
+
+  if (warp == 8) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 1;  // a first pass over the stages waits for nothing
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
+        const int which_tile = tile >= tiles_one;
+        const int2 at = grouped_tile(tile - which_tile * tiles_one, tiles_m, tiles_n);
+        const int a0 = at.x * T::kTile + rank * T::kHalf;
+        const int b0 = KIND == kForward ? at.y * T::kHalf : at.y * T::kTile + rank * T::kHalf;
+        for (int i = 0; i < stages_k; ++i) {
+          if (!mbar_wait_for(empty + s, phase, j.wait)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_expect_tx(full + s, 2 * T::kStageBytes);
+          const uint32_t bar = cluster_addr(full + s, 0);
+          uint8_t* da = sa + s * T::kPartBytes;
+          uint8_t* db = sb + s * T::kPartBytes;
+          // what lies past the end of a tensor reads as 0
+          const int which = KIND == kInput ? i >= stages_one : which_tile;
+          const int k = KIND == kInput ? (i - which * stages_one) * kK : i * kK;
+          const CUtensorMap* ma = maps.a + (KIND == kForward ? 0 : which);
+          const CUtensorMap* mb = maps.b + (KIND == kForward ? rank : KIND == kInput ? which : 0);
+          if constexpr (kAcrossA) {
+            tma_load_2d_pair(da, ma, a0, k, bar);
+            tma_load_2d_pair(da + T::kPartBytes / 2, ma, a0 + 64, k, bar);
+          } else {
+            tma_load_2d_pair(da, ma, k, a0, bar);
+          }
+          if constexpr (kAcrossB) {
+            tma_load_2d_pair(db, mb, b0, k, bar);
+            tma_load_2d_pair(db + T::kPartBytes / 2, mb, b0 + 64, k, bar);
+          } else {
+            tma_load_2d_pair(db, mb, k, b0, bar);
+          }
+          if (++s == T::kStages) s = 0, phase ^= 1;
+        }
+      }
+      if (!ok) give_up();
+    }
+  } else if (warp == 9) {
+    if (rank == 0 && elect_one()) {
+      int s = 0, b = 0;
+      uint32_t phase = 0, acc_phase = 1;
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
+        if (!mbar_wait_for(acc_free + b, acc_phase, j.wait)) {
+          ok = false;
+          break;
+        }
+        for (int i = 0; i < stages_k; ++i) {
+          if (!mbar_wait_for(full + s, phase, j.wait)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sa + s * T::kPartBytes), bb = smem_u32(sb + s * T::kPartBytes);
+          const uint64_t da = kAcrossA ? desc_across_k(a, T::kPartBytes / 2) : desc_along_k(a);
+          const uint64_t db = kAcrossB ? desc_across_k(bb, T::kPartBytes / 2) : desc_along_k(bb);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 16 elements
+            tc_mma_bf16_pair(tmem + b * T::kTile, da + (kAcrossA ? 128 : 2) * k, db + (kAcrossB ? 128 : 2) * k,
+                             idesc_bf16(T::kTile, T::kTile, kAcrossA, kAcrossB), i > 0 || k > 0);
+          tc_commit_pair(empty + s);
+          if (++s == T::kStages) s = 0, phase ^= 1;
+        }
+        if (ok) tc_commit_pair(acc_full + b);
+        if (++b == T::kBufs) b = 0, acc_phase ^= 1;
+      }
+      if (!ok) give_up();
+      tc_commit_own(ended);
+      mbar_wait_bounded(ended, 0);  // before the memory that they use goes
+    }
+  } else {
+    const int half = warp >> 2;
+    uint8_t* buf = so + warp * T::kOutBytes;
+    int b = 0;
+    uint32_t phase = 0;
+    // 32 columns of the lane's row, packed, as 16-byte groups 4 q and on of its 128 bytes in
+    // the order of the 128-byte swizzle
+    auto put = [&](int q, const uint32_t (&w)[16]) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * q + g) ^ (lane & 7)) * 16)) =
+            make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+    };
+    auto wait_stored = [&] {  // the buffer's last store has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
+    auto store = [&](const CUtensorMap* map, int col, int64_t row) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_2d(map, col, static_cast<int>(row), buf);
+    };
+    auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_free + b, 0));
+    };
+    auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf2(__uint_as_float(lo), __uint_as_float(hi)); };
+    for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs) {
+      const bool there = mbar_wait_for(acc_full + b, phase, j.wait);
+      if (__any_sync(kFull, !there || *failed)) {
+        give_up();
+        break;
+      }
+      tc_fence_after();
+      const int which = tile >= tiles_one;
+      const int2 at = grouped_tile(tile - which * tiles_one, tiles_m, tiles_n);
+      const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + b * T::kTile;
+      const int64_t row0 = static_cast<int64_t>(at.x) * T::kTile + rank * T::kHalf + (warp & 3) * 32;
+      if constexpr (KIND == kForward) {
+        const int col0 = at.y * T::kHalf + half * 64;
+        const bool on = row0 < j.rows && col0 < j.cols;
+        uint32_t pg[2][16], pu[2][16];
+        wait_stored();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t g[32], u[32], w[16];
+          tc_load_all<1>(mine + half * 64 + q * 32, g);
+          tc_load_all<1>(mine + T::kHalf + half * 64 + q * 32, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            pg[q][i] = pack(g[2 * i], g[2 * i + 1]), pu[q][i] = pack(u[2 * i], u[2 * i + 1]);
+            w[i] = pack_bf2(activate<ACT>(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
+                            activate<ACT>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+          }
+          put(q, w);
+        }
+        release();
+        if (on) store(maps.o, col0, row0);
+        if (j.keep) {
+          wait_stored();
+          put(0, pg[0]), put(1, pg[1]);
+          if (on) store(maps.o + 1, col0, row0);
+          wait_stored();
+          put(0, pu[0]), put(1, pu[1]);
+          if (on) store(maps.o + 2, col0, row0);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col0 = at.y * T::kTile + half * T::kHalf + c * 64;
+          wait_stored();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[32], w[16];
+            tc_load_all<1>(mine + half * T::kHalf + c * 64 + q * 32, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack(v[2 * i], v[2 * i + 1]);
+            put(q, w);
+          }
+          if (c == 1) release();
+          if (row0 < j.rows && col0 < j.cols) store(maps.o + which, col0, row0);
+        }
+      }
+      if (++b == T::kBufs) b = 0, phase ^= 1;
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  cluster_sync_all();  // neither CTA ends while the other's products or barriers use its memory
+  if (*failed) {
+    // Copies may be in flight that neither CTA can wait for (mx4_matmul.cu): no more are
+    // issued, and they have the time of a wait to land in.
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1ll << 31) __nanosleep(10000);
+    __syncwarp();
+    cluster_sync_all();
+  }
+  if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free_pair(tmem, T::kCols);
+  }
+}
+
+// --------------------------------------------------- gradient's factors ---
+// dg and du of 16 neighbouring elements a thread.  Bound by memory: three tensors in, two out.
+template <int ACT>
+__global__ void __launch_bounds__(256)
+    k_gated_factors(const void* gate, const void* up, const void* dout, int64_t pieces, void* dg, void* du) {
+  pdl_begin();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  const Raw<false, 16> g = load_raw<false, 16>(gate, i * 16), u = load_raw<false, 16>(up, i * 16),
+                       d = load_raw<false, 16>(dout, i * 16);
+  float2 a[8], b[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 z = pair<false, 16>(g, k), o = pair<false, 16>(d, k);
+    const float2 x = activate_slope<ACT>(z.x), y = activate_slope<ACT>(z.y);
+    a[k] = pmul(pmul(o, pair<false, 16>(u, k)), make_float2(x.y, y.y));
+    b[k] = pmul(o, make_float2(x.x, y.x));
+  }
+  store_raw<false, 16>(dg, i * 16, pack_raw<false, 16>(a));
+  store_raw<false, 16>(du, i * 16, pack_raw<false, 16>(b));
+}
+
+// ------------------------------------------------------------- launch ----
+// A bf16 matrix in boxes of 64 columns (128 bytes, swizzled) by box_rows rows.
+cudaError_t bf16_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows) {
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, rows, cols, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+template <int KIND, int ACT>
+cudaError_t launch_wide(const Job& j, const Maps& maps, cudaStream_t st) {
+  auto* kern = k_gated_wide<KIND, ACT>;
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Wide::kSmem)) return e;
+  const int tile_n = KIND == kForward ? Wide::kHalf : Wide::kTile;
+  const int64_t tiles = (j.cols + tile_n - 1) / tile_n * ((j.rows + Wide::kTile - 1) / Wide::kTile) * (KIND == kWeights ? 2 : 1);
+  const int64_t pairs = std::min<int64_t>(tiles, num_sms() / 2);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Wide::kThreads), Wide::kSmem, st, j, maps);
+}
+
+template <int BN>
+cudaError_t launch_few(const GatedFfnArgs& a, int parts, cudaStream_t st) {
+  using T = Few<BN>;
+  auto* kern = a.activation == kSilu ? k_gated_ffn<BN, kSilu> : k_gated_ffn<BN, kGeluTanh>;
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), T::kSmem)) return e;
+  CUtensorMap mg, mu, mx;
+  if (cudaError_t e = bf16_map(&mg, a.w_gate, a.features, a.H, T::kFeatures)) return e;
+  if (cudaError_t e = bf16_map(&mu, a.w_up, a.features, a.H, T::kFeatures)) return e;
+  if (cudaError_t e = bf16_map(&mx, a.x, a.rows, a.H, BN)) return e;
+  const FewJob j{a.out, a.gate, a.up, a.status, a.rows, a.features, wait_cycles, a.H};
+  return launch_parts(kern,
+                      dim3(static_cast<unsigned>((a.features + T::kFeatures - 1) / T::kFeatures),
+                           static_cast<unsigned>((a.rows + BN - 1) / BN), static_cast<unsigned>(parts)),
+                      T::kThreads, T::kSmem, st, j, mg, mu, mx);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
+  const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : 128;
+  const int64_t stages = (a.H + kK - 1) / kK;
+  const int64_t tiles = ((a.features + 63) / 64) * ((a.rows + bn - 1) / bn);
+  int parts = 1;
+  while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  if (a.rows > 128 && parts == 1) {
+    Maps m{};
+    if (cudaError_t e = bf16_map(m.a, a.x, a.rows, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.b, a.w_gate, a.features, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.b + 1, a.w_up, a.features, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.o, a.out, a.rows, a.features, 32)) return e;
+    if (a.gate) {
+      if (cudaError_t e = bf16_map(m.o + 1, a.gate, a.rows, a.features, 32)) return e;
+      if (cudaError_t e = bf16_map(m.o + 2, a.up, a.rows, a.features, 32)) return e;
+    }
+    const Job j{a.status, a.rows, a.features, wait_cycles, a.H, a.gate != nullptr};
+    return a.activation == kSilu ? launch_wide<kForward, kSilu>(j, m, st) : launch_wide<kForward, kGeluTanh>(j, m, st);
+  }
+  if (bn == 16) return launch_few<16>(a, parts, st);
+  if (bn == 32) return launch_few<32>(a, parts, st);
+  if (bn == 64) return launch_few<64>(a, parts, st);
+  return launch_few<128>(a, parts, st);
+}
+
+cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
+  const int64_t n = a.rows * a.features;
+  void* dg = a.ws;
+  void* du = static_cast<__nv_bfloat16*>(a.ws) + n;
+  if (cudaError_t e = launch_pdl(a.activation == kSilu ? k_gated_factors<kSilu> : k_gated_factors<kGeluTanh>,
+                                 dim3(static_cast<unsigned>((n / 16 + 255) / 256)), dim3(256), 0, st, a.gate, a.up,
+                                 a.dout, n / 16, dg, du))
+    return e;
+  if (a.dx) {
+    Maps m{};
+    if (cudaError_t e = bf16_map(m.a, dg, a.rows, a.features, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.a + 1, du, a.rows, a.features, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.b, a.w_gate, a.features, a.H, 64)) return e;
+    if (cudaError_t e = bf16_map(m.b + 1, a.w_up, a.features, a.H, 64)) return e;
+    if (cudaError_t e = bf16_map(m.o, a.dx, a.rows, a.H, 32)) return e;
+    const Job j{a.status, a.rows, a.H, wait_cycles, static_cast<int>(a.features), 0};
+    if (cudaError_t e = launch_wide<kInput, kSilu>(j, m, st)) return e;
+  }
+  if (a.dw_gate) {
+    Maps m{};
+    if (cudaError_t e = bf16_map(m.a, dg, a.rows, a.features, 64)) return e;
+    if (cudaError_t e = bf16_map(m.a + 1, du, a.rows, a.features, 64)) return e;
+    if (cudaError_t e = bf16_map(m.b, a.x, a.rows, a.H, 64)) return e;
+    if (cudaError_t e = bf16_map(m.o, a.dw_gate, a.features, a.H, 32)) return e;
+    if (cudaError_t e = bf16_map(m.o + 1, a.dw_up, a.features, a.H, 32)) return e;
+    const Job j{a.status, a.features, a.H, wait_cycles, static_cast<int>(a.rows), 0};
+    if (cudaError_t e = launch_wide<kWeights, kSilu>(j, m, st)) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace fc

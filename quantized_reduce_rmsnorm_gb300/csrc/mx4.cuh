@@ -191,6 +191,17 @@ __device__ __forceinline__ void unpack_raw(const Raw<F32, W>& r, float* f) {
   }
 }
 
+// Sum over the row's threads: one warp, or the CTA (red: 32 floats of its own
+// for each of a row's sums, so that one barrier serves).
+__device__ __forceinline__ float row_sum(float v, float* red, bool one_warp) {
+  v = warp_sum(v);
+  if (one_warp) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int n = (blockDim.x + 31) >> 5, l = threadIdx.x & 31;
+  return warp_sum(l < n ? red[l] : 0.0f);
+}
+
 // ------------------------------------------------------------ bounded waits --
 // Waits for phase `parity` of the barrier for at most about `cycles` clock cycles;
 // false: not complete by then.  One loop, its tries suspended for at most a part of the

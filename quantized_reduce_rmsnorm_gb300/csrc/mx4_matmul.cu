@@ -11,12 +11,10 @@
 // memory and issues the products, four warps bring the result out.  (Issued under
 // `lane == 0` and not under an elected lane, 8192 x 8192 x 8192 took 374 us instead
 // of 262, before any other step.)
-#include <cuda.h>
-
 #include <algorithm>
 
 #include "block.h"
-#include "mx4.cuh"
+#include "tc.cuh"
 
 namespace fc {
 namespace {
@@ -52,27 +50,6 @@ struct Job {
 };
 
 // ------------------------------------------------------------- tcgen05 ----
-__device__ __forceinline__ void tmem_alloc(uint32_t* where, int cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)),
-               "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t at, int cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// Arrives on bar when all tcgen05 work that this thread issued is done.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
 // 32 rows of 16 bytes (512 neighbouring bytes) to four columns of the first 32
 // lanes, and again to the other three groups of 32 lanes.
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
@@ -86,32 +63,8 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, 
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
-// 16 neighbouring columns of this warp's 32 lanes.
-__device__ __forceinline__ void tc_load16(uint32_t tmem, uint32_t v[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-      "[%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(tmem));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// One lane of a converged warp.  The tcgen05 and TMA instructions are issued
-// under this predicate and not under `lane == 0`: the compiler knows it to be
-// uniform, and their operands then need no loop over the lanes.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
-// Shared-memory matrix descriptors: rows of 128 bytes with the 128-byte
-// swizzle, 1024 bytes from one group of eight rows to the next; and rows of 16
-// bytes without a swizzle, 128 bytes from group to group.
-__device__ __forceinline__ uint64_t desc_codes(uint32_t smem) {
-  return static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory matrix descriptor of scales: rows of 16 bytes without a swizzle, 128 bytes
+// from one group of eight rows to the next.
 __device__ __forceinline__ uint64_t desc_scales(uint32_t smem) {
   return static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
 }
@@ -129,13 +82,6 @@ __device__ __forceinline__ void store_out(const Job& j, int64_t t, int f, float 
     static_cast<__nv_bfloat16*>(j.out)[t * j.features + f] = __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // ------------------------------------------------ few tokens: k in parts --
 // With few tokens the weights' bytes count and there are fewer tiles than SMs:
 // the CTAs of a cluster take the parts of k of one tile, leave their sums in
@@ -143,18 +89,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 // in order (no atomics: the same bits every time).  Bound by the weights' bytes:
 // one token by 8192 x 8192, weights that are not in L2, 8.5 us, 4.2 TB/s (floor 5.3 us;
 // one CTA a tile 11.5); what is left is a launch, the first copies' latency and the join.
-__device__ __forceinline__ float4 ld_cluster(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
-}
-
 template <int BN>
 __global__ void __launch_bounds__(kThreads)
     k_mx4_matmul(const Job j, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x) {
@@ -243,8 +177,8 @@ __global__ void __launch_bounds__(kThreads)
           tc_copy_scales(sf + 4 * q, desc_scales(smem_u32(ssa + s * T::kSfBytes + q * 512)));
           tc_copy_scales(sf + 8 + 4 * q, desc_scales(smem_u32(ssb + s * T::kSfBytes + q * 512)));
         }
-        const uint64_t da = desc_codes(smem_u32(sa + s * T::kABytes));
-        const uint64_t db = desc_codes(smem_u32(sb + s * T::kBBytes));
+        const uint64_t da = desc_along_k(smem_u32(sa + s * T::kABytes));
+        const uint64_t db = desc_along_k(smem_u32(sb + s * T::kBBytes));
         const int steps = min(4, (j.H - i * kStageK + 63) / 64);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 64 elements: 32 bytes further along the row
@@ -354,23 +288,6 @@ struct Wide {
   static_assert(kTile + kStages * kSfCols <= kCols && kSmem <= 227 * 1024, "fits");
 };
 
-// The same as above for a pair of CTAs.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* where, int cols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free_pair(uint32_t at, int cols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
-}
-// Arrives on bar of both CTAs.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
 // Each CTA's shared memory to its own tensor memory.
 __device__ __forceinline__ void tc_copy_scales_pair(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
@@ -383,74 +300,6 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
-// Into this CTA's shared memory, counted on a barrier of the pair (a cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-// Arrives on bar of this CTA alone.
-__device__ __forceinline__ void tc_commit_own(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-template <int N>  // N * 32 neighbouring columns of this warp's 32 lanes
-__device__ __forceinline__ void tc_load_all(uint32_t tmem, uint32_t (&v)[N * 32]) {
-#pragma unroll
-  for (int b = 0; b < N; ++b) {
-    uint32_t* r = v + b * 32;
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(tmem + b * 32));
-  }
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// N * 64 neighbouring columns of 16 lanes (0 or 16 on from tmem's), as fragments of
-// 16 lanes by 8 columns: thread l has lane l / 4, columns 2 (l % 4) and the next, in
-// the first two of a fragment's four registers, and lane l / 4 + 8 in the others.
-template <int N>
-__device__ __forceinline__ void tc_load_fragments(uint32_t tmem, uint32_t (&v)[N * 32]) {
-#pragma unroll
-  for (int b = 0; b < N; ++b) {
-    uint32_t* r = v + b * 32;
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-        "[%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(tmem + b * 64));
-  }
-}
-// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: thread l's
-// register m holds row l / 4, columns 2 (l % 4) and the next of matrix m; `row` is
-// where column l % 8 of matrix l / 8 goes.
-__device__ __forceinline__ void store_transposed(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(a), "r"(b),
-               "r"(c), "r"(d)
-               : "memory");
-}
-
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
-               "r"(y), "r"(smem_u32(src))
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 template <bool OUT32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThreads, 1)
     k_mx4_matmul_wide(const Job j, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -552,8 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
         copy_scales(s, 0);
         for (int i = 0; i < stages_k; ++i) {
           const uint32_t sf = tmem + T::kTile + s * T::kSfCols;
-          const uint64_t da = desc_codes(smem_u32(sa + s * T::kCodeBytes));
-          const uint64_t db = desc_codes(smem_u32(sb + s * T::kCodeBytes));
+          const uint64_t da = desc_along_k(smem_u32(sa + s * T::kCodeBytes));
+          const uint64_t db = desc_along_k(smem_u32(sb + s * T::kCodeBytes));
           const int steps = min(4, (j.H - i * kStageK + 63) / 64);
           auto product = [&](int k) {
             if (k < steps)
@@ -658,66 +507,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
 }
 
 // ------------------------------------------------------------- launch ----
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
-// Codes [rows, H / 2 bytes] in boxes of 128 bytes by box_rows rows; bytes and
-// rows past the end read as 0.
+// Codes [rows, H / 2 bytes] in boxes of 128 bytes by box_rows rows.
 cudaError_t codes_map(CUtensorMap* m, const void* codes, int64_t rows, int H, int box_rows) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(H / 2), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(H / 2)};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t step[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, rows, H / 2, box_rows, 128, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-// out [rows, features] in boxes of 32 features by 16 tokens (bf16: 64-byte swizzle);
-// what lies past the end is not written.
+// out [rows, features] in boxes of 32 features by 16 tokens (bf16: 64-byte swizzle).
 cudaError_t out_map(CUtensorMap* m, const Mx4MatmulArgs& a) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.features), static_cast<cuuint64_t>(a.rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.features) * (a.out_f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {32, 16}, step[2] = {1, 1};
-  return fn(m, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides,
-            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, a.out_f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
+  return a.out_f32 ? matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.out, a.rows, a.features, 16, 32,
+                                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE)
+                   : matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.rows, a.features, 16, 32,
+                                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 // Scale tiles as rows of 128 bytes, two neighbouring tiles (1024 bytes) a box.
 cudaError_t scales_map(CUtensorMap* m, const uint8_t* scales, int64_t rows, int KT) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>((rows + 127) / 128) * KT * 4};
-  const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, 8}, step[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(scales), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
+  return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, scales, (rows + 127) / 128 * KT * 4, 128, 8, 128,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 template <bool OUT32>
@@ -744,21 +551,10 @@ cudaError_t launch(const Mx4MatmulArgs& a, const Job& j, int parts, cudaStream_t
   CUtensorMap mw, mx;
   if (cudaError_t e = codes_map(&mw, a.w_codes, a.features, a.H, kM)) return e;
   if (cudaError_t e = codes_map(&mx, a.x_codes, a.rows, a.H, BN)) return e;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = static_cast<unsigned>(parts);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.features + kM - 1) / kM), static_cast<unsigned>((a.rows + BN - 1) / BN),
-                     static_cast<unsigned>(parts));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Tile<BN>::kSmem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, j, mw, mx);
+  return launch_parts(kern,
+                      dim3(static_cast<unsigned>((a.features + kM - 1) / kM),
+                           static_cast<unsigned>((a.rows + BN - 1) / BN), static_cast<unsigned>(parts)),
+                      kThreads, Tile<BN>::kSmem, st, j, mw, mx);
 }
 
 }  // namespace

@@ -30,7 +30,9 @@ EXPORTS = (
     "fc_last_error", "fc_version", "fc_token_split", "fc_select_protocol", "fc_allgather_dequant",
     "fc_protocol_estimate", "fc_mx4_codes_bytes", "fc_mx4_scales_bytes", "fc_mx4_quantize",
     "fc_mx4_dequantize", "fc_mx4_matmul", "fc_block_norm", "fc_block_norm_backward_workspace",
-    "fc_block_norm_backward",
+    "fc_block_norm_backward", "fc_layer_norm", "fc_layer_norm_backward_workspace",
+    "fc_layer_norm_backward", "fc_fp8_scales", "fc_fp8_quantize", "fc_fp8_dequantize",
+    "fc_fp8_matmul", "fc_gated_ffn", "fc_gated_ffn_backward_workspace", "fc_gated_ffn_backward",
 )
 
 
@@ -68,6 +70,10 @@ class Mx4(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 class BlockNormSpec(ctypes.Structure):
     _fields_ = [("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
                 ("pre_weight", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
@@ -82,6 +88,7 @@ class BlockNormGrads(ctypes.Structure):
 
 
 KERNEL_AUTO, KERNEL_STREAM, KERNEL_TMA = 0, 1, 2
+ACT_SILU, ACT_GELU_TANH = 0, 1
 
 
 INT8_G128 = QSpec(FMT_INT8_SYM, 128)
@@ -141,6 +148,16 @@ def load(path: Optional[str] = None):
         "fc_block_norm": (i32, [P, P, i64, i64, i32, P, P, P, Mx4, P]),
         "fc_block_norm_backward_workspace": (ctypes.c_size_t, [i64, i64, i64]),
         "fc_block_norm_backward": (i32, [P, P, P, P, i64, i64, i32, P, P, P, P, P]),
+        "fc_layer_norm": (i32, [P, P, i64, i64, i32, P, P, f32, P, P, P, P]),
+        "fc_layer_norm_backward_workspace": (ctypes.c_size_t, [i64, i64]),
+        "fc_layer_norm_backward": (i32, [P, P, P, P, i64, i64, i32, P, P, P, P, P, P, P]),
+        "fc_fp8_scales": (ctypes.c_size_t, [i64, i64, i64]),
+        "fc_fp8_quantize": (i32, [P, i32, i64, i64, i64, Fp8, P]),
+        "fc_fp8_dequantize": (i32, [Fp8, i64, i64, i64, P, i32, P]),
+        "fc_fp8_matmul": (i32, [Fp8, Fp8, i64, i64, i64, P, i32, P, P]),
+        "fc_gated_ffn": (i32, [P, P, P, i64, i64, i64, i32, P, P, P, P, P]),
+        "fc_gated_ffn_backward_workspace": (ctypes.c_size_t, [i64, i64]),
+        "fc_gated_ffn_backward": (i32, [P, P, P, P, P, P, i64, i64, i64, i32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -686,3 +703,216 @@ def block_norm_backward(x: torch.Tensor, h: Optional[torch.Tensor], dy: Optional
     where given, dresidual, dpost_weight, dpre_weight (fp32) and dgate.  Keywords
     as block_norm's; workspace from alloc_block_norm_workspace."""
     _once(bind_block_norm_backward(x, h, dy, dh, dx, workspace, **kw), stream)
+
+
+# ------------------------------------------------------------- layer norm ---
+def bind_layer_norm(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None,
+                    residual_in: Optional[torch.Tensor] = None,
+                    residual_out: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                    stats: Optional[torch.Tensor] = None) -> DeviceBound:
+    rows, hidden = _rows_hidden(x)
+    P = ctypes.c_void_p
+    args = [P(_ptr(x)), P(_want(residual_in, x.shape, x.dtype, "residual_in")), rows, hidden,
+            _dtype(x, "x"), P(_want(weight, (hidden,), x.dtype, "weight")),
+            P(_want(bias, (hidden,), x.dtype, "bias")), eps,
+            P(_want(residual_out, x.shape, x.dtype, "residual_out")),
+            P(_want(y, x.shape, x.dtype, "y")),
+            P(_want(stats, (rows, 2), torch.float32, "stats")), None]
+    keep = (x, residual_in, weight, bias, residual_out, y, stats)
+    return DeviceBound(load().fc_layer_norm, args, 11, keep=keep, device=_one_device(*keep))
+
+
+def layer_norm(x: torch.Tensor, y: torch.Tensor, stream=None, **kw):
+    """Residual add and layer norm in one pass over the rows:
+
+    residual_out = x + residual_in
+    y            = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias, h = residual_out
+
+    x, y and, given together, residual_in and residual_out (without them h is x):
+    [rows, hidden], bf16 or fp32.  Keywords: weight and bias [hidden], each optional,
+    eps, and stats, fp32 [rows, 2], which receives each row's mean and inverse
+    deviation for layer_norm_backward."""
+    _once(bind_layer_norm(x, y, **kw), stream)
+
+
+def alloc_layer_norm_workspace(rows: int, hidden: int, device="cuda"):
+    """Workspace of one layer_norm_backward call at a time."""
+    n = load().fc_layer_norm_backward_workspace(rows, hidden)
+    return torch.empty(max(n, 32), dtype=torch.uint8, device=device)
+
+
+def bind_layer_norm_backward(h: torch.Tensor, stats: torch.Tensor, dy: torch.Tensor,
+                             dx: torch.Tensor, workspace: torch.Tensor,
+                             dh: Optional[torch.Tensor] = None,
+                             weight: Optional[torch.Tensor] = None,
+                             dweight: Optional[torch.Tensor] = None,
+                             dbias: Optional[torch.Tensor] = None,
+                             d_status: Optional[torch.Tensor] = None) -> DeviceBound:
+    rows, hidden = _rows_hidden(h)
+    need = load().fc_layer_norm_backward_workspace(rows, hidden)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    P = ctypes.c_void_p
+    args = [P(_ptr(h)), P(_want(stats, (rows, 2), torch.float32, "stats")),
+            P(_want(dy, h.shape, h.dtype, "dy")), P(_want(dh, h.shape, h.dtype, "dh")), rows, hidden,
+            _dtype(h, "h"), P(_want(weight, (hidden,), h.dtype, "weight")),
+            P(_want(dx, h.shape, h.dtype, "dx")),
+            P(_want(dweight, (hidden,), torch.float32, "dweight")),
+            P(_want(dbias, (hidden,), torch.float32, "dbias")), P(_ptr(workspace)),
+            P(_want(d_status, (2,), torch.int32, "d_status")), None]
+    keep = (h, stats, dy, dh, weight, dx, dweight, dbias, workspace, d_status)
+    return DeviceBound(load().fc_layer_norm_backward, args, 13, keep=keep, device=_one_device(*keep))
+
+
+def layer_norm_backward(h: torch.Tensor, stats: torch.Tensor, dy: torch.Tensor, dx: torch.Tensor,
+                        workspace: torch.Tensor, stream=None, **kw):
+    """Gradient of layer_norm.  h is what was normed (residual_out, or x), stats what the
+    forward pass wrote, dy the gradient of y; dx receives that of h, which is that of
+    x and of residual_in.  Keywords: dh (the gradient of residual_out by itself),
+    weight, dweight and dbias (fp32), d_status; workspace from
+    alloc_layer_norm_workspace."""
+    _once(bind_layer_norm_backward(h, stats, dy, dx, workspace, **kw), stream)
+
+
+# ------------------------------------------------ 8-bit floating point -----
+def fp8_scales(rows: int, hidden: int, block_rows: int = 1) -> int:
+    return load().fc_fp8_scales(rows, hidden, block_rows)
+
+
+def alloc_fp8(rows: int, hidden: int, block_rows: int = 1, device="cuda"):
+    """Caller-owned (codes, scales) of an 8-bit [rows, hidden] tensor with a scale for each
+    block of block_rows (1: an activation's, 128: a weight's) by 128."""
+    if hidden <= 0 or hidden % 16:
+        raise ValueError(f"hidden must be a positive multiple of 16 (got {hidden})")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128 (got {block_rows})")
+    return (torch.empty(rows, hidden, dtype=torch.uint8, device=device),
+            torch.empty(-(-rows // block_rows), -(-hidden // 128), dtype=torch.float32, device=device))
+
+
+def _fp8(q, rows: int, hidden: int, block_rows: int, name: str) -> Fp8:
+    codes, scales = q
+    if codes.dtype != torch.uint8 or tuple(codes.shape) != (rows, hidden):
+        raise ValueError(f"{name}'s codes must be [{rows}, {hidden}] uint8 "
+                         f"(got {tuple(codes.shape)} {codes.dtype})")
+    want = (-(-rows // block_rows), -(-hidden // 128))
+    if scales.dtype != torch.float32 or tuple(scales.shape) != want:
+        raise ValueError(f"{name}'s scales must be {want} float32 (got {tuple(scales.shape)} {scales.dtype})")
+    return Fp8(_ptr(codes), _ptr(scales))
+
+
+def _block_rows(q, rows: int) -> int:
+    """1 or 128, by the scales' rows (one row is the same block either way)."""
+    return 1 if q[1].dim() == 2 and q[1].shape[0] == rows else 128
+
+
+def bind_fp8_quantize(x: torch.Tensor, out) -> DeviceBound:
+    rows, hidden = _rows_hidden(x)
+    br = _block_rows(out, rows)
+    return DeviceBound(load().fc_fp8_quantize,
+                       [ctypes.c_void_p(_ptr(x)), _dtype(x, "x"), rows, hidden, br,
+                        _fp8(out, rows, hidden, br, "out"), None], 6,
+                       keep=(x, *out), device=_one_device(x, *out))
+
+
+def fp8_quantize(x: torch.Tensor, out, stream=None):
+    """Quantize [rows, hidden] bf16 or fp32 to 8-bit out = (codes, scales), in the blocks
+    that out was laid out for (alloc_fp8)."""
+    _once(bind_fp8_quantize(x, out), stream)
+
+
+def bind_fp8_dequantize(q, out: torch.Tensor) -> DeviceBound:
+    rows, hidden = _rows_hidden(out)
+    br = _block_rows(q, rows)
+    return DeviceBound(load().fc_fp8_dequantize,
+                       [_fp8(q, rows, hidden, br, "q"), rows, hidden, br, ctypes.c_void_p(_ptr(out)),
+                        _dtype(out, "out"), None], 6,
+                       keep=(*q, out), device=_one_device(*q, out))
+
+
+def fp8_dequantize(q, out: torch.Tensor, stream=None):
+    """out[rows, hidden] (bf16 or fp32) = the values q = (codes, scales) stands for."""
+    _once(bind_fp8_dequantize(q, out), stream)
+
+
+def bind_fp8_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None) -> DeviceBound:
+    rows, features = _rows_hidden(out)
+    if w[0].dim() != 2 or w[0].shape[0] != features:
+        raise ValueError(f"w's codes must be [{features}, hidden] (got {tuple(w[0].shape)})")
+    hidden = w[0].shape[1]
+    return DeviceBound(load().fc_fp8_matmul,
+                       [_fp8(x, rows, hidden, 1, "x"), _fp8(w, features, hidden, 128, "w"), rows,
+                        features, hidden, ctypes.c_void_p(_ptr(out)), _dtype(out, "out"),
+                        ctypes.c_void_p(_want(d_status, (2,), torch.int32, "d_status")), None], 8,
+                       keep=(*x, *w, out, d_status), device=_one_device(*x, *w, out, d_status))
+
+
+def fp8_matmul(x, w, out: torch.Tensor, d_status: Optional[torch.Tensor] = None, stream=None):
+    """out[rows, features] (bf16 or fp32) = x w^T of two 8-bit tensors: x = (codes, scales)
+    of [rows, hidden] with block_rows 1, w of [features, hidden] with block_rows 128."""
+    _once(bind_fp8_matmul(x, w, out, d_status), stream)
+
+
+# ------------------------------------------------- gated feed-forward ------
+def bind_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: torch.Tensor,
+                   activation: int = ACT_SILU, gate: Optional[torch.Tensor] = None,
+                   up: Optional[torch.Tensor] = None,
+                   d_status: Optional[torch.Tensor] = None) -> DeviceBound:
+    rows, hidden = _rows_hidden(x)
+    features, B, P = out.shape[-1], torch.bfloat16, ctypes.c_void_p
+    args = [P(_want(x, (rows, hidden), B, "x")), P(_want(w_gate, (features, hidden), B, "w_gate")),
+            P(_want(w_up, (features, hidden), B, "w_up")), rows, features, hidden, activation,
+            P(_want(out, (rows, features), B, "out")), P(_want(gate, (rows, features), B, "gate")),
+            P(_want(up, (rows, features), B, "up")),
+            P(_want(d_status, (2,), torch.int32, "d_status")), None]
+    keep = (x, w_gate, w_up, out, gate, up, d_status)
+    return DeviceBound(load().fc_gated_ffn, args, 11, keep=keep, device=_one_device(*keep))
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: torch.Tensor,
+              stream=None, **kw):
+    """The gated feed-forward block's projections, activation and product in one kernel:
+    out[rows, features] = act(x w_gate^T) * (x w_up^T), all bf16, x [rows, hidden], w_gate
+    and w_up [features, hidden].  Keywords: activation (ACT_SILU or ACT_GELU_TANH); gate
+    and up [rows, features], which receive the two projections for
+    gated_ffn_backward; d_status."""
+    _once(bind_gated_ffn(x, w_gate, w_up, out, **kw), stream)
+
+
+def alloc_gated_ffn_workspace(rows: int, features: int, device="cuda"):
+    """Workspace of one gated_ffn_backward call at a time."""
+    n = load().fc_gated_ffn_backward_workspace(rows, features)
+    return torch.empty(max(n, 32), dtype=torch.uint8, device=device)
+
+
+def bind_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                            gate: torch.Tensor, up: torch.Tensor, dout: torch.Tensor,
+                            workspace: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                            dw_gate: Optional[torch.Tensor] = None,
+                            dw_up: Optional[torch.Tensor] = None, activation: int = ACT_SILU,
+                            d_status: Optional[torch.Tensor] = None) -> DeviceBound:
+    rows, hidden = _rows_hidden(x)
+    features, B, P = dout.shape[-1], torch.bfloat16, ctypes.c_void_p
+    need = load().fc_gated_ffn_backward_workspace(rows, features)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    act, weight = (rows, features), (features, hidden)
+    args = [P(_want(x, (rows, hidden), B, "x")), P(_want(w_gate, weight, B, "w_gate")),
+            P(_want(w_up, weight, B, "w_up")), P(_want(gate, act, B, "gate")),
+            P(_want(up, act, B, "up")), P(_want(dout, act, B, "dout")), rows, features, hidden,
+            activation, P(_want(dx, (rows, hidden), B, "dx")), P(_want(dw_gate, weight, B, "dw_gate")),
+            P(_want(dw_up, weight, B, "dw_up")), P(_ptr(workspace)),
+            P(_want(d_status, (2,), torch.int32, "d_status")), None]
+    keep = (x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, workspace, d_status)
+    return DeviceBound(load().fc_gated_ffn_backward, args, 15, keep=keep, device=_one_device(*keep))
+
+
+def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
+                       up: torch.Tensor, dout: torch.Tensor, workspace: torch.Tensor, stream=None,
+                       **kw):
+    """Gradient of gated_ffn.  gate and up are the projections that the forward pass kept,
+    dout the gradient of out.  Keywords: dx and (both or neither) dw_gate and dw_up, bf16,
+    which receive the gradients; activation; d_status.  workspace from
+    alloc_gated_ffn_workspace."""
+    _once(bind_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, workspace, **kw), stream)
