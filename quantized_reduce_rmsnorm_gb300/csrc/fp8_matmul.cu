@@ -337,18 +337,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
       bool ok = true;
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs)
         for (int i = 0; i < j.KB; ++i) {
-          if (!mbar_wait_for(acc_free + b, acc_phase, j.wait) || !mbar_wait_for(full + s, phase, j.wait)) {
+          const uint64_t da = desc_along_k(smem_u32(sa + s * T::kCodeBytes));
+          const uint64_t db = desc_along_k(smem_u32(sb + s * T::kCodeBytes));
+          if (!mbar_wait_for(full + s, phase, j.wait) || !mbar_wait_for(acc_free + b, acc_phase, j.wait)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t da = desc_along_k(smem_u32(sa + s * T::kCodeBytes));
-          const uint64_t db = desc_along_k(smem_u32(sb + s * T::kCodeBytes));
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 elements
             tc_mma_e4m3_pair(tmem + b * T::kTile, da + 2 * k, db + 2 * k, idesc_e4m3(T::kTile, T::kTile), k > 0);
-          tc_commit_pair(empty + s);
           tc_commit_pair(acc_full + b);
+          tc_commit_pair(empty + s);
           if (++s == T::kStages) s = 0, phase ^= 1;
           if (++b == T::kBufs) b = 0, acc_phase ^= 1;
         }
@@ -362,6 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
     int b = 0;
     uint32_t phase = 0;
     bool there = true;
+    const uint32_t freed = cluster_addr(acc_free, 0);
     for (int tile = blockIdx.x >> 1; tile < tiles && there; tile += pairs) {
       const int2 at = grouped_tile(tile, tiles_m, tiles_n);
       const int64_t row0 = static_cast<int64_t>(at.x) * T::kTile + rank * T::kHalf + (warp & 3) * 32;
@@ -369,32 +370,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OUT32>::kThread
       // past the ends any scale serves: the sums there are 0 and are not stored
       const float* sx = j.x_scales + min(row0 + lane, j.rows - 1) * j.KB;
       const float* sw = j.w_scales + min(static_cast<int64_t>(col0 / kK), (j.features - 1) / kK) * j.KB;
-      float next = sx[0] * sw[0];
+      // the two scales of the next block are on their way while this one's sums are added
+      float fx = sx[0], fw = sw[0];
       float2 acc[T::kHalf / 2];
 #pragma unroll
       for (int c = 0; c < T::kHalf / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
       for (int i = 0; i < j.KB; ++i) {
-        const float2 f = dup2(next);
-        if (i + 1 < j.KB) next = sx[i + 1] * sw[i + 1];
+        const float2 f = dup2(fx * fw);
+        if (i + 1 < j.KB) fx = sx[i + 1], fw = sw[i + 1];
         there = mbar_wait_for(acc_full + b, phase, j.wait);
-        if (__any_sync(kFull, !there || *failed)) {
+        if (__any_sync(kFull, !there)) {
           there = false;
           give_up();
           break;
         }
         tc_fence_after();
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + b * T::kTile + half * T::kHalf;
+        // 16 columns at a time, the next 16 on their way
+        uint32_t v[2][16];
+        tc_load16_start(mine, v[0]);
+        tc_load16_wait(v[0]);
 #pragma unroll
-        for (int c = 0; c < T::kHalf; c += 32) {
-          uint32_t v[32];
-          tc_load_all<1>(mine + c, v);
+        for (int c = 0; c < T::kHalf / 16; ++c) {
+          if (c + 1 < T::kHalf / 16) tc_load16_start(mine + 16 * (c + 1), v[(c + 1) & 1]);
+          const uint32_t* u = v[c & 1];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            acc[c / 2 + k] = pfma(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f, acc[c / 2 + k]);
+          for (int k = 0; k < 8; ++k)
+            acc[8 * c + k] = pfma(make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), f, acc[8 * c + k]);
+          if (c + 1 < T::kHalf / 16) tc_load16_wait(v[(c + 1) & 1]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_free + b, 0));
+        if (lane == 0) mbar_arrive_cluster(freed + 8 * b);
         if (++b == T::kBufs) b = 0, phase ^= 1;
       }
       if (!there || row0 >= j.rows) continue;
