@@ -10,7 +10,9 @@
 //
 // x / s is taken as q = x r and one correction q + (x - q s) r, r = 1 / s rounded to
 // nearest: the remainder is exact, so the result is the quotient's rounding (Markstein,
-// IBM J. Res. Dev. 34, 1990), three operations a value and not a division.
+// IBM J. Res. Dev. 34, 1990), three operations a value and not a division.  They are
+// taken with -r, so that what comes is the quotient's negative and a zero's sign survives
+// the sums; the codes' signs are turned afterwards, four at once.
 #pragma once
 
 #include "mx4.cuh"
@@ -25,7 +27,7 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
 // Sixteen values by their scale, to codes.
 template <bool F32>
 __device__ __forceinline__ uint4 fp8_encode16(const Raw<F32, 16>& x, float scale) {
-  const float2 r = dup2(__frcp_rn(scale)), s = dup2(-scale);
+  const float2 r = dup2(-__frcp_rn(scale)), s = dup2(scale);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -37,7 +39,7 @@ __device__ __forceinline__ uint4 fp8_encode16(const Raw<F32, 16>& x, float scale
       q = pfma(pfma(q, s, v), r, q);
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[k]) : "f"(q.y), "f"(q.x));
     }
-    w[i] = h[0] | static_cast<uint32_t>(h[1]) << 16;
+    w[i] = (h[0] | static_cast<uint32_t>(h[1]) << 16) ^ 0x80808080u;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
