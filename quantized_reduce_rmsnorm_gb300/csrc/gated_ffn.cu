@@ -222,20 +222,33 @@ __global__ void __launch_bounds__(Few<BN>::kThreads, 2)
 // the eight result warps, each 32 rows by half the columns, round, stage and store one
 // tile while the products of the next run.
 //
-// One kernel for the three kinds of product.  An operand lies along k (its rows are the
-// matrix's rows) or across it (its rows are the matrix's columns, read as they lie):
-//   kForward: A = x, B = the gate's weight (the first CTA's half) and the other's
-//             (the second's), both along k: 256 tokens by 128 features of both.
-//   kInput:   A = dg, then du, along k; B = w_gate, then w_up, across: dx.
-//   kWeights: A = dg, or du, across k; B = x across k: dw_gate, then dw_up.
-enum Kind { kForward, kInput, kWeights };
+// An operand lies along k (its rows are the matrix's rows) or across it (its rows are the
+// matrix's columns, read as they lie).  The forward pass:
+//   A = x, B = the gate's weight (the first CTA's half) and the other's (the second's), both
+//   along k: 256 tokens by 128 features of both.
+// The gradient, in one launch, so that its products share the pairs out evenly:
+//   dx: A = dg, then du, along k; B = w_gate, then w_up, across;
+//   dw_gate, then dw_up: A = dg, or du, across k; B = x across k.
+// A pair's tiles of dx come first; pairs that have one more of them than others have
+// `ahead` tiles of the weights fewer, as many as take the time of one of dx.
+enum Pass { kForward, kBackward };
 
 struct Job {
   int32_t* status;
-  int64_t rows, cols;  // of one matrix of the output (kForward: of out)
+  int64_t rows, features;
   int64_t wait;        // cycles
-  int k;               // elements of k (kInput: of one of the two)
-  int keep;            // kForward: g and u are kept
+  int H;
+  int keep;            // forward: g and u are kept
+  int tiles_first;     // forward: all tiles; backward: those of dx
+  int tiles_weights;   // backward: those of both weights
+  int ahead;
+};
+
+// The tile of a pair's turn `step`; false: it has no more.
+struct Tile {
+  int m, n;       // in tiles of the output
+  int k_stages;
+  int weights;    // backward: 0 dx, 1 dw_gate, 2 dw_up
 };
 
 struct Wide {
@@ -249,17 +262,45 @@ struct Wide {
   static_assert(kCols <= 512 && kSmem <= 227 * 1024, "fits");
 };
 
-// The maps of A and B (the second of each for the other weight or its gradient) and of the
-// outputs (kForward: out, g, u; kWeights: one for each weight).
+// Matrices: forward 0 x, 1 w_gate, 2 w_up; backward 0 dg, 1 du, 2 w_gate, 3 w_up, 4 x.  Outputs:
+// forward out, g, u; backward dx, dw_gate, dw_up.
 struct Maps {
-  CUtensorMap a[2], b[2], o[3];
+  CUtensorMap in[5], out[3];
 };
 
-template <int KIND, int ACT>
+template <int PASS>
+__device__ __forceinline__ bool tile_of(const Job& j, int pair, int pairs, int step, Tile& t) {
+  constexpr int kTileN = PASS == kForward ? Wide::kHalf : Wide::kTile;
+  const int tiles_t = static_cast<int>((j.rows + Wide::kTile - 1) / Wide::kTile);  // of tokens
+  int tile = pair + step * pairs;
+  if (PASS == kForward || tile < j.tiles_first) {
+    if (PASS == kForward && tile >= j.tiles_first) return false;
+    const int cols = PASS == kForward ? static_cast<int>(j.features) : j.H;
+    const int2 at = grouped_tile(tile, tiles_t, (cols + kTileN - 1) / kTileN);
+    const int k = PASS == kForward ? (j.H + kK - 1) / kK : 2 * ((static_cast<int>(j.features) + kK - 1) / kK);
+    t = Tile{at.x, at.y, k, 0};
+    return true;
+  }
+  const int extra = j.tiles_first % pairs;  // pairs with one more tile of dx
+  step -= j.tiles_first / pairs + (pair < extra);
+  if (pair >= extra) {
+    tile = step * (pairs - extra) + pair - extra;
+    if (step >= j.ahead) tile = j.ahead * (pairs - extra) + (step - j.ahead) * pairs + pair - extra;
+  } else {
+    tile = j.ahead * (pairs - extra) + step * pairs + pair + pairs - extra;
+  }
+  if (tile >= j.tiles_weights) return false;
+  const int one = j.tiles_weights / 2, second = tile >= one;
+  const int tiles_m = (static_cast<int>(j.features) + Wide::kTile - 1) / Wide::kTile;
+  const int2 at = grouped_tile(tile - second * one, tiles_m, (j.H + Wide::kTile - 1) / Wide::kTile);
+  t = Tile{at.x, at.y, static_cast<int>((j.rows + kK - 1) / kK), 1 + second};
+  return true;
+}
+
+template <int PASS, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     k_gated_wide(const Job j, const __grid_constant__ Maps maps) {
   using T = Wide;
-  constexpr bool kAcrossA = KIND == kWeights, kAcrossB = KIND != kForward;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sa = base;                               // [stage] 128 rows of A
@@ -273,12 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
   volatile uint32_t* failed = tmem_at + 1;      // a role of either CTA gave up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1;
-  constexpr int kTileN = KIND == kForward ? T::kHalf : T::kTile;  // columns of the output
-  const int tiles_n = static_cast<int>((j.cols + kTileN - 1) / kTileN);
-  const int tiles_m = static_cast<int>((j.rows + T::kTile - 1) / T::kTile);
-  const int tiles_one = tiles_n * tiles_m, tiles = KIND == kWeights ? 2 * tiles_one : tiles_one;
-  const int stages_one = (j.k + kK - 1) / kK, stages_k = KIND == kInput ? 2 * stages_one : stages_one;
+  const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  Tile t;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
@@ -305,12 +342,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       int s = 0;
       uint32_t phase = 1;  // a first pass over the stages waits for nothing
       bool ok = true;
-      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
-        const int which_tile = tile >= tiles_one;
-        const int2 at = grouped_tile(tile - which_tile * tiles_one, tiles_m, tiles_n);
-        const int a0 = at.x * T::kTile + rank * T::kHalf;
-        const int b0 = KIND == kForward ? at.y * T::kHalf : at.y * T::kTile + rank * T::kHalf;
-        for (int i = 0; i < stages_k; ++i) {
+      for (int step = 0; ok && tile_of<PASS>(j, pair, pairs, step, t); ++step) {
+        const int a0 = t.m * T::kTile + rank * T::kHalf;
+        const int b0 = PASS == kForward ? t.n * T::kHalf : t.n * T::kTile + rank * T::kHalf;
+        for (int i = 0; i < t.k_stages; ++i) {
           if (!mbar_wait_for(empty + s, phase, j.wait)) {
             ok = false;
             break;
@@ -320,21 +355,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
           uint8_t* da = sa + s * T::kPartBytes;
           uint8_t* db = sb + s * T::kPartBytes;
           // what lies past the end of a tensor reads as 0
-          const int which = KIND == kInput ? i >= stages_one : which_tile;
-          const int k = KIND == kInput ? (i - which * stages_one) * kK : i * kK;
-          const CUtensorMap* ma = maps.a + (KIND == kForward ? 0 : which);
-          const CUtensorMap* mb = maps.b + (KIND == kForward ? rank : KIND == kInput ? which : 0);
-          if constexpr (kAcrossA) {
-            tma_load_2d_pair(da, ma, a0, k, bar);
-            tma_load_2d_pair(da + T::kPartBytes / 2, ma, a0 + 64, k, bar);
+          if constexpr (PASS == kForward) {
+            tma_load_2d_pair(da, maps.in, i * kK, a0, bar);
+            tma_load_2d_pair(db, maps.in + 1 + rank, i * kK, b0, bar);
           } else {
-            tma_load_2d_pair(da, ma, k, a0, bar);
-          }
-          if constexpr (kAcrossB) {
-            tma_load_2d_pair(db, mb, b0, k, bar);
-            tma_load_2d_pair(db + T::kPartBytes / 2, mb, b0 + 64, k, bar);
-          } else {
-            tma_load_2d_pair(db, mb, k, b0, bar);
+            const int half_k = t.k_stages >> 1;  // dx: stages of dg, then as many of du
+            const int which = t.weights ? t.weights - 1 : i >= half_k;
+            const int k = (t.weights ? i : i - which * half_k) * kK;
+            const CUtensorMap* ma = maps.in + which;
+            const CUtensorMap* mb = maps.in + (t.weights ? 4 : 2 + which);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 64 rows of an operand each
+              const int row = a0 + 64 * h;
+              tma_load_2d_pair(da + h * (T::kPartBytes / 2), ma, t.weights ? row : k, t.weights ? k : row, bar);
+              tma_load_2d_pair(db + h * (T::kPartBytes / 2), mb, b0 + 64 * h, k, bar);
+            }
           }
           if (++s == T::kStages) s = 0, phase ^= 1;
         }
@@ -346,24 +381,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       int s = 0, b = 0;
       uint32_t phase = 0, acc_phase = 1;
       bool ok = true;
-      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
+      for (int step = 0; ok && tile_of<PASS>(j, pair, pairs, step, t); ++step) {
         if (!mbar_wait_for(acc_free + b, acc_phase, j.wait)) {
           ok = false;
           break;
         }
-        for (int i = 0; i < stages_k; ++i) {
+        const bool across = PASS == kBackward && t.weights;  // A's; B's is the pass's
+        const uint32_t idesc = idesc_bf16(T::kTile, T::kTile, across, PASS == kBackward);
+        const uint32_t step_a = across ? 128 : 2, step_b = PASS == kBackward ? 128 : 2;
+        for (int i = 0; i < t.k_stages; ++i) {
           if (!mbar_wait_for(full + s, phase, j.wait)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t a = smem_u32(sa + s * T::kPartBytes), bb = smem_u32(sb + s * T::kPartBytes);
-          const uint64_t da = kAcrossA ? desc_across_k(a, T::kPartBytes / 2) : desc_along_k(a);
-          const uint64_t db = kAcrossB ? desc_across_k(bb, T::kPartBytes / 2) : desc_along_k(bb);
+          const uint64_t da = across ? desc_across_k(a, T::kPartBytes / 2) : desc_along_k(a);
+          const uint64_t db = PASS == kBackward ? desc_across_k(bb, T::kPartBytes / 2) : desc_along_k(bb);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 16 elements
-            tc_mma_bf16_pair(tmem + b * T::kTile, da + (kAcrossA ? 128 : 2) * k, db + (kAcrossB ? 128 : 2) * k,
-                             idesc_bf16(T::kTile, T::kTile, kAcrossA, kAcrossB), i > 0 || k > 0);
+            tc_mma_bf16_pair(tmem + b * T::kTile, da + step_a * k, db + step_b * k, idesc, i > 0 || k > 0);
           tc_commit_pair(empty + s);
           if (++s == T::kStages) s = 0, phase ^= 1;
         }
@@ -402,20 +439,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_free + b, 0));
     };
     auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf2(__uint_as_float(lo), __uint_as_float(hi)); };
-    for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs) {
+    for (int step = 0; tile_of<PASS>(j, pair, pairs, step, t); ++step) {
       const bool there = mbar_wait_for(acc_full + b, phase, j.wait);
       if (__any_sync(kFull, !there || *failed)) {
         give_up();
         break;
       }
       tc_fence_after();
-      const int which = tile >= tiles_one;
-      const int2 at = grouped_tile(tile - which * tiles_one, tiles_m, tiles_n);
       const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + b * T::kTile;
-      const int64_t row0 = static_cast<int64_t>(at.x) * T::kTile + rank * T::kHalf + (warp & 3) * 32;
-      if constexpr (KIND == kForward) {
-        const int col0 = at.y * T::kHalf + half * 64;
-        const bool on = row0 < j.rows && col0 < j.cols;
+      const int64_t row0 = static_cast<int64_t>(t.m) * T::kTile + rank * T::kHalf + (warp & 3) * 32;
+      if constexpr (PASS == kForward) {
+        const int col0 = t.n * T::kHalf + half * 64;
+        const bool on = row0 < j.rows && col0 < j.features;
         uint32_t pg[2][16], pu[2][16];
         wait_stored();
 #pragma unroll
@@ -432,19 +467,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
           put(q, w);
         }
         release();
-        if (on) store(maps.o, col0, row0);
+        if (on) store(maps.out, col0, row0);
         if (j.keep) {
           wait_stored();
           put(0, pg[0]), put(1, pg[1]);
-          if (on) store(maps.o + 1, col0, row0);
+          if (on) store(maps.out + 1, col0, row0);
           wait_stored();
           put(0, pu[0]), put(1, pu[1]);
-          if (on) store(maps.o + 2, col0, row0);
+          if (on) store(maps.out + 2, col0, row0);
         }
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int col0 = at.y * T::kTile + half * T::kHalf + c * 64;
+          const int col0 = t.n * T::kTile + half * T::kHalf + c * 64;
           wait_stored();
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -455,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
             put(q, w);
           }
           if (c == 1) release();
-          if (row0 < j.rows && col0 < j.cols) store(maps.o + which, col0, row0);
+          if (row0 < (t.weights ? j.features : j.rows) && col0 < j.H) store(maps.out + t.weights, col0, row0);
         }
       }
       if (++b == T::kBufs) b = 0, phase ^= 1;
@@ -509,14 +544,20 @@ cudaError_t bf16_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, 
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int KIND, int ACT>
-cudaError_t launch_wide(const Job& j, const Maps& maps, cudaStream_t st) {
-  auto* kern = k_gated_wide<KIND, ACT>;
+template <int PASS, int ACT>
+cudaError_t launch_wide(Job j, const Maps& maps, cudaStream_t st) {
+  auto* kern = k_gated_wide<PASS, ACT>;
   if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Wide::kSmem)) return e;
-  const int tile_n = KIND == kForward ? Wide::kHalf : Wide::kTile;
-  const int64_t tiles = (j.cols + tile_n - 1) / tile_n * ((j.rows + Wide::kTile - 1) / Wide::kTile) * (KIND == kWeights ? 2 : 1);
-  const int64_t pairs = std::min<int64_t>(tiles, num_sms() / 2);
+  const int pairs = std::min(j.tiles_first + j.tiles_weights, num_sms() / 2);
+  // as many tiles of the weights as take the time of one of dx, by their stages of k and
+  // about eight that a tile takes besides
+  const int64_t k_in = 2 * ((j.features + kK - 1) / kK) + 8, k_weights = (j.rows + kK - 1) / kK + 8;
+  j.ahead = static_cast<int>((k_in + k_weights / 2) / k_weights);
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Wide::kThreads), Wide::kSmem, st, j, maps);
+}
+
+int wide_tiles(int64_t rows, int64_t cols, int of_cols) {
+  return static_cast<int>((rows + Wide::kTile - 1) / Wide::kTile * ((cols + of_cols - 1) / of_cols));
 }
 
 template <int BN>
@@ -545,15 +586,16 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
   while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
   if (a.rows > 128 && parts == 1) {
     Maps m{};
-    if (cudaError_t e = bf16_map(m.a, a.x, a.rows, a.H, Wide::kHalf)) return e;
-    if (cudaError_t e = bf16_map(m.b, a.w_gate, a.features, a.H, Wide::kHalf)) return e;
-    if (cudaError_t e = bf16_map(m.b + 1, a.w_up, a.features, a.H, Wide::kHalf)) return e;
-    if (cudaError_t e = bf16_map(m.o, a.out, a.rows, a.features, 32)) return e;
+    if (cudaError_t e = bf16_map(m.in, a.x, a.rows, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.in + 1, a.w_gate, a.features, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.in + 2, a.w_up, a.features, a.H, Wide::kHalf)) return e;
+    if (cudaError_t e = bf16_map(m.out, a.out, a.rows, a.features, 32)) return e;
     if (a.gate) {
-      if (cudaError_t e = bf16_map(m.o + 1, a.gate, a.rows, a.features, 32)) return e;
-      if (cudaError_t e = bf16_map(m.o + 2, a.up, a.rows, a.features, 32)) return e;
+      if (cudaError_t e = bf16_map(m.out + 1, a.gate, a.rows, a.features, 32)) return e;
+      if (cudaError_t e = bf16_map(m.out + 2, a.up, a.rows, a.features, 32)) return e;
     }
-    const Job j{a.status, a.rows, a.features, wait_cycles, a.H, a.gate != nullptr};
+    const Job j{a.status, a.rows, a.features, wait_cycles, a.H, a.gate != nullptr,
+                wide_tiles(a.rows, a.features, Wide::kHalf), 0, 0};
     return a.activation == kSilu ? launch_wide<kForward, kSilu>(j, m, st) : launch_wide<kForward, kGeluTanh>(j, m, st);
   }
   if (bn == 16) return launch_few<16>(a, parts, st);
@@ -570,27 +612,21 @@ cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
                                  dim3(static_cast<unsigned>((n / 16 + 255) / 256)), dim3(256), 0, st, a.gate, a.up,
                                  a.dout, n / 16, dg, du))
     return e;
-  if (a.dx) {
-    Maps m{};
-    if (cudaError_t e = bf16_map(m.a, dg, a.rows, a.features, Wide::kHalf)) return e;
-    if (cudaError_t e = bf16_map(m.a + 1, du, a.rows, a.features, Wide::kHalf)) return e;
-    if (cudaError_t e = bf16_map(m.b, a.w_gate, a.features, a.H, 64)) return e;
-    if (cudaError_t e = bf16_map(m.b + 1, a.w_up, a.features, a.H, 64)) return e;
-    if (cudaError_t e = bf16_map(m.o, a.dx, a.rows, a.H, 32)) return e;
-    const Job j{a.status, a.rows, a.H, wait_cycles, static_cast<int>(a.features), 0};
-    if (cudaError_t e = launch_wide<kInput, kSilu>(j, m, st)) return e;
-  }
+  Maps m{};
+  if (cudaError_t e = bf16_map(m.in, dg, a.rows, a.features, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 1, du, a.rows, a.features, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 2, a.w_gate, a.features, a.H, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 3, a.w_up, a.features, a.H, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 4, a.x, a.rows, a.H, 64)) return e;
+  if (a.dx)
+    if (cudaError_t e = bf16_map(m.out, a.dx, a.rows, a.H, 32)) return e;
   if (a.dw_gate) {
-    Maps m{};
-    if (cudaError_t e = bf16_map(m.a, dg, a.rows, a.features, 64)) return e;
-    if (cudaError_t e = bf16_map(m.a + 1, du, a.rows, a.features, 64)) return e;
-    if (cudaError_t e = bf16_map(m.b, a.x, a.rows, a.H, 64)) return e;
-    if (cudaError_t e = bf16_map(m.o, a.dw_gate, a.features, a.H, 32)) return e;
-    if (cudaError_t e = bf16_map(m.o + 1, a.dw_up, a.features, a.H, 32)) return e;
-    const Job j{a.status, a.features, a.H, wait_cycles, static_cast<int>(a.rows), 0};
-    if (cudaError_t e = launch_wide<kWeights, kSilu>(j, m, st)) return e;
+    if (cudaError_t e = bf16_map(m.out + 1, a.dw_gate, a.features, a.H, 32)) return e;
+    if (cudaError_t e = bf16_map(m.out + 2, a.dw_up, a.features, a.H, 32)) return e;
   }
-  return cudaSuccess;
+  const Job j{a.status, a.rows, a.features, wait_cycles, a.H, 0, a.dx ? wide_tiles(a.rows, a.H, Wide::kTile) : 0,
+              a.dw_gate ? 2 * wide_tiles(a.features, a.H, Wide::kTile) : 0, 0};
+  return launch_wide<kBackward, kSilu>(j, m, st);
 }
 
 }  // namespace fc

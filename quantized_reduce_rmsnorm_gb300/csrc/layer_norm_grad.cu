@@ -252,10 +252,9 @@ cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
   auto threads = [&](int W, int CL) { return (cols(CL) / W + 31) / 32 * 32; };
   auto stage = [&](int CL) { return (a.dh ? 3 : 2) * cols(CL) * (F32 ? 4 : 2); };
   auto stages = [&](int CL, int ctas) { return std::min(kMostStages, kMost / ctas / stage(CL)); };
-  if (const int n = stages(1, 2); n >= 2) {
-    const int t = threads(8, 1);
-    if (t <= 256) return launch_staged<F32, 8, 1, 256, 3>(job, t, n, n * stage(1), st);
-    if (t <= 640) return launch_staged<F32, 8, 1, 640, 2>(job, t, n, n * stage(1), st);
+  if (threads(8, 1) <= 640) {
+    const int n = stages(1, 1);
+    return launch_staged<F32, 8, 1, 640, 1>(job, threads(8, 1), n, n * stage(1), st);
   }
   if (threads(8, 1) <= 1024) {
     const int n = stages(1, 1);
