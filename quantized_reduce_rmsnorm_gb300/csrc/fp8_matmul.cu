@@ -35,16 +35,20 @@ struct Job {
 // block of the weight's, its columns are tokens: one token costs 16 columns, not 128
 // rows.  The CTAs of a cluster take the parts of k of one tile, leave their sums in their
 // shared memory, and each adds up a slice of the features over the parts, in order (no
-// atomics: the same bits every time).
+// atomics: the same bits every time).  The products of the tokens' scales and the
+// features' come a batch of blocks at a time, so that their loads wait together and not
+// block by block.
 template <int BN>
 struct Tile {
   static constexpr int kM = 128, kThreads = 192;  // warps 0-3: result; 4: copies; 5: products
-  static constexpr int kStages = BN >= 128 ? 3 : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;  // two CTAs an SM
+  static constexpr int kStages = BN >= 64 ? 4 : BN >= 32 ? 5 : 6;  // two CTAs an SM
   static constexpr int kABytes = kM * kK, kBBytes = BN * kK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBufs = BN >= 128 ? 2 : 4;  // block sums in tensor memory
+  static constexpr int kBufs = 4;  // block sums in tensor memory
   static constexpr int kCols = BN * kBufs;
-  static constexpr int kSmem = kStages * kStageBytes + 4 * BN * 4 + 1024 + 256;
+  static constexpr int kBatch = 16;  // blocks
+  static constexpr int kFactors = kBatch * BN;       // of a batch, for all tokens; two batches
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kFactors * 4 + 1024 + 256;
   static_assert(2 * kCols <= 512 && 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
@@ -56,8 +60,8 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sa = base;                                    // [stage][128 rows][128 bytes]
   uint8_t* sb = sa + T::kStages * T::kABytes;            // [stage][BN rows][128 bytes]
-  float* scale = reinterpret_cast<float*>(sb + T::kStages * T::kBBytes);  // [result warp][BN]
-  uint64_t* full = reinterpret_cast<uint64_t*>(scale + 4 * BN);
+  float* factors = reinterpret_cast<float*>(sb + T::kStages * T::kBBytes);  // [2][block of the batch][token]
+  uint64_t* full = reinterpret_cast<uint64_t*>(factors + 2 * T::kFactors);
   uint64_t* empty = full + T::kStages;
   uint64_t* acc_full = empty + T::kStages;   // [buffer] holds a block's sums
   uint64_t* acc_free = acc_full + T::kBufs;
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
   const uint32_t tmem = *tmem_at;
   pdl_begin();
 
-  float acc[BN];
+  float2 acc[BN / 2];
   bool there = true;
   if (warp == 4) {
     if (elect_one()) {
@@ -137,34 +141,42 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
       mbar_wait_bounded(ended, 0);  // before the memory that they use goes
     }
   } else {
-    // the tokens' scales of a block, times the features', BN to each warp
-    constexpr int kPer = (BN + 31) / 32;
-    float* mine = scale + warp * BN;
+    // a thread's factors of a batch: those of token e / kBatch, block e % kBatch, for e = its
+    // index and every 128th after it
+    constexpr int kPer = T::kFactors / 128;
     const float* sw = j.w_scales + static_cast<int64_t>(blockIdx.x) * j.KB;
-    const float* sx = j.x_scales + (t0 + lane) * j.KB;
-    auto scales_of = [&](int i, float (&v)[kPer]) {
-      const float w = sw[i];
+    const float* sx = j.x_scales + t0 * j.KB;
+    float next[kPer];
+    auto fetch = [&](int first) {
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        const int t = q * 32 + lane;
-        v[q] = t < BN && t0 + t < j.rows ? sx[static_cast<int64_t>(q * 32) * j.KB + i] * w : 0.0f;
+        const int e = q * 128 + threadIdx.x, t = e / T::kBatch, i = first + e % T::kBatch;
+        next[q] = i < i1 && t0 + t < j.rows ? sx[static_cast<int64_t>(t) * j.KB + i] * sw[i] : 0.0f;
       }
     };
-    float next[kPer];
-    scales_of(i0, next);
+    fetch(i0);
 #pragma unroll
-    for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < BN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+    auto sum = [&](int c) { return c & 1 ? acc[c / 2].y : acc[c / 2].x; };
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     int b = 0;
     uint32_t phase = 0;
     for (int i = i0; i < i1; ++i) {
+      const int in = (i - i0) % T::kBatch;
+      float* batch = factors + ((i - i0) / T::kBatch & 1) * T::kFactors;
+      if (in == 0) {
+        // whoever is still at the batch before this one does not read this half
 #pragma unroll
-      for (int q = 0; q < kPer; ++q)
-        if (q * 32 + lane < BN) mine[q * 32 + lane] = next[q];
-      __syncwarp();
-      if (i + 1 < i1) scales_of(i + 1, next);
-      there = __all_sync(kFull, mbar_wait_for(acc_full + b, phase, j.wait));
-      if (!there) break;
+        for (int q = 0; q < kPer; ++q) {
+          const int e = q * 128 + threadIdx.x;
+          batch[e % T::kBatch * BN + e / T::kBatch] = next[q];
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (i + T::kBatch < i1) fetch(i + T::kBatch);
+      }
+      const float* mine = batch + in * BN;
+      // a wait that runs out ends the tile: the ones after it do not wait
+      there = __all_sync(kFull, mbar_wait_for(acc_full + b, phase, there ? j.wait : 0) && there);
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < BN; c += 16) {
@@ -173,10 +185,9 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           const float4 f = *reinterpret_cast<const float4*>(mine + c + k);
-          acc[c + k] = __fmaf_rn(__uint_as_float(v[k]), f.x, acc[c + k]);
-          acc[c + k + 1] = __fmaf_rn(__uint_as_float(v[k + 1]), f.y, acc[c + k + 1]);
-          acc[c + k + 2] = __fmaf_rn(__uint_as_float(v[k + 2]), f.z, acc[c + k + 2]);
-          acc[c + k + 3] = __fmaf_rn(__uint_as_float(v[k + 3]), f.w, acc[c + k + 3]);
+          float2* a = acc + (c + k) / 2;
+          a[0] = pfma(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(f.x, f.y), a[0]);
+          a[1] = pfma(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(f.z, f.w), a[1]);
         }
       }
       tc_fence_before();
@@ -194,16 +205,16 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
       // a part without its sums makes NaN of the tile
 #pragma unroll
       for (int c = 0; c < BN; ++c)
-        if (c < tokens) part[c * T::kM + f] = there ? acc[c] : __uint_as_float(0x7FC00000u);
+        if (c < tokens) part[c * T::kM + f] = there ? sum(c) : __uint_as_float(0x7FC00000u);
     } else if (n0 + f < j.features && there) {
 #pragma unroll
       for (int c = 0; c < BN; ++c)
         if (c < tokens) {
           const int64_t at = (t0 + c) * j.features + n0 + f;
           if (j.out_f32)
-            static_cast<float*>(j.out)[at] = acc[c];
+            static_cast<float*>(j.out)[at] = sum(c);
           else
-            static_cast<__nv_bfloat16*>(j.out)[at] = __float2bfloat16_rn(acc[c]);
+            static_cast<__nv_bfloat16*>(j.out)[at] = __float2bfloat16_rn(sum(c));
         }
     }
   }
@@ -493,7 +504,7 @@ cudaError_t launch(const Fp8MatmulArgs& a, const Job& j, int parts, cudaStream_t
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, cudaStream_t st) {
   const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, wait_cycles,
               (a.H + kK - 1) / kK, a.out_f32 ? 1 : 0};
-  const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : 128;
+  const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64;
   const int64_t tiles = ((a.features + 127) / 128) * ((a.rows + bn - 1) / bn);
   int parts = 1;
   while (parts < kMostParts && parts * 8 <= j.KB && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
@@ -501,8 +512,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, cudaStream_t st) {
     return a.out_f32 ? launch_wide<true>(a, j, st) : launch_wide<false>(a, j, st);
   if (bn == 16) return launch<16>(a, j, parts, st);
   if (bn == 32) return launch<32>(a, j, parts, st);
-  if (bn == 64) return launch<64>(a, j, parts, st);
-  return launch<128>(a, j, parts, st);
+  return launch<64>(a, j, parts, st);
 }
 
 }  // namespace fc

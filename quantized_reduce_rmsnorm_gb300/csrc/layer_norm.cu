@@ -15,6 +15,8 @@
 // Bound by memory: x and r in, h and y out.  As in block_norm.cu a CTA holds a row in
 // registers, rows that fit one warp take one each, weights come from L1 where they are
 // used, and rows start for L2 before a CTA takes them.
+#include <algorithm>
+
 #include "block.h"
 #include "mx4.cuh"
 
@@ -31,28 +33,14 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float* red, bool one_warp) 
   return make_float2(warp_sum(l < n ? red[l] : 0.0f), warp_sum(l < n ? red[32 + l] : 0.0f));
 }
 
-// TEAM: one warp a row, four rows a CTA; else one row a CTA.  W: columns of a thread.
-template <bool F32, int W, bool TEAM, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) k_layer_norm(const LayerNormArgs a) {
-  __shared__ float red[3][32];
-  pdl_begin();
-  const uint32_t row = TEAM ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const int t = TEAM ? threadIdx.x & 31 : threadIdx.x;
-  const int e = t * W;
-  if (row >= a.rows) return;  // TEAM only: a whole warp
-  const bool live = e < a.H;
-  const int64_t at = static_cast<int64_t>(row) * a.H + e;
+// One row, by its team: TEAM one warp, else the CTA.  hr: the thread's columns of x.
+template <bool F32, int W, bool TEAM>
+__device__ __forceinline__ void norm_row(const LayerNormArgs& a, Raw<F32, W> hr, int64_t row, int e, bool live,
+                                         float (&red)[3][32]) {
+  const int64_t at = row * a.H + e;
   const float inv_n = 1.0f / static_cast<float>(a.H);
-  if (!TEAM && threadIdx.x == 0 && row + a.ahead < a.rows) {
-    const uint32_t bytes = a.H * (F32 ? 4 : 2);
-    const int64_t off = static_cast<int64_t>(row + a.ahead) * bytes;
-    prefetch_l2(static_cast<const char*>(a.x) + off, bytes);
-    if (a.res_in) prefetch_l2(static_cast<const char*>(a.res_in) + off, bytes);
-  }
-  Raw<F32, W> hr;
   float2 ss = make_float2(0.0f, 0.0f);
   if (live) {
-    hr = load_raw<F32, W>(a.x, at);
     if (a.res_in) {
       const Raw<F32, W> rr = load_raw<F32, W>(a.res_in, at);
       float2 u[W / 2];
@@ -78,18 +66,21 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm(const LayerNormArgs a
   const float d = s.x * inv_n;
   const float var = __fmaf_rn(-d, d, s.y * inv_n);
   const float inv = inv_sqrt((var < 0.0f ? 0.0f : var) + a.eps);  // NaN stays
-  if (a.stats && t == 0) *reinterpret_cast<float2*>(a.stats + 2 * static_cast<int64_t>(row)) = make_float2(mean + d, inv);
+  if (a.stats && e == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean + d, inv);
   if (!live) return;
+  const float2 vi = dup2(inv), shift = dup2(-d * inv);
   float2 u[W / 2];
 #pragma unroll
-  for (int i = 0; i < W / 2; ++i)
-    u[i] = pmul(padd(padd(pair<F32, W>(hr, i), minus), dup2(-d)), dup2(inv));
-  if (a.weight) {
+  for (int i = 0; i < W / 2; ++i) u[i] = pfma(padd(pair<F32, W>(hr, i), minus), vi, shift);
+  if (a.weight && a.bias) {
+    const Raw<F32, W> w = load_weight<F32, W>(a.weight, e), b = load_weight<F32, W>(a.bias, e);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) u[i] = pfma(u[i], pair<F32, W>(w, i), pair<F32, W>(b, i));
+  } else if (a.weight) {
     const Raw<F32, W> w = load_weight<F32, W>(a.weight, e);
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) u[i] = pmul(u[i], pair<F32, W>(w, i));
-  }
-  if (a.bias) {
+  } else if (a.bias) {
     const Raw<F32, W> b = load_weight<F32, W>(a.bias, e);
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) u[i] = padd(u[i], pair<F32, W>(b, i));
@@ -97,10 +88,58 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm(const LayerNormArgs a
   store_raw<F32, W>(a.y, at, pack_raw<F32, W>(u));
 }
 
+// TEAM: one warp a row, four rows a CTA; else one row a CTA.  W: columns of a thread.
+template <bool F32, int W, bool TEAM, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_layer_norm(const LayerNormArgs a) {
+  __shared__ float red[3][32];
+  pdl_begin();
+  const uint32_t row = TEAM ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int e = (TEAM ? threadIdx.x & 31 : threadIdx.x) * W;
+  if (row >= a.rows) return;  // TEAM only: a whole warp
+  const bool live = e < a.H;
+  if (!TEAM && threadIdx.x == 0 && row + a.ahead < a.rows) {
+    const uint32_t bytes = a.H * (F32 ? 4 : 2);
+    const int64_t off = static_cast<int64_t>(row + a.ahead) * bytes;
+    prefetch_l2(static_cast<const char*>(a.x) + off, bytes);
+    if (a.res_in) prefetch_l2(static_cast<const char*>(a.res_in) + off, bytes);
+  }
+  Raw<F32, W> hr;
+  if (live) hr = load_raw<F32, W>(a.x, static_cast<int64_t>(row) * a.H + e);
+  norm_row<F32, W, TEAM>(a, hr, row, e, live, red);
+}
+
+// A CTA takes row after row, without a residual: the next row's loads are on their way while
+// this one is summed (with a residual the four streams fill the memory's time as they are,
+// and two rows of registers would cost a CTA an SM).
 template <bool F32, int W, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_layer_norm_rows(const LayerNormArgs a) {
+  __shared__ float red[3][32];
+  pdl_begin();
+  const int e = threadIdx.x * W;
+  const bool live = e < a.H;
+  Raw<F32, W> next;
+  if (live) next = load_raw<F32, W>(a.x, static_cast<int64_t>(blockIdx.x) * a.H + e);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const Raw<F32, W> hr = next;
+    if (live && row + gridDim.x < a.rows) next = load_raw<F32, W>(a.x, (row + gridDim.x) * a.H + e);
+    norm_row<F32, W, false>(a, hr, row, e, live, red);
+  }
+}
+
+// MINB: CTAs an SM with a residual, of one row each; ROWS: without one, of rows in turn.
+template <bool F32, int W, int MAXT, int MINB, int ROWS>
 cudaError_t launch_rows(const LayerNormArgs& a, cudaStream_t st) {
-  return launch_pdl(k_layer_norm<F32, W, false, MAXT, MINB>, dim3(static_cast<unsigned>(a.rows)),
-                    dim3(static_cast<unsigned>((a.H / W + 31) / 32 * 32)), 0, st, a);
+  const int threads = (a.H / W + 31) / 32 * 32;
+  if (a.res_in)
+    return launch_pdl(k_layer_norm<F32, W, false, MAXT, MINB>, dim3(static_cast<unsigned>(a.rows)), dim3(threads), 0, st, a);
+  auto* kern = k_layer_norm_rows<F32, W, MAXT, ROWS>;
+  const int occ = occupancy_memo(reinterpret_cast<const void*>(kern), threads, 0, 1, [&] {
+    int v = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, 0);
+    return v;
+  });
+  const int64_t ctas = std::min<int64_t>(a.rows, static_cast<int64_t>(num_sms()) * std::max(occ, 1));
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), 0, st, a);
 }
 template <bool F32, int W>
 cudaError_t launch_teams(const LayerNormArgs& a, cudaStream_t st) {
@@ -114,11 +153,11 @@ cudaError_t launch_layer_norm(bool f32, LayerNormArgs a, cudaStream_t st) {
   a.ahead = num_sms();
   if (!f32) {
     if (a.H <= 512) return launch_teams<false, 16>(a, st);
-    return a.H > 8192 ? launch_rows<false, 16, 1024, 1>(a, st) : launch_rows<false, 16, 512, 3>(a, st);
+    return a.H > 8192 ? launch_rows<false, 16, 1024, 1, 1>(a, st) : launch_rows<false, 16, 512, 2, 2>(a, st);
   }
   if (a.H <= 256) return launch_teams<true, 8>(a, st);
-  if (a.H <= 5120) return launch_rows<true, 8, 640, 2>(a, st);
-  return a.H <= 8192 ? launch_rows<true, 8, 1024, 1>(a, st) : launch_rows<true, 16, 1024, 1>(a, st);
+  if (a.H <= 5120) return launch_rows<true, 8, 640, 3, 2>(a, st);
+  return a.H <= 8192 ? launch_rows<true, 8, 1024, 1, 1>(a, st) : launch_rows<true, 16, 1024, 1, 1>(a, st);
 }
 
 }  // namespace fc
