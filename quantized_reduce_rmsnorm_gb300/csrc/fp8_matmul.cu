@@ -37,7 +37,8 @@ struct Job {
 // shared memory, and each adds up a slice of the features over the parts, in order (no
 // atomics: the same bits every time).  The products of the tokens' scales and the
 // features' come a batch of blocks at a time, so that their loads wait together and not
-// block by block.
+// block by block.  Bound by the weights' bytes and a launch's start and join: one token by
+// 8192 x 8192 12.5 us, 5.4 TB/s (floor 9.9 us); 64 tokens 15.7, the result warps' time.
 template <int BN>
 struct Tile {
   static constexpr int kM = 128, kThreads = 192;  // warps 0-3: result; 4: copies; 5: products
@@ -263,6 +264,17 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, 2)
 // warps, each 32 tokens by 128 features (one block of the weight's), empty the other:
 // a thread has one token, so one factor, the product of the token's and the features'
 // scales, serves all 128 of its sums.
+// Bound by the turns of the two buffers: 8192 x 8192 x 8192 396 to 417 us, 2.7 PFLOP/s
+// (floor 288); the same products summed in tensor memory, read once a tile, take 327.  A
+// block takes about 780 cycles, of which the products 540: handing a buffer over
+// and back costs as much again as emptying it.  Steps: scales loaded where they are used
+// 1213; a block ahead, with 16 columns of sums on their way 945; buffers handed back
+// without a release to the whole cluster, which waits for every load and store of the
+// thread, 443; the products' warp asking for the copies before the buffer 405.  Not kept:
+// halves of 128 features with four buffers (418; the products alone are as fast), sixteen
+// result warps (470), warps that make the factors in shared memory (442), scales eight
+// blocks ahead by asynchronous copies (466), more registers for the result warps by
+// setmaxnreg and 32 columns on their way (437 to 550), one CTA a tile (461).
 template <bool OUT32>
 struct Wide {
   static constexpr int kTile = 256, kHalf = 128;
@@ -504,10 +516,20 @@ cudaError_t launch(const Fp8MatmulArgs& a, const Job& j, int parts, cudaStream_t
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, cudaStream_t st) {
   const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, wait_cycles,
               (a.H + kK - 1) / kK, a.out_f32 ? 1 : 0};
+  // Few tokens, in tiles of at most 64 (128 tokens 8192 x 8192: 23.3 us, in one tile of 128
+  // 26.2): a thread of that kernel has a feature, so each token's factor is a load, and
+  // the weights are read once for each tile of tokens.  k is cut into as many parts, of
+  // eight blocks at least, as keep two CTAs an SM; eight parts of 64 tokens only where there
+  // is then one, for their join (us, 1 / 2 / 4 / 8 parts: 1 token 8192 x 8192 16.8 / 14.8 /
+  // 12.5 / 15.6, 16 tokens 1024 x 8192 14.7 / 9.3 / 6.3 / 4.7, 64 tokens 4096 x 4096 15.6 /
+  // 10.8 / 9.0 / 10.1).  Above 128 tokens, and where k is not cut, the persistent kernel
+  // (us, it / few tokens: 300 tokens 4096 x 4096 17.3 / 21.0, 128 tokens 8192 x 8192 29.4 /
+  // 23.3; with k cut 200 tokens 4096 x 4096 17.1 / 14.1, 512 tokens 2048 x 8192 29.1 / 22.7).
   const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64;
   const int64_t tiles = ((a.features + 127) / 128) * ((a.rows + bn - 1) / bn);
   int parts = 1;
-  while (parts < kMostParts && parts * 8 <= j.KB && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  while (parts < kMostParts && parts * 8 <= j.KB && tiles * parts * 2 <= (bn == 64 && parts == 4 ? 1 : 2) * num_sms())
+    parts *= 2;
   if (a.rows > 128 && parts == 1)
     return a.out_f32 ? launch_wide<true>(a, j, st) : launch_wide<false>(a, j, st);
   if (bn == 16) return launch<16>(a, j, parts, st);

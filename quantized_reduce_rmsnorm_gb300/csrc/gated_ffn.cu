@@ -47,7 +47,8 @@ __device__ __forceinline__ float2 activate_slope(float z) {
 // gate and the same 64 of the other projection, its columns are tokens: one token costs
 // 16 columns, not 128 rows.  The CTAs of a cluster take the parts of k of one tile and
 // leave their sums in their shared memory, where the two projections of a feature meet;
-// each adds up a slice of the features over the parts, in order (no atomics).
+// each adds up a slice of the features over the parts, in order (no atomics).  Bound by the
+// weights' bytes: one token by 8192 x 8192 41.6 us, 6.5 TB/s (0.95 of the measured copy rate).
 struct FewJob {
   void* out;
   void* gate;
@@ -231,6 +232,13 @@ __global__ void __launch_bounds__(Few<BN>::kThreads, 2)
 //   dw_gate, then dw_up: A = dg, or du, across k; B = x across k.
 // A pair's tiles of dx come first; pairs that have one more of them than others have
 // `ahead` tiles of the weights fewer, as many as take the time of one of dx.
+//
+// Bound by the products: 4096 tokens by 8192 x 8192 forward 606 to 645 us, 1.7 to 1.8 PFLOP/s
+// (0.9 or more of the measured burst rate, the rate of long runs under the power limit),
+// the tensor pipe active 87 % of the time at 2048 x 4096 x 4096, where the last of 3.4 turns
+// of the tiles leaves pairs idle; the gradient of 4096 x 4096 x 8192 671 to 704 us, of which
+// the factors' kernel is 50, the tensor pipe active 94 % of the products' time (two launches
+// with tiles in turn: 698; 777 x 2064 x 4112 70 us against 52).
 enum Pass { kForward, kBackward };
 
 struct Job {
@@ -516,7 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 }
 
 // --------------------------------------------------- gradient's factors ---
-// dg and du of 16 neighbouring elements a thread.  Bound by memory: three tensors in, two out.
+// dg and du of 16 neighbouring elements a thread.  Bound by memory: three tensors in, two out,
+// 2048 x 4096 13.2 us, 6.4 TB/s.
 template <int ACT>
 __global__ void __launch_bounds__(256)
     k_gated_factors(const void* gate, const void* up, const void* dout, int64_t pieces, void* dg, void* du) {
@@ -586,8 +595,15 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
   const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 || small ? 64 : 128;
   const int64_t stages = (a.H + kK - 1) / kK;
   const int64_t tiles = ((a.features + 63) / 64) * ((a.rows + bn - 1) / bn);
+  // k in as many parts, of eight stages at least, as keep two CTAs an SM, as for the 8-bit
+  // product (us, 1 / 2 / 4 / 8 parts: 1 token 8192 x 8192 47.1 / 41.6 / 43.4 / 46.3, 1 token
+  // 4096 x 4096 16.9 / 14.8 / 12.6 / 15.7, 64 tokens 2048 x 4096 21.8 / 14.0 / 11.5 / 12.8).
+  // Above 128 tokens, and where k is not cut, the persistent kernel (us, it / few tokens: 333
+  // tokens 4112 x 2064 16.0 / 23.6; with k cut 200 tokens 4096 x 4096 23.3 / 21.0, 512 tokens
+  // 2048 x 4096 22.7 / 19.9).
   int parts = 1;
-  while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  while (parts < kMostParts && parts * 8 <= stages && tiles * parts * 2 <= (bn == 64 && parts == 4 ? 1 : 2) * num_sms())
+    parts *= 2;
   if (a.rows > 128 && parts == 1) {
     Maps m{};
     if (cudaError_t e = bf16_map(m.in, a.x, a.rows, a.H, Wide::kHalf)) return e;

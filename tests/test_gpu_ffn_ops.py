@@ -753,3 +753,52 @@ def test_what_the_binding_refuses():
         fc.gated_ffn(x, w, w, out, gate=torch.empty_like(out))
     with pytest.raises(fc.FcommError, match="asked for"):
         fc.gated_ffn_backward(x, w, w, out, out, out, fc.alloc_gated_ffn_workspace(8, 16))
+
+
+@pytest.mark.parametrize("rows", [1, 70, 300])
+def test_serving_step_captured_and_replayed(rows):
+    """Norm, projections, quantisation and product captured into one graph and replayed on new
+    inputs, launches without a wait between them: the bits of the calls one after another."""
+    s, s2 = layer(rows, 528, 1040, 9), layer(rows, 528, 1040, 9)
+    for c in s["calls"]:
+        c()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for c in s["calls"]:
+            c(side)
+    for k in range(3):
+        for t in (s, s2):
+            t["x"].copy_(randn(gen_of("serve", k), rows, 528, dtype=B16))
+        s["out"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        for c in s2["calls"]:
+            c()
+            torch.cuda.synchronize()
+        for name in ("h", "y", "a", "g", "u", "out"):
+            assert torch.isfinite(s[name]).all() and torch.equal(s[name], s2[name]), name
+
+
+def test_two_graphs_at_once():
+    """Two captured gradients, each with a workspace of its own, replayed on two streams at once."""
+    jobs = []
+    for k, (rows, features, hidden) in enumerate([(300, 528, 400), (130, 1040, 272)]):
+        i = ffn_grad_case(gen_of("graphs", k), rows, features, hidden)
+        want, out = ffn_grad_outputs(i), ffn_grad_outputs(i)
+        run_ffn_grad(i, want)
+        ws = fc.alloc_gated_ffn_workspace(rows, features)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            run_ffn_grad(i, out, ws=ws, stream=st)
+        jobs.append((i, want, out, ws, st, graph))
+    for _ in range(5):
+        for *_, st, graph in jobs:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, want, out, *_ in jobs:
+        assert all(torch.equal(want[k], out[k]) for k in want)
