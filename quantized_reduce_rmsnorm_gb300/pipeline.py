@@ -12,9 +12,9 @@ standing in as P slabs in one GPU's HBM:
   them.
 
 With a ``projection`` weight the step goes on into the next layer: y is
-quantized to microscaled 4-bit floating point and multiplied with the weight,
-which is quantized once, at construction; the product is one rank's partial
-sums of the next boundary.
+quantized to microscaled 4-bit floating point, or to 8-bit floating point with a
+scale for each block of 128, and multiplied with the weight, which is quantized
+once, at construction; the product is one rank's partial sums of the next boundary.
 
 With ``splits`` > 1 (BF16_TAGGED, INT8, INT4) the token rows are split into
 that many subsets whose fused calls run on their own streams (TokenWeave's
@@ -54,8 +54,10 @@ def qs_bytes(w: Workload, E: int) -> int:
 
 class Pipeline:
     def __init__(self, w: Workload, inputs: dict, device="cuda", with_payload=True,
-                 split: str = "even", projection: Optional[torch.Tensor] = None):
-        """projection: bf16 or fp32 [features, H] weight of the next projection, or None."""
+                 split: str = "even", projection: Optional[torch.Tensor] = None,
+                 projection_format: str = "mx4"):
+        """projection: bf16 or fp32 [features, H] weight of the next projection, or None, in
+        the format "mx4" or "fp8"."""
         self.w = w
         self.device = device
         self.spec = fc.QSpec(w.fmt, w.group)
@@ -97,10 +99,19 @@ class Pipeline:
         if projection is not None:
             if projection.dim() != 2 or projection.shape[1] != H:
                 raise ValueError(f"projection must be [features, {H}] (got {tuple(projection.shape)})")
+            if projection_format not in ("mx4", "fp8"):
+                raise ValueError(f"projection_format must be mx4 or fp8 (got {projection_format!r})")
             features = projection.shape[0]
-            self.weight = fc.alloc_mx4(features, H, device)
-            fc.mx4_quantize(projection.to(device).contiguous(), self.weight)
-            self.y_mx4 = fc.alloc_mx4(T, H, device)
+            self.fp8 = projection_format == "fp8"
+            projection = projection.to(device).contiguous()
+            if self.fp8:
+                self.weight = fc.alloc_fp8(features, H, 128, device)
+                fc.fp8_quantize(projection, self.weight)
+                self.y_fp8 = fc.alloc_fp8(T, H, 1, device)
+            else:
+                self.weight = fc.alloc_mx4(features, H, device)
+                fc.mx4_quantize(projection, self.weight)
+                self.y_mx4 = fc.alloc_mx4(T, H, device)
             self.out = torch.empty(T, features, dtype=torch.bfloat16, device=device)
             self.projection_status = torch.zeros(2, dtype=torch.int32, device=device)
         self.launches_per_step = self._launches()
@@ -112,9 +123,16 @@ class Pipeline:
         spends no host time converting arguments."""
         w = self.w
         self._send, self._fuse, self._split = None, None, []
-        self._project = [] if self.weight is None else [
-            fc.bind_mx4_quantize(self.y, self.y_mx4),
-            fc.bind_mx4_matmul(self.y_mx4, self.weight, self.out, d_status=self.projection_status)]
+        if self.weight is None:
+            self._project = []
+        elif self.fp8:
+            self._project = [
+                fc.bind_fp8_quantize(self.y, self.y_fp8),
+                fc.bind_fp8_matmul(self.y_fp8, self.weight, self.out, d_status=self.projection_status)]
+        else:
+            self._project = [
+                fc.bind_mx4_quantize(self.y, self.y_mx4),
+                fc.bind_mx4_matmul(self.y_mx4, self.weight, self.out, d_status=self.projection_status)]
         if w.fmt in (FMT_INT8_SYM, FMT_INT4_ASYM):
             self._send = fc.bind_group_quantize_multi(self.x, self.spec, self.codes)
             if max(1, w.splits) == 1:
@@ -258,7 +276,9 @@ class Pipeline:
         b = self._boundary_bytes()
         if self.weight is not None:
             features = self.out.shape[1]
-            b["projection"] = 2 * w.T * w.H + features * w.H // 2 + features * w.H // 32 + 2 * w.T * features
+            weight = features * w.H + 4 * self.weight[1].numel() if self.fp8 else \
+                features * w.H // 2 + features * w.H // 32
+            b["projection"] = 2 * w.T * w.H + weight + 2 * w.T * features
         return b
 
     def _boundary_bytes(self) -> dict:

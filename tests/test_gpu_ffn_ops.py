@@ -802,3 +802,36 @@ def test_two_graphs_at_once():
     torch.cuda.synchronize()
     for _, want, out, *_ in jobs:
         assert all(torch.equal(want[k], out[k]) for k in want)
+
+
+@pytest.mark.parametrize("name", ["decode", "prefill", "decode-qtagged"])
+def test_pipeline_into_an_8_bit_projection(name):
+    """The boundary's step with an 8-bit projection: h, y and the payload as without it, and
+    the product of the quantised y with the quantised weight."""
+    from quantized_reduce_rmsnorm_gb300 import synth
+    from quantized_reduce_rmsnorm_gb300.pipeline import Pipeline
+    w = synth.Workload(**{**synth.WORKLOADS[name].__dict__, "T": 48})
+    inp = synth.make_inputs(w, seed=3)
+    weight = randn(gen_of("projection", name), 1040, w.H, std=w.H ** -0.5, dtype=B16)
+    plain, pipe = Pipeline(w, inp), Pipeline(w, inp, projection=weight, projection_format="fp8")
+    assert pipe.launches_per_step == plain.launches_per_step + 3
+    assert set(pipe.alg_bytes()) == set(plain.alg_bytes()) | {"projection"}
+    plain.step()
+    pipe.step()
+    want, got = plain.outputs(), pipe.outputs()
+    for k in want:
+        assert want[k] is None and got[k] is None or (want[k] == got[k]).all(), k
+    assert got["projection_status"].tolist() == [0, fc.STATUS_NO_INDEX]
+    q = ref.quantise(pipe.y.cpu(), 1)
+    assert torch.equal(pipe.y_fp8[0].cpu(), q[0]) and torch.equal(pipe.y_fp8[1].cpu(), q[1])
+    xv = ref.values(q[0]) * ref.spread(q[1], 48, w.H)
+    wv = ref.values(pipe.weight[0]) * ref.spread(pipe.weight[1], 1040, w.H)
+    value, size = xv.cuda() @ wv.T, xv.abs().cuda() @ wv.abs().T
+    within(pipe.out, value, HALF[B16] * value.abs() + (256 + w.H // 128 + 10) * U * size, "out")
+    if name != "decode-qtagged":
+        pipe.capture()
+        pipe.out.zero_()
+        pipe.replay()
+        assert (pipe.outputs()["out"] == got["out"]).all()
+    with pytest.raises(ValueError, match="projection_format"):
+        Pipeline(w, inp, projection=weight, projection_format="fp4")
