@@ -154,6 +154,15 @@ struct GatedFfnArgs {
 };
 cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st);
 
+// Tokens whose dx the kernel of few tokens makes.
+constexpr int64_t kFewDx = 64;
+// bf16 numbers that stand for each of the gradient's factors dg and du, and that the
+// workspace holds: two for few tokens, whose gradients the weights' bytes bound, and where
+// there are few of them in all.
+constexpr int gated_ffn_terms(int64_t rows, int64_t features) {
+  return rows <= kFewDx || rows * features <= 1 << 17 ? 2 : 1;
+}
+
 struct GatedFfnGradArgs {
   const void* x;
   const void* w_gate;
@@ -164,7 +173,7 @@ struct GatedFfnGradArgs {
   void* dx;               // NULL: not wanted; so for the weights' two
   void* dw_gate;
   void* dw_up;
-  void* ws;               // [2][rows, features] bf16
+  void* ws;               // [terms][2][rows, features] bf16
   int32_t* status;
   int64_t rows;
   int64_t features;

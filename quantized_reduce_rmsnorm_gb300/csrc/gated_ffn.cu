@@ -8,9 +8,11 @@
 // All products are tcgen05.mma kind::f16 with binary32 sums in tensor memory; each result
 // is rounded once.  Both projections share a tile's copies of x, and their sums meet in
 // the thread that has a token's row of both, so g and u leave the chip only where the
-// caller keeps them (in bf16, for the gradient).  dg and du are rounded to bf16, as the
-// tensor core takes them, in the workspace; their rounding, at most 2^-9 of each term, is
-// within that of the results.
+// caller keeps them (in bf16, for the gradient).  dg and du go to the tensor core in bf16, by
+// the workspace.  In large products one bf16 number stands for each: its rounding, at most
+// 2^-9 of a term, is no more than a result's own, and independent from term to term.  In
+// small ones (gated_ffn_terms), where the errors of a few terms decide and more products cost
+// little, each is the sum of two bf16 numbers, 16 bits of it.
 #include <algorithm>
 
 #include "block.h"
@@ -229,7 +231,8 @@ __global__ void __launch_bounds__(Few<BN>::kThreads, 2)
 //   along k: 256 tokens by 128 features of both.
 // The gradient, in one launch, so that its products share the pairs out evenly:
 //   dx: A = dg, then du, along k; B = w_gate, then w_up, across;
-//   dw_gate, then dw_up: A = dg, or du, across k; B = x across k.
+//   dw_gate, then dw_up: A = dg, or du, across k; B = x across k;
+// both once more with the second terms of dg and du where there are any.
 // A pair's tiles of dx come first; pairs that have one more of them than others have
 // `ahead` tiles of the weights fewer, as many as take the time of one of dx.
 //
@@ -250,6 +253,7 @@ struct Job {
   int tiles_first;     // forward: all tiles; backward: those of dx
   int tiles_weights;   // backward: those of both weights
   int ahead;
+  int terms;           // backward: of dg and du
 };
 
 // The tile of a pair's turn `step`; false: it has no more.
@@ -270,10 +274,10 @@ struct Wide {
   static_assert(kCols <= 512 && kSmem <= 227 * 1024, "fits");
 };
 
-// Matrices: forward 0 x, 1 w_gate, 2 w_up; backward 0 dg, 1 du, 2 w_gate, 3 w_up, 4 x.  Outputs:
-// forward out, g, u; backward dx, dw_gate, dw_up.
+// Matrices: forward 0 x, 1 w_gate, 2 w_up; backward 0 dg, 1 du, 2 and 3 their second terms, 4
+// w_gate, 5 w_up, 6 x.  Outputs: forward out, g, u; backward dx, dw_gate, dw_up.
 struct Maps {
-  CUtensorMap in[5], out[3];
+  CUtensorMap in[7], out[3];
 };
 
 template <int PASS>
@@ -285,7 +289,7 @@ __device__ __forceinline__ bool tile_of(const Job& j, int pair, int pairs, int s
     if (PASS == kForward && tile >= j.tiles_first) return false;
     const int cols = PASS == kForward ? static_cast<int>(j.features) : j.H;
     const int2 at = grouped_tile(tile, tiles_t, (cols + kTileN - 1) / kTileN);
-    const int k = PASS == kForward ? (j.H + kK - 1) / kK : 2 * ((static_cast<int>(j.features) + kK - 1) / kK);
+    const int k = PASS == kForward ? (j.H + kK - 1) / kK : j.terms * 2 * ((static_cast<int>(j.features) + kK - 1) / kK);
     t = Tile{at.x, at.y, k, 0};
     return true;
   }
@@ -301,7 +305,7 @@ __device__ __forceinline__ bool tile_of(const Job& j, int pair, int pairs, int s
   const int one = j.tiles_weights / 2, second = tile >= one;
   const int tiles_m = (static_cast<int>(j.features) + Wide::kTile - 1) / Wide::kTile;
   const int2 at = grouped_tile(tile - second * one, tiles_m, (j.H + Wide::kTile - 1) / Wide::kTile);
-  t = Tile{at.x, at.y, static_cast<int>((j.rows + kK - 1) / kK), 1 + second};
+  t = Tile{at.x, at.y, j.terms * static_cast<int>((j.rows + kK - 1) / kK), 1 + second};
   return true;
 }
 
@@ -353,6 +357,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       for (int step = 0; ok && tile_of<PASS>(j, pair, pairs, step, t); ++step) {
         const int a0 = t.m * T::kTile + rank * T::kHalf;
         const int b0 = PASS == kForward ? t.n * T::kHalf : t.n * T::kTile + rank * T::kHalf;
+        // backward: k in runs, of dg, of du (dx alone) and of their second terms
+        const int run = PASS == kForward ? 0 : t.k_stages / (t.weights ? j.terms : 2 * j.terms);
+        int which = PASS == kBackward && t.weights ? t.weights - 1 : 0, in_run = 0;
         for (int i = 0; i < t.k_stages; ++i) {
           if (!mbar_wait_for(empty + s, phase, j.wait)) {
             ok = false;
@@ -367,11 +374,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
             tma_load_2d_pair(da, maps.in, i * kK, a0, bar);
             tma_load_2d_pair(db, maps.in + 1 + rank, i * kK, b0, bar);
           } else {
-            const int half_k = t.k_stages >> 1;  // dx: stages of dg, then as many of du
-            const int which = t.weights ? t.weights - 1 : i >= half_k;
-            const int k = (t.weights ? i : i - which * half_k) * kK;
+            const int k = in_run * kK;
             const CUtensorMap* ma = maps.in + which;
-            const CUtensorMap* mb = maps.in + (t.weights ? 4 : 2 + which);
+            const CUtensorMap* mb = maps.in + (t.weights ? 6 : 4 + (which & 1));
+            if (++in_run == run) in_run = 0, which += t.weights ? 2 : 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 64 rows of an operand each
               const int row = a0 + 64 * h;
@@ -523,12 +529,182 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
   }
 }
 
+// ------------------------------------- gradient of few tokens: k in parts --
+// dx of at most 64 tokens: again the weights' bytes count.  The tile's 128 rows are columns of
+// the weights (read across k, as they lie), its columns tokens: the first terms of dg and
+// du, then as many columns of the second terms, whose products cost no more bytes.  The
+// cluster's CTAs take the parts of k, which runs over the gate's features and then over the
+// other's, and join their sums as above.
+struct FewDxJob {
+  void* dx;
+  int32_t* status;
+  int64_t rows;
+  int64_t wait;     // cycles
+  int H;
+  int run;          // stages of k of one weight
+};
+
+template <int BN>
+struct FewDx {
+  static constexpr int kM = 128, kThreads = 192;  // warps 0-3: result; 4: copies; 5: products
+  static constexpr int kN = 2 * BN;
+  static constexpr int kStages = BN >= 64 ? 3 : BN >= 32 ? 4 : 5;  // two CTAs an SM
+  static constexpr int kABytes = kM * 128, kBBytes = kN * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+  static_assert(2 * kN <= 512 && 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(FewDx<BN>::kThreads, 2) k_gated_dx(const FewDxJob j, const __grid_constant__ Maps maps) {
+  using T = FewDx<BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sa = base;                                    // [stage][two blocks of 64 columns][64 k][128 bytes]
+  uint8_t* sb = sa + T::kStages * T::kABytes;            // [stage][first terms, second terms][BN rows][128 bytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + T::kStages * T::kBBytes);
+  uint64_t* empty = full + T::kStages;
+  uint64_t* done = empty + T::kStages;       // the accumulator holds this part's sums
+  uint64_t* ended = done + 1;                // all copies and products issued have ended
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ended + 1);
+  volatile uint32_t* failed = tmem_at + 1;
+  float* part = reinterpret_cast<float*>(base);          // [BN][128] sums, when the stages are done with
+  static_assert(BN * T::kM * 4 <= T::kStages * T::kStageBytes, "the sums fit where the stages were");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * T::kM;
+  const int parts = gridDim.z, part_id = blockIdx.z;     // a cluster is the parts of a tile
+  const int i0 = 2 * j.run * part_id / parts, i1 = 2 * j.run * (part_id + 1) / parts;
+  const int tokens = static_cast<int>(j.rows);           // at most BN
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    mbar_init(done, 1), mbar_init(ended, 2);
+    *failed = 0;
+    mbar_init_fence();
+  }
+  // taken before the next kernel may start, so that all of this grid's CTAs have theirs
+  if (warp == 5) tmem_alloc(tmem_at, T::kN);
+  if (warp == 4 && elect_one())
+    for (int i = i0; i < i1 && i < i0 + T::kStages; ++i) {
+      const CUtensorMap* w = maps.in + 4 + (i >= j.run);
+      const int k = (i >= j.run ? i - j.run : i) * kK;
+      tma_prefetch_2d(w, n0, k);
+      tma_prefetch_2d(w, n0 + 64, k);
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_begin();
+
+  if (warp == 4) {
+    if (elect_one()) {
+      int s = 0, used = 0;
+      uint32_t phase = 1;  // a first pass over the stages waits for nothing
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_for(empty + s, phase, j.wait)) {
+          *failed = 1;
+          break;
+        }
+        const int which = i >= j.run, k = (i - which * j.run) * kK;
+        mbar_expect_tx(full + s, T::kStageBytes);
+        tma_load_2d(sa + s * T::kABytes, maps.in + 4 + which, n0, k, full + s);
+        tma_load_2d(sa + s * T::kABytes + T::kABytes / 2, maps.in + 4 + which, n0 + 64, k, full + s);
+        tma_load_2d(sb + s * T::kBBytes, maps.in + which, k, 0, full + s);
+        tma_load_2d(sb + s * T::kBBytes + T::kBBytes / 2, maps.in + 2 + which, k, 0, full + s);
+        used = min(used + 1, T::kStages);
+        if (++s == T::kStages) s = 0, phase ^= 1;
+      }
+      // the last copies land before the CTA ends, also where the products gave up on them
+      for (int q = 0; q < used; ++q) {
+        if (--s < 0) s = T::kStages - 1, phase ^= 1;
+        mbar_wait_bounded(full + s, phase ^ 1);
+      }
+      mbar_arrive(ended);
+    }
+  } else if (warp == 5) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = i0; i < i1; ++i) {
+        if (!mbar_wait_for(full + s, phase, j.wait)) {
+          *failed = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t da = desc_across_k(smem_u32(sa + s * T::kABytes), T::kABytes / 2);
+        const uint64_t db = desc_along_k(smem_u32(sb + s * T::kBBytes));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 16 elements
+          tc_mma_bf16(tmem, da + 128 * k, db + 2 * k, idesc_bf16(T::kM, T::kN, true, false), i > i0 || k > 0);
+        tc_commit(empty + s);
+        if (++s == T::kStages) s = 0, phase ^= 1;
+      }
+      if (ok) tc_commit(done);
+      tc_commit(ended);
+      mbar_wait_bounded(ended, 0);  // before the memory that they use goes
+    }
+  } else {
+    const bool there = __all_sync(kFull, mbar_wait_for(done, 0, j.wait));
+    if (!there) *failed = 1;
+    mbar_wait_bounded(ended, 0);  // the sums go where the copies went
+    tc_fence_after();
+    __syncwarp();
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int c = 0; c < tokens; c += 16) {
+      uint32_t v[16], u[16];
+      tc_load16(mine + c, v);
+      tc_load16(mine + BN + c, u);
+      // a part without its sums makes NaN of the tile
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        part[(c + i) * T::kM + warp * 32 + lane] =
+            there ? __uint_as_float(v[i]) + __uint_as_float(u[i]) : __uint_as_float(0x7FC00000u);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();  // every part's sums are in its shared memory
+  const int shift = 5 - (31 - __clz(parts));  // log2 of the slice's groups of four columns
+  for (int k = threadIdx.x; k < tokens << shift; k += T::kThreads) {
+    const int t = k >> shift, f = ((part_id << shift) + (k & ((1 << shift) - 1))) * 4;
+    const float* p = part + t * T::kM + f;
+    float4 v[kMostParts], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int r = 0; r < kMostParts; ++r)
+      if (r < parts) v[r] = ld_cluster(cluster_addr(p, r));
+#pragma unroll
+    for (int r = 0; r < kMostParts; ++r)
+      if (r < parts) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+    if (n0 + f < j.H)  // a multiple of 16: all four or none
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.dx) + static_cast<int64_t>(t) * j.H + n0 + f) =
+          make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
+  }
+  __syncwarp();
+  cluster_sync_all();  // no part's memory goes before the others have read it
+  if (threadIdx.x == 0 && *failed && j.status) *j.status = kErrCuda;
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, T::kN);
+  }
+}
+
 // --------------------------------------------------- gradient's factors ---
+// v less its rounding r; 0 where r is not finite.
+__device__ __forceinline__ float2 rest(float2 v, float2 r) {
+  auto one = [](float a, float b) { return fabsf(b) < __uint_as_float(0x7F800000u) ? a - b : 0.0f; };
+  return make_float2(one(v.x, r.x), one(v.y, r.y));
+}
+
 // dg and du of 16 neighbouring elements a thread.  Bound by memory: three tensors in, two out,
 // 2048 x 4096 13.2 us, 6.4 TB/s.
-template <int ACT>
+template <int ACT, int TERMS>
 __global__ void __launch_bounds__(256)
-    k_gated_factors(const void* gate, const void* up, const void* dout, int64_t pieces, void* dg, void* du) {
+    k_gated_factors(const void* gate, const void* up, const void* dout, int64_t pieces, void* dg, void* du, void* dg2,
+                    void* du2) {
   pdl_begin();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= pieces) return;
@@ -542,8 +718,15 @@ __global__ void __launch_bounds__(256)
     a[k] = pmul(pmul(o, pair<false, 16>(u, k)), make_float2(x.y, y.y));
     b[k] = pmul(o, make_float2(x.x, y.x));
   }
-  store_raw<false, 16>(dg, i * 16, pack_raw<false, 16>(a));
-  store_raw<false, 16>(du, i * 16, pack_raw<false, 16>(b));
+  const Raw<false, 16> ra = pack_raw<false, 16>(a), rb = pack_raw<false, 16>(b);
+  store_raw<false, 16>(dg, i * 16, ra);
+  store_raw<false, 16>(du, i * 16, rb);
+  if constexpr (TERMS == 2) {  // what the rounding left; of an infinity or a NaN nothing more
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = rest(a[k], pair<false, 16>(ra, k)), b[k] = rest(b[k], pair<false, 16>(rb, k));
+    store_raw<false, 16>(dg2, i * 16, pack_raw<false, 16>(a));
+    store_raw<false, 16>(du2, i * 16, pack_raw<false, 16>(b));
+  }
 }
 
 // ------------------------------------------------------------- launch ----
@@ -560,9 +743,25 @@ cudaError_t launch_wide(Job j, const Maps& maps, cudaStream_t st) {
   const int pairs = std::min(j.tiles_first + j.tiles_weights, num_sms() / 2);
   // as many tiles of the weights as take the time of one of dx, by their stages of k and
   // about eight that a tile takes besides
-  const int64_t k_in = 2 * ((j.features + kK - 1) / kK) + 8, k_weights = (j.rows + kK - 1) / kK + 8;
+  const int64_t k_in = j.terms * 2 * ((j.features + kK - 1) / kK) + 8, k_weights = j.terms * ((j.rows + kK - 1) / kK) + 8;
   j.ahead = static_cast<int>((k_in + k_weights / 2) / k_weights);
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Wide::kThreads), Wide::kSmem, st, j, maps);
+}
+
+template <int BN>
+cudaError_t launch_few_dx(const GatedFfnGradArgs& a, Maps m, cudaStream_t st) {
+  using T = FewDx<BN>;
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k_gated_dx<BN>), T::kSmem)) return e;
+  auto* ws = static_cast<__nv_bfloat16*>(a.ws);
+  for (int k = 0; k < 4; ++k)
+    if (cudaError_t e = bf16_map(m.in + k, ws + k * a.rows * a.features, a.rows, a.features, BN)) return e;
+  const int run = static_cast<int>((a.features + kK - 1) / kK);
+  const int64_t tiles = (a.H + T::kM - 1) / T::kM;
+  int parts = 1;
+  while (parts < kMostParts && parts * 8 <= 2 * run && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  const FewDxJob j{a.dx, a.status, a.rows, wait_cycles, a.H, run};
+  return launch_parts(k_gated_dx<BN>, dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(parts)), T::kThreads,
+                      T::kSmem, st, j, m);
 }
 
 int wide_tiles(int64_t rows, int64_t cols, int of_cols) {
@@ -615,7 +814,7 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
       if (cudaError_t e = bf16_map(m.out + 2, a.up, a.rows, a.features, 32)) return e;
     }
     const Job j{a.status, a.rows, a.features, wait_cycles, a.H, a.gate != nullptr,
-                wide_tiles(a.rows, a.features, Wide::kHalf), 0, 0};
+                wide_tiles(a.rows, a.features, Wide::kHalf), 0, 0, 1};
     return a.activation == kSilu ? launch_wide<kForward, kSilu>(j, m, st) : launch_wide<kForward, kGeluTanh>(j, m, st);
   }
   if (bn == 16) return launch_few<16>(a, parts, st);
@@ -626,26 +825,37 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   const int64_t n = a.rows * a.features;
-  void* dg = a.ws;
-  void* du = static_cast<__nv_bfloat16*>(a.ws) + n;
-  if (cudaError_t e = launch_pdl(a.activation == kSilu ? k_gated_factors<kSilu> : k_gated_factors<kGeluTanh>,
-                                 dim3(static_cast<unsigned>((n / 16 + 255) / 256)), dim3(256), 0, st, a.gate, a.up,
-                                 a.dout, n / 16, dg, du))
+  const int terms = gated_ffn_terms(a.rows, a.features);
+  auto* ws = static_cast<__nv_bfloat16*>(a.ws);  // [term][dg, du][rows, features]
+  auto* factors = terms == 2 ? a.activation == kSilu ? k_gated_factors<kSilu, 2> : k_gated_factors<kGeluTanh, 2>
+                             : a.activation == kSilu ? k_gated_factors<kSilu, 1> : k_gated_factors<kGeluTanh, 1>;
+  if (cudaError_t e = launch_pdl(factors, dim3(static_cast<unsigned>((n / 16 + 255) / 256)), dim3(256), 0, st, a.gate,
+                                 a.up, a.dout, n / 16, static_cast<void*>(ws), static_cast<void*>(ws + n),
+                                 static_cast<void*>(ws + 2 * n), static_cast<void*>(ws + 3 * n)))
     return e;
   Maps m{};
-  if (cudaError_t e = bf16_map(m.in, dg, a.rows, a.features, 64)) return e;
-  if (cudaError_t e = bf16_map(m.in + 1, du, a.rows, a.features, 64)) return e;
-  if (cudaError_t e = bf16_map(m.in + 2, a.w_gate, a.features, a.H, 64)) return e;
-  if (cudaError_t e = bf16_map(m.in + 3, a.w_up, a.features, a.H, 64)) return e;
-  if (cudaError_t e = bf16_map(m.in + 4, a.x, a.rows, a.H, 64)) return e;
-  if (a.dx)
+  for (int k = 0; k < 2 * terms; ++k)
+    if (cudaError_t e = bf16_map(m.in + k, ws + k * n, a.rows, a.features, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 4, a.w_gate, a.features, a.H, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 5, a.w_up, a.features, a.H, 64)) return e;
+  if (cudaError_t e = bf16_map(m.in + 6, a.x, a.rows, a.H, 64)) return e;
+  bool wide_dx = a.dx != nullptr;
+  if (a.dx && a.rows <= kFewDx) {
+    if (cudaError_t e = a.rows <= 16   ? launch_few_dx<16>(a, m, st)
+                        : a.rows <= 32 ? launch_few_dx<32>(a, m, st)
+                                       : launch_few_dx<64>(a, m, st))
+      return e;
+    wide_dx = false;
+    if (!a.dw_gate) return cudaSuccess;
+  }
+  if (wide_dx)
     if (cudaError_t e = bf16_map(m.out, a.dx, a.rows, a.H, 32)) return e;
   if (a.dw_gate) {
     if (cudaError_t e = bf16_map(m.out + 1, a.dw_gate, a.features, a.H, 32)) return e;
     if (cudaError_t e = bf16_map(m.out + 2, a.dw_up, a.features, a.H, 32)) return e;
   }
-  const Job j{a.status, a.rows, a.features, wait_cycles, a.H, 0, a.dx ? wide_tiles(a.rows, a.H, Wide::kTile) : 0,
-              a.dw_gate ? 2 * wide_tiles(a.features, a.H, Wide::kTile) : 0, 0};
+  const Job j{a.status, a.rows, a.features, wait_cycles, a.H, 0, wide_dx ? wide_tiles(a.rows, a.H, Wide::kTile) : 0,
+              a.dw_gate ? 2 * wide_tiles(a.features, a.H, Wide::kTile) : 0, 0, terms};
   return launch_wide<kBackward, kSilu>(j, m, st);
 }
 

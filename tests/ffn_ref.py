@@ -149,9 +149,11 @@ def gated_grad_reference(x, wg, wu, gate, up, dout, name):
     rel = (5 * p.abs() + 24) * U
     eg = rel * (d * u).abs() * (s + (z * dp).abs() * s * (torch.sigmoid(-p) + 1)) + 2.0 ** -110 * (d * u).abs()
     eu = rel * (d * a).abs() + 2.0 ** -110 * d.abs()
-    half = HALF[torch.bfloat16]
-    tg, tu = eg + half * dg.abs(), eu + half * du.abs()  # of dg and du as the products take them
+    # dg and du as the products take them: two bf16 numbers each for few tokens or few values, else one
+    terms = 2 if len(z) <= 64 or z.numel() <= 1 << 17 else 1
+    half = HALF[torch.bfloat16] ** terms
+    tg, tu = eg + half * dg.abs(), eu + half * du.abs()
     R, F = x.shape[0], wg.shape[0]
-    return {"dx": (dg @ wg + du @ wu, tg @ wg.abs() + tu @ wu.abs() + 2 * F * TC * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())),
-            "dw_gate": (dg.T @ x, tg.T @ x.abs() + R * TC * (dg.abs().T @ x.abs())),
-            "dw_up": (du.T @ x, tu.T @ x.abs() + R * TC * (du.abs().T @ x.abs()))}
+    return {"dx": (dg @ wg + du @ wu, tg @ wg.abs() + tu @ wu.abs() + 2 * F * terms * TC * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())),
+            "dw_gate": (dg.T @ x, tg.T @ x.abs() + R * terms * TC * (dg.abs().T @ x.abs())),
+            "dw_up": (du.T @ x, tu.T @ x.abs() + R * terms * TC * (du.abs().T @ x.abs()))}

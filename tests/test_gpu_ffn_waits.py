@@ -82,7 +82,15 @@ def test_wide_gated_ffn_that_gives_up(rows, features, hidden):
     give_up((fc.bind_gated_ffn(x, wg, wu, out, gate=gate, up=up, d_status=st), st), [out, gate, up], limits=FEW, times=1)
 
 
-@pytest.mark.parametrize("rows,features,hidden", [(200, 528, 272), (1100, 4368, 144)])
+@pytest.mark.parametrize("rows,features,hidden", [(5, 272, 160), (30, 512, 272), (64, 4112, 1040)])
+def test_gated_ffn_gradient_of_few_tokens_that_gives_up(rows, features, hidden):
+    x, wg, wu, d = ffn_tensors(rows, features, hidden)
+    dx, st = torch.empty_like(x), status_word()
+    call = fc.bind_gated_ffn_backward(x, wg, wu, d, d, d, fc.alloc_gated_ffn_workspace(rows, features), dx=dx, d_status=st)
+    give_up((call, st), [dx])
+
+
+@pytest.mark.parametrize("rows,features,hidden", [(20, 272, 528), (200, 528, 272), (1100, 4368, 144)])
 def test_gated_ffn_gradient_that_gives_up(rows, features, hidden):
     x, wg, wu, d = ffn_tensors(rows, features, hidden)
     outs, st = [torch.empty_like(t) for t in (x, wg, wu)], status_word()
