@@ -512,7 +512,7 @@ fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int6
  * gradient of out.  With dg = dout * up * act'(gate) and du = dout * act(gate):
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  * in bf16 after a binary32 sum, dg and du rounded to the sum of two bf16 numbers where
- * rows <= 64 or rows * features <= 2^17, to one above (as much again as the results' own
+ * rows <= 128 or rows * features <= 2^19, to one above (as much again as the results' own
  * rounding).  dx may be NULL, and both of dw_gate and dw_up, not all
  * three.  Sums run in a fixed order.  workspace: fc_gated_ffn_backward_workspace
  * bytes, 32-byte aligned, this call's own until it has run.  rows == 0 sets the

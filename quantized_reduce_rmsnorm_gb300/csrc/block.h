@@ -154,13 +154,15 @@ struct GatedFfnArgs {
 };
 cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st);
 
-// Tokens whose dx the kernel of few tokens makes.
-constexpr int64_t kFewDx = 64;
+// Tokens at most for which the kernel of few tokens makes dx.
+constexpr int64_t kFewDx = 128;
 // bf16 numbers that stand for each of the gradient's factors dg and du, and that the
 // workspace holds: two for few tokens, whose gradients the weights' bytes bound, and where
-// there are few of them in all.
+// there are few factors in all: with one the error of dw, as of its own rounding and as
+// much again, is then left to a few terms (1.41 times that of its rounding, and up to 1.6
+// of 250 drawn sizes with the fewest; above 2^20 factors up to 1.46).
 constexpr int gated_ffn_terms(int64_t rows, int64_t features) {
-  return rows <= kFewDx || rows * features <= 1 << 17 ? 2 : 1;
+  return rows <= kFewDx || rows * features <= 1 << 19 ? 2 : 1;
 }
 
 struct GatedFfnGradArgs {

@@ -530,8 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 }
 
 // ------------------------------------- gradient of few tokens: k in parts --
-// dx of at most 64 tokens: again the weights' bytes count.  The tile's 128 rows are columns of
-// the weights (read across k, as they lie), its columns tokens: the first terms of dg and
+// dx of at most 128 tokens: again the weights' bytes count.  The tile's 128 rows are columns
+// of the weights (read across k, as they lie), its columns tokens: the first terms of dg and
 // du, then as many columns of the second terms, whose products cost no more bytes.  The
 // cluster's CTAs take the parts of k, which runs over the gate's features and then over the
 // other's, and join their sums as above.
@@ -548,15 +548,17 @@ template <int BN>
 struct FewDx {
   static constexpr int kM = 128, kThreads = 192;  // warps 0-3: result; 4: copies; 5: products
   static constexpr int kN = 2 * BN;
-  static constexpr int kStages = BN >= 64 ? 3 : BN >= 32 ? 4 : 5;  // two CTAs an SM
+  static constexpr int kPerSm = BN >= 128 ? 1 : 2;  // CTAs
+  static constexpr int kStages = BN >= 128 ? 4 : BN >= 64 ? 3 : BN >= 32 ? 4 : 5;
   static constexpr int kABytes = kM * 128, kBBytes = kN * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
-  static_assert(2 * kN <= 512 && 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(kPerSm * kN <= 512 && kPerSm * (kSmem + 1024) <= 228 * 1024, "fits");
 };
 
 template <int BN>
-__global__ void __launch_bounds__(FewDx<BN>::kThreads, 2) k_gated_dx(const FewDxJob j, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(FewDx<BN>::kThreads, FewDx<BN>::kPerSm)
+    k_gated_dx(const FewDxJob j, const __grid_constant__ Maps maps) {
   using T = FewDx<BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -758,7 +760,7 @@ cudaError_t launch_few_dx(const GatedFfnGradArgs& a, Maps m, cudaStream_t st) {
   const int run = static_cast<int>((a.features + kK - 1) / kK);
   const int64_t tiles = (a.H + T::kM - 1) / T::kM;
   int parts = 1;
-  while (parts < kMostParts && parts * 8 <= 2 * run && tiles * parts * 2 <= 2 * num_sms()) parts *= 2;
+  while (parts < kMostParts && parts * 8 <= 2 * run && tiles * parts * 2 <= T::kPerSm * num_sms()) parts *= 2;
   const FewDxJob j{a.dx, a.status, a.rows, wait_cycles, a.H, run};
   return launch_parts(k_gated_dx<BN>, dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(parts)), T::kThreads,
                       T::kSmem, st, j, m);
@@ -840,10 +842,12 @@ cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   if (cudaError_t e = bf16_map(m.in + 5, a.w_up, a.features, a.H, 64)) return e;
   if (cudaError_t e = bf16_map(m.in + 6, a.x, a.rows, a.H, 64)) return e;
   bool wide_dx = a.dx != nullptr;
-  if (a.dx && a.rows <= kFewDx) {
+  // k in parts, for 65 to 128 tokens where it is long for the tiles there are.
+  if (a.dx && (a.rows <= 64 || (a.rows <= kFewDx && 2 * a.features >= a.H))) {
     if (cudaError_t e = a.rows <= 16   ? launch_few_dx<16>(a, m, st)
                         : a.rows <= 32 ? launch_few_dx<32>(a, m, st)
-                                       : launch_few_dx<64>(a, m, st))
+                        : a.rows <= 64 ? launch_few_dx<64>(a, m, st)
+                                       : launch_few_dx<128>(a, m, st))
       return e;
     wide_dx = false;
     if (!a.dw_gate) return cudaSuccess;

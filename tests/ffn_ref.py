@@ -150,7 +150,7 @@ def gated_grad_reference(x, wg, wu, gate, up, dout, name):
     eg = rel * (d * u).abs() * (s + (z * dp).abs() * s * (torch.sigmoid(-p) + 1)) + 2.0 ** -110 * (d * u).abs()
     eu = rel * (d * a).abs() + 2.0 ** -110 * d.abs()
     # dg and du as the products take them: two bf16 numbers each for few tokens or few values, else one
-    terms = 2 if len(z) <= 64 or z.numel() <= 1 << 17 else 1
+    terms = 2 if len(z) <= 128 or z.numel() <= 1 << 19 else 1
     half = HALF[torch.bfloat16] ** terms
     tg, tu = eg + half * dg.abs(), eu + half * du.abs()
     R, F = x.shape[0], wg.shape[0]

@@ -26,7 +26,7 @@ def test_sizes():
     assert ws(5, 64) == 5 * 64 * 8 and ws(10 ** 6, 64) == 608 * 64 * 8 and ws(0, 64) == 0
     ws = L.fc_gated_ffn_backward_workspace
     assert ws(5, 64) == 5 * 64 * 8 and ws(1 << 20, 1 << 14) == 1 << 36 and ws(0, 64) == 0
-    assert ws(64, 1 << 14) == 1 << 23 and ws(65, 1 << 14) == 65 << 16 and ws(128, 1024) == 1 << 20
+    assert ws(128, 1 << 14) == 1 << 24 and ws(129, 1 << 14) == 129 << 16 and ws(512, 1024) == 1 << 22
 
 
 # ------------------------------------------------------------ references ---

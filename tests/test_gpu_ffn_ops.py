@@ -18,7 +18,7 @@ value, an fp32 one u; a step of the tensor core's sum 2^-23 of the sum of the si
   of the blocks and the eight parts: (128 * 2 + blocks + 10) u of the sum of the sizes.
 * gated feed-forward: K steps of 2^-23 for each projection, carried through the activation
   (ffn_ref.gated_reference); its gradient with dg and du rounded to bf16, 2^-8 of each
-  of their terms, or, for up to 64 tokens or 2^17 values, to two bf16 numbers, 2^-16, then R,
+  of their terms, or, for up to 128 tokens or 2^19 values, to two bf16 numbers, 2^-16, then R,
   or twice the features, steps of 2^-23, for each of the one or two.
 """
 import pytest
@@ -457,7 +457,7 @@ def run_ffn_grad(i, out, name="silu", ws=None, stream=None, **kw):
 
 
 @pytest.mark.parametrize("name", list(ACT))
-@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES + [(33, 80, 8208), (65, 4112, 144)])
+@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES + [(33, 80, 8208), (65, 4112, 144), (128, 1040, 528), (127, 2064, 16)])
 def test_gated_ffn_backward(rows, features, hidden, name):
     i = ffn_grad_case(gen_of("ffng", rows, features, hidden, name), rows, features, hidden)
     out = ffn_grad_outputs(i)
