@@ -534,7 +534,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 // of the weights (read across k, as they lie), its columns tokens: the first terms of dg and
 // du, then as many columns of the second terms, whose products cost no more bytes.  The
 // cluster's CTAs take the parts of k, which runs over the gate's features and then over the
-// other's, and join their sums as above.
+// other's, and join their sums as above.  The whole gradient of 64 tokens, 4096 x 4096: 37.8
+// us, of which the bytes of the weights and their gradients take 20 (with every product in
+// the kernel of many tokens, and one term, 43.9).
 struct FewDxJob {
   void* dx;
   int32_t* status;
@@ -842,8 +844,11 @@ cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   if (cudaError_t e = bf16_map(m.in + 5, a.w_up, a.features, a.H, 64)) return e;
   if (cudaError_t e = bf16_map(m.in + 6, a.x, a.rows, a.H, 64)) return e;
   bool wide_dx = a.dx != nullptr;
-  // k in parts, for 65 to 128 tokens where it is long for the tiles there are.
-  if (a.dx && (a.rows <= 64 || (a.rows <= kFewDx && 2 * a.features >= a.H))) {
+  // dx of few tokens with k in parts, where k is long enough to pay for a launch of its own
+  // (us, in parts / with the weights' products: 64 tokens 4096 x 4096 37.8 / 76.6, 128 tokens
+  // 8192 x 4096 76 / 153, 128 x 2048 x 8192 44.3 / 48.9, 64 x 496 x 4096 14.8 / 16.3, 64 x 384 x
+  // 1024 13.2 / 12.3, 128 x 256 x 4096 16.2 / 11.5).
+  if (a.dx && a.rows <= kFewDx && a.features >= kFewDxFeatures) {
     if (cudaError_t e = a.rows <= 16   ? launch_few_dx<16>(a, m, st)
                         : a.rows <= 32 ? launch_few_dx<32>(a, m, st)
                         : a.rows <= 64 ? launch_few_dx<64>(a, m, st)

@@ -374,6 +374,9 @@ def test_fp8_product_with_far_scales(rows):
 FFN_SHAPES = [(1, 16, 16), (1, 144, 64), (3, 528, 400), (16, 128, 4096), (17, 272, 144), (40, 4112, 2064),
               (64, 512, 8192), (100, 272, 1040), (128, 128, 128), (129, 144, 272), (257, 1040, 528), (300, 4112, 256),
               (777, 528, 1168), (1300, 2576, 80)]
+# the gradient of few tokens with k in parts, and next to where it is not
+FEW_SHAPES = [(16, 1040, 272), (30, 528, 1040), (33, 80, 8208), (65, 4112, 144), (128, 1040, 528), (127, 2064, 16),
+              (128, 496, 272), (129, 4112, 144)]
 
 
 def ffn_case(g, rows, features, hidden):
@@ -457,7 +460,7 @@ def run_ffn_grad(i, out, name="silu", ws=None, stream=None, **kw):
 
 
 @pytest.mark.parametrize("name", list(ACT))
-@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES + [(33, 80, 8208), (65, 4112, 144), (128, 1040, 528), (127, 2064, 16)])
+@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES + FEW_SHAPES)
 def test_gated_ffn_backward(rows, features, hidden, name):
     i = ffn_grad_case(gen_of("ffng", rows, features, hidden, name), rows, features, hidden)
     out = ffn_grad_outputs(i)
@@ -473,7 +476,7 @@ def test_gated_ffn_backward(rows, features, hidden, name):
 
 
 @pytest.mark.parametrize("z", [0.0, 64.0])
-@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES)
+@pytest.mark.parametrize("rows,features,hidden", FFN_SHAPES + FEW_SHAPES)
 def test_gated_ffn_gradient_is_exact(rows, features, hidden, z):
     """Where the gate's projection is 0, SiLU is 0 and its slope 1/2; where it is 64, SiLU is 64
     and its slope 1 (in binary32).  With small whole numbers the gradients are exact."""

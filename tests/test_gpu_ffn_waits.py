@@ -82,7 +82,7 @@ def test_wide_gated_ffn_that_gives_up(rows, features, hidden):
     give_up((fc.bind_gated_ffn(x, wg, wu, out, gate=gate, up=up, d_status=st), st), [out, gate, up], limits=FEW, times=1)
 
 
-@pytest.mark.parametrize("rows,features,hidden", [(5, 272, 160), (30, 512, 272), (64, 4112, 1040)])
+@pytest.mark.parametrize("rows,features,hidden", [(5, 528, 160), (30, 512, 272), (64, 4112, 1040), (100, 1040, 528)])
 def test_gated_ffn_gradient_of_few_tokens_that_gives_up(rows, features, hidden):
     x, wg, wu, d = ffn_tensors(rows, features, hidden)
     dx, st = torch.empty_like(x), status_word()
