@@ -2,7 +2,9 @@
 // stand around the fused boundary: the norms of a block with its gate and
 // residual scale (block_norm.cu), their gradient (block_norm_grad.cu),
 // microscaled 4-bit quantisation (mx4.cu) and the product of microscaled
-// tensors (mx4_matmul.cu).
+// tensors (mx4_matmul.cu); and of those that a feed-forward block adds: layer norm
+// and its gradient (layer_norm.cu, layer_norm_grad.cu), 8-bit floating point and its
+// product (fp8.cu, fp8_matmul.cu), the gated feed-forward and its gradient (gated_ffn.cu).
 #pragma once
 
 #include "internal.h"

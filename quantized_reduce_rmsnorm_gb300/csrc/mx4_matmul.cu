@@ -262,8 +262,9 @@ __global__ void __launch_bounds__(kThreads)
 // shared memory and leave each CTA its 128 features by all 256 tokens.  A pair
 // loads a third less than two CTAs with tiles of their own: 35 KB a stage and CTA
 // (8192 x 8192 x 8192: 162 us against 170, with four stages of the five 169; with the
-// scales' moves between the products 160 us, with the waits of mbar_wait_for 153, 7.2
-// PFLOP/s, the tensor pipe active for four fifths of it).  An instruction takes 64
+// scales' moves between the products 160 us, with the waits of mbar_wait_for 153, with the
+// accumulator handed back without a release to the whole cluster 146, 7.5 PFLOP/s, the
+// tensor pipe active for four fifths of it).  An instruction takes 64
 // elements of k; those of 96 that this chip has, at half as much again, are not used.  Copies run
 // ahead into the next tile; the eight result warps take the accumulator into
 // registers (each 32 features by 128 tokens) and hand it back, so that the
