@@ -144,10 +144,11 @@ def gated_grad_reference(x, wg, wu, gate, up, dout, name):
     a, slope, p = activation(name, z)
     s = torch.sigmoid(p)
     dg, du = d * u * slope, d * a
-    # the slope's two terms: s, and z p' s (1 - s), each off by the sigmoid's error; 1 - s by U more
+    # the slope's two terms: s, off by rel of itself, and z p' s t with t = 1 - s, which is off by
+    # what s is, sigmoid(-p) rel (the exponential's share) and 4 U of it, and by its rounding
     dp = torch.ones_like(z) if name == "silu" else 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
     rel = (5 * p.abs() + 24) * U
-    eg = rel * (d * u).abs() * (s + (z * dp).abs() * s * (torch.sigmoid(-p) + 1)) + 2.0 ** -110 * (d * u).abs()
+    eg = (d * u).abs() * (s * rel + (z * dp).abs() * s * (2 * torch.sigmoid(-p) * rel + 6 * U)) + 2.0 ** -110 * (d * u).abs()
     eu = rel * (d * a).abs() + 2.0 ** -110 * d.abs()
     # dg and du as the products take them: two bf16 numbers each for few tokens or few values, else one
     terms = 2 if len(z) <= 128 or z.numel() <= 1 << 19 else 1

@@ -495,6 +495,30 @@ def test_gated_ffn_gradient_is_exact(rows, features, hidden, z):
         assert (out[k][1] == 7).all(), k
 
 
+@pytest.mark.parametrize("name", list(ACT))
+@pytest.mark.parametrize("rows,features", [(1, 208), (140, 4112)])
+def test_gated_ffn_gradient_of_far_projections(rows, features, name):
+    """Projections from the lowest number of the type to the highest: the activation and its
+    slope have their limits there.  One column of x is 1, one feature's weights are 1."""
+    hidden = 32
+    z = torch.cat([torch.linspace(-104, 104, 105), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e38, -3e38, 1e19, -1e19]),
+                   torch.linspace(-8, 8, 95)]).to(B16).cuda()
+    i = dict(x=torch.zeros(rows, hidden, dtype=B16, device="cuda"),
+             w_gate=torch.zeros(features, hidden, dtype=B16, device="cuda"),
+             w_up=torch.zeros(features, hidden, dtype=B16, device="cuda"),
+             gate=torch.zeros(rows, features, dtype=B16, device="cuda"),
+             up=torch.full((rows, features), 0.75, dtype=B16, device="cuda"),
+             dout=torch.zeros(rows, features, dtype=B16, device="cuda"))
+    i["gate"][0, :208], i["dout"][0, :208] = z, 0.5
+    i["x"][0, 0] = 1
+    i["w_gate"][:100, 1], i["w_up"][:105, 2] = 1, 1
+    out = ffn_grad_outputs(i)
+    run_ffn_grad(i, out, name)
+    want = ref.gated_grad_reference(*i.values(), name)
+    for k, (v, tol) in want.items():
+        within(out[k], v, HALF[B16] * v.abs() + tol, k)
+
+
 def test_gated_ffn_gradient_without_the_optional_outputs():
     i = ffn_grad_case(gen_of("optional"), 150, 272, 400)
     out = ffn_grad_outputs(i)
