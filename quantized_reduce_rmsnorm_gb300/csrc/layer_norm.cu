@@ -112,8 +112,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm(const LayerNormArgs a
 }
 
 // A CTA takes row after row, without a residual: the next row's loads are on their way while
-// this one is summed (with a residual the four streams fill the memory's time as they are,
-// and two rows of registers would cost a CTA an SM).
+// this one is summed (with a residual the four streams fill the memory's time as they are).
 template <bool F32, int W, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm_rows(const LayerNormArgs a) {
   __shared__ float red[3][32];
