@@ -156,7 +156,7 @@ struct GatedFfnArgs {
 };
 cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st);
 
-// Tokens at most, and features at least, for which the kernel of few tokens makes dx.
+// Tokens up to which, and features from which on, the kernel of few tokens makes dx.
 constexpr int64_t kFewDx = 128, kFewDxFeatures = 512;
 // bf16 numbers that stand for each of the gradient's factors dg and du, and that the
 // workspace holds: two for few tokens, whose gradients the weights' bytes bound, and where

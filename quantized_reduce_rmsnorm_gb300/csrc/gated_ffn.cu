@@ -531,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 }
 
 // ------------------------------------- gradient of few tokens: k in parts --
-// dx of at most 128 tokens: again the weights' bytes count.  The tile's 128 rows are columns
+// dx of few tokens: again the weights' bytes count.  The tile's 128 rows are columns
 // of the weights (read across k, as they lie), its columns tokens: the first terms of dg and
 // du, then as many columns of the second terms, whose products cost no more bytes.  The
 // cluster's CTAs take the parts of k, which runs over the gate's features and then over the
@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(FewDx<BN>::kThreads, FewDx<BN>::kPerSm)
   const int n0 = blockIdx.x * T::kM;
   const int parts = gridDim.z, part_id = blockIdx.z;     // a cluster is the parts of a tile
   const int i0 = 2 * j.run * part_id / parts, i1 = 2 * j.run * (part_id + 1) / parts;
-  const int tokens = static_cast<int>(j.rows);           // at most BN
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * BN;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(BN), j.rows - t0));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
@@ -615,8 +616,8 @@ __global__ void __launch_bounds__(FewDx<BN>::kThreads, FewDx<BN>::kPerSm)
         mbar_expect_tx(full + s, T::kStageBytes);
         tma_load_2d(sa + s * T::kABytes, maps.in + 4 + which, n0, k, full + s);
         tma_load_2d(sa + s * T::kABytes + T::kABytes / 2, maps.in + 4 + which, n0 + 64, k, full + s);
-        tma_load_2d(sb + s * T::kBBytes, maps.in + which, k, 0, full + s);
-        tma_load_2d(sb + s * T::kBBytes + T::kBBytes / 2, maps.in + 2 + which, k, 0, full + s);
+        tma_load_2d(sb + s * T::kBBytes, maps.in + which, k, static_cast<int>(t0), full + s);
+        tma_load_2d(sb + s * T::kBBytes + T::kBBytes / 2, maps.in + 2 + which, k, static_cast<int>(t0), full + s);
         used = min(used + 1, T::kStages);
         if (++s == T::kStages) s = 0, phase ^= 1;
       }
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(FewDx<BN>::kThreads, FewDx<BN>::kPerSm)
     for (int r = 0; r < kMostParts; ++r)
       if (r < parts) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
     if (n0 + f < j.H)  // a multiple of 16: all four or none
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.dx) + static_cast<int64_t>(t) * j.H + n0 + f) =
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(j.dx) + (t0 + t) * j.H + n0 + f) =
           make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
   }
   __syncwarp();
@@ -761,12 +762,13 @@ cudaError_t launch_few_dx(const GatedFfnGradArgs& a, Maps m, cudaStream_t st) {
   for (int k = 0; k < 4; ++k)
     if (cudaError_t e = bf16_map(m.in + k, ws + k * a.rows * a.features, a.rows, a.features, BN)) return e;
   const int run = static_cast<int>((a.features + kK - 1) / kK);
-  const int64_t tiles = (a.H + T::kM - 1) / T::kM;
+  const int64_t tiles_h = (a.H + T::kM - 1) / T::kM, tiles_t = (a.rows + BN - 1) / BN;
   int parts = 1;
-  while (parts < kMostParts && parts * 8 <= 2 * run && tiles * parts * 2 <= T::kPerSm * num_sms()) parts *= 2;
+  while (parts < kMostParts && parts * 8 <= 2 * run && tiles_h * tiles_t * parts * 2 <= T::kPerSm * num_sms()) parts *= 2;
   const FewDxJob j{a.dx, a.status, a.rows, wait_cycles, a.H, run};
-  return launch_parts(k_gated_dx<BN>, dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(parts)), T::kThreads,
-                      T::kSmem, st, j, m);
+  return launch_parts(k_gated_dx<BN>,
+                      dim3(static_cast<unsigned>(tiles_h), static_cast<unsigned>(tiles_t), static_cast<unsigned>(parts)),
+                      T::kThreads, T::kSmem, st, j, m);
 }
 
 int wide_tiles(int64_t rows, int64_t cols, int of_cols) {
@@ -845,11 +847,15 @@ cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   if (cudaError_t e = bf16_map(m.in + 5, a.w_up, a.features, a.H, 64)) return e;
   if (cudaError_t e = bf16_map(m.in + 6, a.x, a.rows, a.H, 64)) return e;
   bool wide_dx = a.dx != nullptr;
-  // dx of few tokens with k in parts, where k is long enough to pay for a launch of its own
-  // (us, in parts / with the weights' products: 64 tokens 4096 x 4096 37.8 / 76.6, 128 tokens
-  // 8192 x 4096 76 / 153, 128 x 2048 x 8192 44.3 / 48.9, 64 x 496 x 4096 14.8 / 16.3, 64 x 384 x
-  // 1024 13.2 / 12.3, 128 x 256 x 4096 16.2 / 11.5).
-  if (a.dx && a.rows <= kFewDx && a.features >= kFewDxFeatures) {
+  // dx with k in parts, where k is long enough to pay for a launch of its own (us, in parts /
+  // with the weights' products: 64 tokens 4096 x 4096 37.8 / 76.6, 128 tokens 8192 x 4096 76 /
+  // 153, 64 x 496 x 4096 14.8 / 16.3, 64 x 384 x 1024 13.2 / 12.3, 128 x 256 x 4096 16.2 / 11.5):
+  // of up to 128 tokens, and of more where tiles of 128 leave SMs idle and k is long
+  // beside the tokens (140 x 3696 x 4096 53 / 72, 300 x 1024 x 512 17.8 / 23.7, 500 x 1024 x 512
+  // 26.8 / 24.9).
+  const int64_t tiles = (a.H + 127) / 128 * ((a.rows + 127) / 128);
+  const bool long_k = a.features >= kFewDxFeatures && a.features >= 3 * a.rows && tiles * 2 <= num_sms();
+  if (a.dx && (a.rows <= kFewDx ? a.features >= kFewDxFeatures : terms == 2 && long_k)) {
     if (cudaError_t e = a.rows <= 16   ? launch_few_dx<16>(a, m, st)
                         : a.rows <= 32 ? launch_few_dx<32>(a, m, st)
                         : a.rows <= 64 ? launch_few_dx<64>(a, m, st)

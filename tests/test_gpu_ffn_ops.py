@@ -374,9 +374,9 @@ def test_fp8_product_with_far_scales(rows):
 FFN_SHAPES = [(1, 16, 16), (1, 144, 64), (3, 528, 400), (16, 128, 4096), (17, 272, 144), (40, 4112, 2064),
               (64, 512, 8192), (100, 272, 1040), (128, 128, 128), (129, 144, 272), (257, 1040, 528), (300, 4112, 256),
               (777, 528, 1168), (1300, 2576, 80)]
-# the gradient of few tokens with k in parts, and next to where it is not
+# the gradient with k in parts, and next to where it is not
 FEW_SHAPES = [(16, 1040, 272), (30, 528, 1040), (33, 80, 8208), (65, 4112, 144), (128, 1040, 528), (127, 2064, 16),
-              (128, 496, 272), (129, 4112, 144)]
+              (128, 496, 272), (129, 4112, 144), (300, 1040, 528), (161, 3216, 272)]
 
 
 def ffn_case(g, rows, features, hidden):
