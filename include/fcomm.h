@@ -516,7 +516,8 @@ fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int6
  * rounding).  dx may be NULL, and both of dw_gate and dw_up, not all
  * three.  Sums run in a fixed order.  An infinity or a NaN of an input makes
  * infinities or NaN of the sums that it is in.  workspace: fc_gated_ffn_backward_workspace
- * bytes, 32-byte aligned, this call's own until it has run.  rows == 0 sets the
+ * bytes (enough for fewer rows and features too), 32-byte aligned, this call's own
+ * until it has run.  rows == 0 sets the
  * weights' gradients to 0.  Outputs overlap nothing.  d_status: optional, as for
  * fc_mx4_matmul. */
 size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features);

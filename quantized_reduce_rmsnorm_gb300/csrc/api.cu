@@ -1033,7 +1033,9 @@ fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int6
 
 size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features) {
   if (rows <= 0 || features <= 0) return 0;
-  return static_cast<size_t>(rows) * static_cast<size_t>(features) * 4u * fc::gated_ffn_terms(rows, features);
+  // what the call takes, and any with fewer rows or features: those may take two terms
+  const int64_t n = rows * features;
+  return static_cast<size_t>(std::max({4 * n, 8 * std::min(n, fc::kTwoTermFactors), 8 * std::min(rows, fc::kFewDx) * features}));
 }
 
 fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* gate,

@@ -163,8 +163,9 @@ constexpr int64_t kFewDx = 128, kFewDxFeatures = 512;
 // there are few factors in all: with one the error of dw, as of its own rounding and as
 // much again, is then left to a few terms (1.41 times that of its rounding, and up to 1.6
 // of 250 drawn sizes with the fewest; above 2^20 factors up to 1.46).
+constexpr int64_t kTwoTermFactors = 1 << 19;
 constexpr int gated_ffn_terms(int64_t rows, int64_t features) {
-  return rows <= kFewDx || rows * features <= 1 << 19 ? 2 : 1;
+  return rows <= kFewDx || rows * features <= kTwoTermFactors ? 2 : 1;
 }
 
 struct GatedFfnGradArgs {

@@ -26,7 +26,24 @@ def test_sizes():
     assert ws(5, 64) == 5 * 64 * 8 and ws(10 ** 6, 64) == 608 * 64 * 8 and ws(0, 64) == 0
     ws = L.fc_gated_ffn_backward_workspace
     assert ws(5, 64) == 5 * 64 * 8 and ws(1 << 20, 1 << 14) == 1 << 36 and ws(0, 64) == 0
-    assert ws(128, 1 << 14) == 1 << 24 and ws(129, 1 << 14) == 129 << 16 and ws(512, 1024) == 1 << 22
+    assert ws(128, 1 << 14) == 1 << 24 and ws(512, 1024) == 1 << 22 and ws(4096, 8192) == 1 << 27
+
+
+@pytest.mark.parametrize("name", ["fc_layer_norm_backward_workspace", "fc_gated_ffn_backward_workspace"])
+def test_a_workspace_serves_smaller_calls(name):
+    """A workspace laid out for the largest call holds what any smaller one takes."""
+    ws = getattr(fc.load(), name)
+    rows, cols = [1, 16, 64, 127, 128, 129, 511, 512, 513, 1023, 1024, 1025, 4096], [16, 512, 1024, 1040, 4096, 16384]
+    for f in cols:
+        sizes = [ws(r, f) for r in rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    for r in rows:
+        sizes = [ws(r, f) for f in cols]
+        assert sizes == sorted(sizes)
+    if name == "fc_gated_ffn_backward_workspace":  # dg and du, in one bf16 number or two
+        for r in rows:
+            for f in cols:
+                assert ws(r, f) >= r * f * (8 if r <= 128 or r * f <= 1 << 19 else 4)
 
 
 # ------------------------------------------------------------ references ---
