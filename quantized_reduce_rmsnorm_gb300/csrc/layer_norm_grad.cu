@@ -104,18 +104,19 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm_grad(const GradJob jo
   if (t == 0) from = static_cast<const char*>(a.h) + shift;
   if (t == 1) from = static_cast<const char*>(a.dy) + shift;
   if (t == 2) from = static_cast<const char*>(a.dh) + shift;
-  auto stage_row = [&](int row, int st) {  // the first warp
-    if (row >= r1) return;
+  // Row `row` + k, for row <= r1: without the sum, which passes 2^31 where rows end next to it.
+  auto stage_row = [&](int row, int k, int st) {  // the first warp
+    if (k >= r1 - row) return;
     if (t == 0) {
       fence_proxy_async_smem();
       mbar_expect_tx(full + st, slots * row_bytes);
     }
     __syncwarp();
     if (t < slots)
-      bulk_load(ring + (st * slots + t) * row_bytes, from + static_cast<int64_t>(row) * stride, row_bytes, full + st);
+      bulk_load(ring + (st * slots + t) * row_bytes, from + (static_cast<int64_t>(row) + k) * stride, row_bytes, full + st);
   };
   if (t < 32)
-    for (int k = 0; k < stages; ++k) stage_row(r0 + k, k);
+    for (int k = 0; k < stages; ++k) stage_row(r0, k, k);
 
   const float inv_n = 1.0f / static_cast<float>(H);
   const float2 zero = make_float2(0.0f, 0.0f);
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm_grad(const GradJob jo
       stop = true;
       break;
     }
-    if (t < 32) stage_row(row + stages, s);
+    if (t < 32) stage_row(row, stages, s);
     if (++s == stages) s = 0, phase ^= 1;
     if (!on) continue;
     const float2 m0 = dup2(-(r[0] * inv_n)), m1 = dup2(-(r[1] * inv_n));
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_layer_norm_grad(const GradJob jo
   }
   if (stop && t == 0) {  // a copy never landed: say so, and let those in flight land
     if (a.status) *a.status = kErrCuda;
-    for (int i = row; i < min(row + stages, r1); ++i) mbar_wait_bounded(full + (i - r0) % stages, ((i - r0) / stages) & 1);
+    for (int i = row - r0; i < row - r0 + min(stages, r1 - row); ++i) mbar_wait_bounded(full + i % stages, (i / stages) & 1);
   }
   if constexpr (CL > 1) {  // no CTA's memory goes while another may write to it
     __syncwarp();

@@ -602,6 +602,31 @@ def test_layer_norm_past_the_32_bit_offsets():
     assert torch.equal(dx[rows - k:], dx2)
 
 
+def test_layer_norm_gradient_of_the_most_rows():
+    """2^31 - 1 rows: the rows that a CTA stages ahead of its last ones would pass 2^31.  Whole
+    numbers at both ends, with mean 0 and deviation 1 given: the result is exact."""
+    rows, hidden, k = 2 ** 31 - 1, 16, 9
+    h, dy = (torch.zeros(rows, hidden, dtype=B16, device="cuda") for _ in range(2))
+    stats = torch.zeros(rows, 2, device="cuda")
+    stats[:, 1] = 1
+    g, ends = gen_of("most rows"), (slice(0, k), slice(rows - k, rows))
+    want, dw, db = [], 0, 0
+    for r in ends:
+        h[r], dy[r] = small_ints(g, k, hidden), small_ints(g, k, hidden)
+        n, e = h[r].double(), dy[r].double()
+        want.append((e - e.mean(1, keepdim=True) - n * (e * n).mean(1, keepdim=True)).float().to(B16))
+        dw, db = dw + (e * n).sum(0).float(), db + e.sum(0).float()
+    got_w, got_b = (torch.full((hidden,), float("nan"), device="cuda") for _ in range(2))
+    st = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    fc.layer_norm_backward(h, stats, dy, dy, fc.alloc_layer_norm_workspace(rows, hidden), dweight=got_w, dbias=got_b,
+                           d_status=st)
+    assert st.tolist() == [0, fc.STATUS_NO_INDEX]
+    for r, v in zip(ends, want):
+        assert torch.equal(dy[r], v)
+    assert (dy[1 << 30:(1 << 30) + 4096] == 0).all()
+    assert torch.equal(got_w, dw) and torch.equal(got_b, db)
+
+
 @pytest.mark.parametrize("rows,features", [(140000, 32768), (100, 4190000)])
 def test_products_past_the_32_bit_offsets(rows, features):
     (x, w), _ = ref.exact_pair(gen_of("far", rows), 64, 128, 64)
