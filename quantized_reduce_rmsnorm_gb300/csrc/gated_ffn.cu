@@ -41,8 +41,9 @@ __device__ __forceinline__ float2 activate_slope(float z) {
   const float p = ACT == kSilu ? z : kGeluScale * __fmaf_rn(kGeluCube * zz, z, z);
   const float dp = ACT == kSilu ? 1.0f : kGeluScale * __fmaf_rn(3.0f * kGeluCube, zz, 1.0f);
   const float s = sigmoid(p), a = z * s, t = 1.0f - s;
-  // far out s or 1 - s is 0, and what it multiplies may be past binary32
-  return make_float2(a, s == 0.0f || t == 0.0f ? s : __fmaf_rn(a, dp * t, s));
+  // far out s or 1 - s is 0, and what it multiplies may be past binary32; an infinite z has no
+  // slope (infinity times 0)
+  return make_float2(a, s == 0.0f || t == 0.0f ? __fmaf_rn(z, 0.0f, s) : __fmaf_rn(a, dp * t, s));
 }
 
 // ------------------------------------------------ few tokens: k in parts --

@@ -519,6 +519,29 @@ def test_gated_ffn_gradient_of_far_projections(rows, features, name):
         within(out[k], v, HALF[B16] * v.abs() + tol, k)
 
 
+@pytest.mark.parametrize("name", list(ACT))
+@pytest.mark.parametrize("rows,features,hidden", [(16, 1040, 272), (65, 4112, 144), (161, 3216, 272), (300, 4112, 256)])
+def test_gated_ffn_gradient_of_infinities_and_nans(rows, features, hidden, name):
+    """An infinity or a NaN of the gate's projection, the other's or the gradient spoils the
+    sums that it is in, as by the formula in 64 bits, and no others."""
+    i = ffn_grad_case(gen_of("spoilt", rows, features, name), rows, features, hidden)
+    clean = ffn_grad_outputs(i)
+    run_ffn_grad(i, clean, name)
+    inf, nan = float("inf"), float("nan")
+    at = [("gate", inf), ("gate", -inf), ("gate", nan), ("up", inf), ("up", -inf), ("up", nan), ("dout", inf), ("dout", nan)]
+    for k, (which, v) in enumerate(at):
+        i[which][rows - 1 - k, 5 + k * (features // 8)] = v
+    out = ffn_grad_outputs(i)
+    run_ffn_grad(i, out, name)
+    want = ref.gated_grad_reference(*i.values(), name)
+    for k, (v, _) in want.items():
+        spoilt = ~torch.isfinite(v)
+        lines = spoilt.any(1)
+        assert torch.equal(spoilt, lines[:, None].expand_as(spoilt)) and 0 < lines.sum() <= 8
+        assert torch.equal(~torch.isfinite(out[k]), spoilt), (k, (torch.isfinite(out[k]) & spoilt).any(1).nonzero())
+        assert torch.equal(out[k][~lines], clean[k][~lines]), k
+
+
 def test_gated_ffn_gradient_without_the_optional_outputs():
     i = ffn_grad_case(gen_of("optional"), 150, 272, 400)
     out = ffn_grad_outputs(i)
