@@ -158,3 +158,33 @@ def gated_grad_reference(x, wg, wu, gate, up, dout, name):
     return {"dx": (dg @ wg + du @ wu, tg @ wg.abs() + tu @ wu.abs() + 2 * F * terms * TC * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())),
             "dw_gate": (dg.T @ x, tg.T @ x.abs() + R * terms * TC * (dg.abs().T @ x.abs())),
             "dw_up": (du.T @ x, tu.T @ x.abs() + R * terms * TC * (du.abs().T @ x.abs()))}
+
+
+def two_term_case(g: torch.Generator, rows: int, features: int, hidden: int, device="cpu"):
+    """Inputs of the gradient (SiLU) whose factors need two bf16 numbers each and whose sums
+    binary32 holds exactly, with their dg and du: where the gate's projection is 65, SiLU is 65
+    and its slope 1 (in binary32); dout is odd and up such that dg = dout up is odd and above
+    256, as du = 65 dout is.  Weights of -1, 0 and 1: a sum of sizes is below 1430 features."""
+    assert 2 * 715 * features < 2 ** 24 and 3 * 715 * rows < 2 ** 24
+
+    def odd(lo, hi, *shape):
+        v = 2 * torch.randint(lo // 2, (hi + 1) // 2, shape, generator=g) + 1
+        return v * (2 * torch.randint(0, 2, shape, generator=g) - 1)
+
+    def ints(most, *shape):
+        return torch.randint(-most, most + 1, shape, generator=g)
+
+    i = dict(x=ints(3, rows, hidden), w_gate=ints(1, features, hidden), w_up=ints(1, features, hidden),
+             gate=torch.full((rows, features), 65), up=odd(53, 65, rows, features), dout=odd(5, 11, rows, features))
+    i = {k: v.to(torch.bfloat16).to(device) for k, v in i.items()}
+    d, u = i["dout"].double(), i["up"].double()
+    dg, du = d * u, 65 * d
+    assert dg.abs().min() > 256 and max(dg.abs().max(), du.abs().max()) <= 715 and (dg % 2 != 0).all()
+    return i, dg, du
+
+
+def gradients(i, dg, du):
+    """bf16 gradients of the factors, of sums that are exact."""
+    x, wg, wu = (i[k].double() for k in ("x", "w_gate", "w_up"))
+    out = {"dx": dg @ wg + du @ wu, "dw_gate": dg.T @ x, "dw_up": du.T @ x}
+    return {k: v.float().to(torch.bfloat16) for k, v in out.items()}

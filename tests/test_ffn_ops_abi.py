@@ -108,6 +108,23 @@ def test_gated_gradient_reference_is_that_of_the_formula():
             assert torch.allclose(got[k][0], v.grad, rtol=1e-10, atol=1e-10), k
 
 
+@pytest.mark.parametrize("rows,features,hidden", [(1, 144, 64), (16, 1040, 272), (65, 4112, 144), (300, 1040, 528)])
+def test_two_term_inputs_show_both_second_terms(rows, features, hidden):
+    """With the second bf16 number of dg or of du left out, or the two exchanged, every row of dx
+    differs, and almost every row of the weights' gradients (of 16 tokens and more: a sum
+    of one or two factors is often rounded to that of their first numbers)."""
+    i, dg, du = ref.two_term_case(torch.Generator().manual_seed(rows), rows, features, hidden)
+    (g1, u1), want = (v.to(torch.bfloat16).double() for v in (dg, du)), ref.gradients(i, dg, du)
+    g2, u2 = dg - g1, du - u1
+    for v in (g2, u2):
+        assert (v != 0).all() and torch.equal(v.to(torch.bfloat16).double(), v)
+    for a, b, spoilt in ((g1, du, ("dx", "dw_gate")), (dg, u1, ("dx", "dw_up")), (g1 + u2, u1 + g2, tuple(want))):
+        got = ref.gradients(i, a, b)
+        assert (got["dx"] != want["dx"]).any(1).all()
+        for k in spoilt:
+            assert rows < 16 or (got[k] != want[k]).any(1).double().mean() > 0.95, k
+
+
 def test_layer_norm_gradient_reference_is_that_of_the_formula():
     g = torch.Generator().manual_seed(4)
     h, dy, dh = (torch.randn(5, 48, generator=g, dtype=torch.float64) for _ in range(3))

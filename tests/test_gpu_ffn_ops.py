@@ -495,6 +495,19 @@ def test_gated_ffn_gradient_is_exact(rows, features, hidden, z):
         assert (out[k][1] == 7).all(), k
 
 
+@pytest.mark.parametrize("rows,features,hidden", [s for s in FFN_SHAPES + FEW_SHAPES if s[0] <= 128 or s[0] * s[1] <= 1 << 19])
+def test_gated_ffn_gradient_of_two_term_factors_is_exact(rows, features, hidden):
+    """Factors that need both of their bf16 numbers, for few tokens or few factors: bit for bit."""
+    i, dg, du = ref.two_term_case(gen_of("two terms", rows, features, hidden), rows, features, hidden, "cuda")
+    want, out = ref.gradients(i, dg, du), {k: guarded(*v.shape) for k, v in ffn_grad_outputs(i).items()}
+    run_ffn_grad(i, {k: v[0] for k, v in out.items()})
+    for k in want:
+        assert torch.equal(out[k][0], want[k]) and (out[k][1] == 7).all(), k
+    dx = {"dx": torch.full_like(i["x"], float("nan"))}
+    run_ffn_grad(i, dx)
+    assert torch.equal(dx["dx"], want["dx"])
+
+
 @pytest.mark.parametrize("name", list(ACT))
 @pytest.mark.parametrize("rows,features", [(1, 208), (140, 4112)])
 def test_gated_ffn_gradient_of_far_projections(rows, features, name):
