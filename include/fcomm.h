@@ -526,6 +526,17 @@ fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w
                                 int64_t hidden, int32_t activation, void* dx, void* dw_gate, void* dw_up,
                                 void* workspace, int32_t* d_status, fc_stream_t stream);
 
+/* fc_gated_ffn_backward with the bf16 numbers that stand for each of dg and du chosen:
+ * factor_terms 0, by size as above, or 2, at every size (the results are then as far off as
+ * their own rounding leaves them, for about twice the products' time).  workspace:
+ * fc_gated_ffn_backward_ex_workspace bytes for the same factor_terms; all else as above. */
+size_t fc_gated_ffn_backward_ex_workspace(int64_t rows, int64_t features, int32_t factor_terms);
+fc_status fc_gated_ffn_backward_ex(const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                   const void* up, const void* dout, int64_t rows, int64_t features,
+                                   int64_t hidden, int32_t activation, int32_t factor_terms, void* dx,
+                                   void* dw_gate, void* dw_up, void* workspace, int32_t* d_status,
+                                   fc_stream_t stream);
+
 /* --------------------------------------------------------------- misc --- */
 const char* fc_status_string(fc_status s);
 /* Message describing the calling thread's last non-OK status ("" if none). */

@@ -1038,12 +1038,29 @@ size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features) {
   return static_cast<size_t>(std::max({4 * n, 8 * std::min(n, fc::kTwoTermFactors), 8 * std::min(rows, fc::kFewDx) * features}));
 }
 
+size_t fc_gated_ffn_backward_ex_workspace(int64_t rows, int64_t features, int32_t factor_terms) {
+  if (factor_terms == 0) return fc_gated_ffn_backward_workspace(rows, features);
+  if (rows <= 0 || features <= 0 || factor_terms != 2) return 0;
+  return static_cast<size_t>(rows) * static_cast<size_t>(features) * 8u;
+}
+
 fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* gate,
                                 const void* up, const void* dout, int64_t rows, int64_t features,
                                 int64_t hidden, int32_t activation, void* dx, void* dw_gate, void* dw_up,
                                 void* workspace, int32_t* d_status, fc_stream_t stream) {
+  return fc_gated_ffn_backward_ex(x, w_gate, w_up, gate, up, dout, rows, features, hidden, activation, 0, dx, dw_gate,
+                                  dw_up, workspace, d_status, stream);
+}
+
+fc_status fc_gated_ffn_backward_ex(const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                   const void* up, const void* dout, int64_t rows, int64_t features,
+                                   int64_t hidden, int32_t activation, int32_t factor_terms, void* dx,
+                                   void* dw_gate, void* dw_up, void* workspace, int32_t* d_status,
+                                   fc_stream_t stream) {
   if (fc_status s = check_product(rows, features, hidden, 16)) return s;
   if (fc_status s = check_activation(activation)) return s;
+  if (factor_terms != 0 && factor_terms != 2)
+    return fail(FC_ERR_INVALID, "factor_terms must be 0 or 2 (got %d)", factor_terms);
   if (!dw_gate != !dw_up) return fail(FC_ERR_INVALID, "dw_gate and dw_up are given together");
   if (!dx && !dw_gate) return fail(FC_ERR_INVALID, "no gradient is asked for");
   if (fc_status s = check_optional(dw_gate, 32, "dw_gate")) return s;
@@ -1053,7 +1070,7 @@ fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w
   const Span o[] = {{dx, rows * hidden * 2, "dx", false},
                     {dw_gate, wn, "dw_gate", false},
                     {dw_up, wn, "dw_up", false},
-                    {workspace, (int64_t)fc_gated_ffn_backward_workspace(rows, features), "workspace", false},
+                    {workspace, (int64_t)fc_gated_ffn_backward_ex_workspace(rows, features, factor_terms), "workspace", false},
                     {d_status, 8, "d_status", false}};
   const Span i[] = {{x, rows * hidden * 2, "x", false}, {w_gate, wn, "w_gate", false}, {w_up, wn, "w_up", false},
                     {gate, n, "gate", false},           {up, n, "up", false},          {dout, n, "dout", false}};
@@ -1089,6 +1106,7 @@ fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w
   a.features = features;
   a.H = static_cast<int>(hidden);
   a.activation = activation;
+  a.terms = factor_terms ? factor_terms : fc::gated_ffn_terms(rows, features);
   if (fc_status s = reset_status(d_status, (cudaStream_t)stream)) return s;
   return cuda_status(fc::launch_gated_ffn_grad(a, (cudaStream_t)stream), "fc_gated_ffn_backward launch");
 }

@@ -159,10 +159,14 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st);
 // Tokens up to which, and features from which on, the kernel of few tokens makes dx.
 constexpr int64_t kFewDx = 128, kFewDxFeatures = 512;
 // bf16 numbers that stand for each of the gradient's factors dg and du, and that the
-// workspace holds: two for few tokens, whose gradients the weights' bytes bound, and where
-// there are few factors in all: with one the error of dw, as of its own rounding and as
-// much again, is then left to a few terms (1.41 times that of its rounding, and up to 1.6
-// of 250 drawn sizes with the fewest; above 2^20 factors up to 1.46).
+// workspace holds, where the caller leaves it to the sizes.  With one the results are off by
+// 1.41 times what their own rounding leaves (root mean square: the factors' roundings are
+// as large as it and independent of it, so the squares add up), with two by that alone.  Two
+// for few tokens, whose gradients the weights' bytes bound, and up to 2^19 factors, where
+// they cost 5 to 12 us (us, one / two numbers, tokens x features x hidden next to the border:
+// 1024 x 528 x 1024 13.0 / 18.2, 2048 x 272 x 1024 17.3 / 26.4, 140 x 3792 x 4096 42.5 / 54.2;
+// further up 1024 x 1040 x 1024 18.4 / 28.2, 777 x 4112 x 2064 48.9 / 89.0, 4096 x 8192 x 4096
+// 650 / 1312).
 constexpr int64_t kTwoTermFactors = 1 << 19;
 constexpr int gated_ffn_terms(int64_t rows, int64_t features) {
   return rows <= kFewDx || rows * features <= kTwoTermFactors ? 2 : 1;
@@ -184,6 +188,7 @@ struct GatedFfnGradArgs {
   int64_t features;
   int H;
   int activation;
+  int terms;              // gated_ffn_terms, or 2
 };
 cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st);
 

@@ -833,7 +833,7 @@ cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   const int64_t n = a.rows * a.features;
-  const int terms = gated_ffn_terms(a.rows, a.features);
+  const int terms = a.terms;
   auto* ws = static_cast<__nv_bfloat16*>(a.ws);  // [term][dg, du][rows, features]
   auto* factors = terms == 2 ? a.activation == kSilu ? k_gated_factors<kSilu, 2> : k_gated_factors<kGeluTanh, 2>
                              : a.activation == kSilu ? k_gated_factors<kSilu, 1> : k_gated_factors<kGeluTanh, 1>;

@@ -33,6 +33,7 @@ EXPORTS = (
     "fc_block_norm_backward", "fc_layer_norm", "fc_layer_norm_backward_workspace",
     "fc_layer_norm_backward", "fc_fp8_scales", "fc_fp8_quantize", "fc_fp8_dequantize",
     "fc_fp8_matmul", "fc_gated_ffn", "fc_gated_ffn_backward_workspace", "fc_gated_ffn_backward",
+    "fc_gated_ffn_backward_ex_workspace", "fc_gated_ffn_backward_ex",
 )
 
 
@@ -158,6 +159,8 @@ def load(path: Optional[str] = None):
         "fc_gated_ffn": (i32, [P, P, P, i64, i64, i64, i32, P, P, P, P, P]),
         "fc_gated_ffn_backward_workspace": (ctypes.c_size_t, [i64, i64]),
         "fc_gated_ffn_backward": (i32, [P, P, P, P, P, P, i64, i64, i64, i32, P, P, P, P, P, P]),
+        "fc_gated_ffn_backward_ex_workspace": (ctypes.c_size_t, [i64, i64, i32]),
+        "fc_gated_ffn_backward_ex": (i32, [P, P, P, P, P, P, i64, i64, i64, i32, i32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -880,9 +883,9 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: to
     _once(bind_gated_ffn(x, w_gate, w_up, out, **kw), stream)
 
 
-def alloc_gated_ffn_workspace(rows: int, features: int, device="cuda"):
-    """Workspace of one gated_ffn_backward call at a time."""
-    n = load().fc_gated_ffn_backward_workspace(rows, features)
+def alloc_gated_ffn_workspace(rows: int, features: int, device="cuda", factor_terms: int = 0):
+    """Workspace of one gated_ffn_backward call (with these factor_terms) at a time."""
+    n = load().fc_gated_ffn_backward_ex_workspace(rows, features, factor_terms)
     return torch.empty(max(n, 32), dtype=torch.uint8, device=device)
 
 
@@ -891,10 +894,11 @@ def bind_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.T
                             workspace: torch.Tensor, dx: Optional[torch.Tensor] = None,
                             dw_gate: Optional[torch.Tensor] = None,
                             dw_up: Optional[torch.Tensor] = None, activation: int = ACT_SILU,
-                            d_status: Optional[torch.Tensor] = None) -> DeviceBound:
+                            d_status: Optional[torch.Tensor] = None,
+                            factor_terms: int = 0) -> DeviceBound:
     rows, hidden = _rows_hidden(x)
     features, B, P = dout.shape[-1], torch.bfloat16, ctypes.c_void_p
-    need = load().fc_gated_ffn_backward_workspace(rows, features)
+    need = load().fc_gated_ffn_backward_ex_workspace(rows, features, factor_terms)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must hold {need} bytes")
     act, weight = (rows, features), (features, hidden)
@@ -905,7 +909,10 @@ def bind_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.T
             P(_want(dw_up, weight, B, "dw_up")), P(_ptr(workspace)),
             P(_want(d_status, (2,), torch.int32, "d_status")), None]
     keep = (x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, workspace, d_status)
-    return DeviceBound(load().fc_gated_ffn_backward, args, 15, keep=keep, device=_one_device(*keep))
+    if factor_terms == 0:
+        return DeviceBound(load().fc_gated_ffn_backward, args, 15, keep=keep, device=_one_device(*keep))
+    args.insert(10, factor_terms)
+    return DeviceBound(load().fc_gated_ffn_backward_ex, args, 16, keep=keep, device=_one_device(*keep))
 
 
 def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
@@ -913,6 +920,7 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
                        **kw):
     """Gradient of gated_ffn.  gate and up are the projections that the forward pass kept,
     dout the gradient of out.  Keywords: dx and (both or neither) dw_gate and dw_up, bf16,
-    which receive the gradients; activation; d_status.  workspace from
-    alloc_gated_ffn_workspace."""
+    which receive the gradients; activation; d_status; factor_terms (0: dg and du in two bf16
+    numbers each for up to 128 tokens or 2^19 factors, else in one; 2: always in two).
+    workspace from alloc_gated_ffn_workspace, for the same factor_terms."""
     _once(bind_gated_ffn_backward(x, w_gate, w_up, gate, up, dout, workspace, **kw), stream)

@@ -274,6 +274,31 @@ def test_gated_ffn_backward_refusals():
         refused(n, *ffn_back(**kw), says="overlaps")
 
 
+def test_gated_ffn_backward_factor_terms():
+    L = fc.load()
+    ws, by_size = L.fc_gated_ffn_backward_ex_workspace, L.fc_gated_ffn_backward_workspace
+    for rows, features in ((1, 16), (128, 4096), (129, 8192), (4096, 8192), (0, 64)):
+        assert ws(rows, features, 0) == by_size(rows, features) and ws(rows, features, 2) == 8 * rows * features
+    assert ws(128, 64, 1) == 0 and ws(128, 64, 3) == 0 and ws(-1, 64, 2) == 0
+
+    def args(terms, **kw):
+        a = ffn_back(**kw)
+        return (*a[:10], terms, *a[10:])
+
+    n = "fc_gated_ffn_backward_ex"
+    for terms in (-1, 1, 3):
+        refused(n, *args(terms), says="factor_terms")
+    refused(n, *args(2, hidden=72), says="multiple of 16")
+    refused(n, *args(2, ws=A[9] + 16), says="must")
+    far = 256 * 4096 * 4  # past what the call takes by size, not what it takes with two terms
+    assert by_size(256, 4096) == far
+    refused(n, *args(2, rows=256, features=4096, d=A[9] + far), says="workspace overlaps d_status")
+    refused(n, *args(2, rows=256, features=4096, d=A[9] + 2 * far - 4), says="workspace overlaps d_status")
+    with pytest.raises(ValueError, match="workspace"):
+        fc.gated_ffn_backward(torch.zeros(256, 64), None, None, None, None, torch.zeros(256, 4096),
+                              fc.alloc_gated_ffn_workspace(256, 4096, "cpu"), factor_terms=2)
+
+
 def test_binding_checks_shapes_and_types():
     """The binding's own checks come before any pointer is taken."""
     with pytest.raises(ValueError, match="multiple of 16"):

@@ -508,6 +508,49 @@ def test_gated_ffn_gradient_of_two_term_factors_is_exact(rows, features, hidden)
     assert torch.equal(dx["dx"], want["dx"])
 
 
+# above 128 tokens and 2^19 factors: with k of dx in parts, and with every product in one launch
+@pytest.mark.parametrize("rows,features,hidden", [(129, 4112, 144), (300, 4112, 256), (140, 4112, 1040), (1300, 2576, 80),
+                                                  (777, 1040, 1168), (64, 528, 400)])
+def test_gated_ffn_gradient_of_two_terms_asked_for_is_exact(rows, features, hidden):
+    """factor_terms=2 at every size: factors that need both of their bf16 numbers, bit for bit;
+    with the terms by size the results are off."""
+    i, dg, du = ref.two_term_case(gen_of("asked", rows, features, hidden), rows, features, hidden, "cuda")
+    want, out = ref.gradients(i, dg, du), {k: guarded(*v.shape) for k, v in ffn_grad_outputs(i).items()}
+    ws, behind = guarded(fc.load().fc_gated_ffn_backward_ex_workspace(rows, features, 2), dtype=torch.uint8)
+    st = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    run_ffn_grad(i, {k: v[0] for k, v in out.items()}, ws=ws, factor_terms=2, d_status=st)
+    assert st.tolist() == [0, fc.STATUS_NO_INDEX] and (behind == 7).all()
+    for k in want:
+        assert torch.equal(out[k][0], want[k]) and (out[k][1] == 7).all(), k
+    by_size = ffn_grad_outputs(i)
+    run_ffn_grad(i, by_size)
+    assert all(torch.equal(by_size[k], want[k]) == (rows == 64) for k in want)
+
+
+def rms(v):
+    return v.square().mean().sqrt().item()
+
+
+@pytest.mark.parametrize("rows,features,hidden", [(300, 4112, 256), (777, 2064, 1040), (2100, 1040, 528)])
+def test_gated_ffn_gradient_error_beside_its_rounding(rows, features, hidden):
+    """The root mean square of the results' distance to the 64-bit ones, in that of their own
+    rounding.  Two terms: a factor is off by 2^-16, and sums by a few 2^-23 of their terms'
+    sizes: 1.02.  One term: the factors' errors are independent of one another and of the
+    result's, so the squares add up; with as many values at each place between two powers of
+    two the two are alike, and the ratio is the root of 2.  A rounding's mean square is 1 / 12
+    of a step's, a step between 2^-8 and 2^-7 of its value, so that whatever the places the
+    factors' share is at most four times the result's: below the root of 5."""
+    i = ffn_grad_case(gen_of("rms", rows, features, hidden), rows, features, hidden)
+    want = ref.gated_grad_reference(*i.values(), "silu")
+    for terms, most in ((0, 5 ** 0.5), (2, 1.02)):
+        out = ffn_grad_outputs(i)
+        run_ffn_grad(i, out, ws=fc.alloc_gated_ffn_workspace(rows, features, factor_terms=terms), factor_terms=terms)
+        for k, (v, _) in want.items():
+            ratio = rms(out[k].double() - v) / rms(v.to(B16).double() - v)
+            print(f"{k}, factor_terms={terms}: {ratio:.3f} of its rounding")
+            assert ratio <= most, (k, terms)
+
+
 @pytest.mark.parametrize("name", list(ACT))
 @pytest.mark.parametrize("rows,features", [(1, 208), (140, 4112)])
 def test_gated_ffn_gradient_of_far_projections(rows, features, name):
