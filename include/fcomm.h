@@ -427,8 +427,8 @@ fc_status fc_block_norm_backward(const void* x, const void* h, const void* dy, c
  *   h = T(x + residual_in)                          -> residual_out
  *   y = T((h - mean(h)) * inv * weight + bias),  inv = 1 / sqrt(var(h) + eps)
  * with mean, var (the mean of squared distances to the mean) and inv in binary32
- * (a row's squared distances have to add up to less than binary32's largest
- * number).  x, residual_in, residual_out, y: [rows, hidden].  residual_in and
+ * (a row's magnitudes, and its squared distances, have to add up to less than
+ * binary32's largest number).  x, residual_in, residual_out, y: [rows, hidden].  residual_in and
  * residual_out: both or neither; without them h is x.  weight, bias: [hidden],
  * each NULL for none.  stats: fp32 [rows, 2], 8-byte aligned, receives each row's
  * mean and inv for the gradient; NULL if not wanted.  hidden: a multiple of 16,
@@ -475,7 +475,7 @@ size_t fc_fp8_scales(int64_t rows, int64_t hidden, int64_t block_rows);
 fc_status fc_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t hidden, int64_t block_rows,
                           fc_fp8 out, fc_stream_t stream);
 
-/* Read back: out[rows, hidden] = code * scale, rounded once to out_dtype
+/* Read back: out[rows, hidden] = code * scale, a binary32 product, rounded to out_dtype
  * FC_FMT_BF16 or FC_FMT_F32. */
 fc_status fc_fp8_dequantize(fc_fp8 in, int64_t rows, int64_t hidden, int64_t block_rows, void* out,
                             int32_t out_dtype, fc_stream_t stream);
@@ -495,7 +495,8 @@ fc_status fc_fp8_matmul(fc_fp8 x, fc_fp8 w, int64_t rows, int64_t features, int6
 /* The gated feed-forward block's two projections, activation and product:
  *   g = x w_gate^T,  u = x w_up^T,  out = bf16(act(g) * u)
  * x: [rows, hidden], w_gate and w_up: [features, hidden], out: [rows, features], all
- * bf16 and 32-byte aligned; sums, activation and product in binary32.  gate, up:
+ * bf16 and 32-byte aligned; sums, activation and product in binary32 (an activation
+ * below 2^-119 in magnitude, far below 0, may be 0).  gate, up:
  * [rows, features] bf16, receive g and u for the gradient; both or neither.
  * hidden and features: multiples of 16; hidden at most 65536, rows and features at
  * most 2^22.  Outputs overlap nothing.  d_status: optional, as for fc_mx4_matmul. */
@@ -509,16 +510,17 @@ fc_status fc_gated_ffn(const void* x, const void* w_gate, const void* w_up, int6
                        fc_stream_t stream);
 
 /* Gradient of fc_gated_ffn.  gate, up: what the forward pass kept; dout: the
- * gradient of out.  With dg = dout * up * act'(gate) and du = dout * act(gate):
+ * gradient of out.  With dg = dout * up * act'(gate) and du = dout * act(gate), binary32
+ * products in this order:
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  * in bf16 after a binary32 sum, dg and du rounded to the sum of two bf16 numbers where
  * rows <= 128 or rows * features <= 2^19, to one above (as much again as the results' own
- * rounding).  dx may be NULL, and both of dw_gate and dw_up, not all
- * three.  Sums run in a fixed order.  An infinity or a NaN of an input makes
- * infinities or NaN of the sums that it is in.  workspace: fc_gated_ffn_backward_workspace
- * bytes (enough for fewer rows and features too), 32-byte aligned, this call's own
- * until it has run.  rows == 0 sets the
- * weights' gradients to 0.  Outputs overlap nothing.  d_status: optional, as for
+ * rounding; fc_gated_ffn_backward_ex leaves the choice to the caller).  dx may be NULL,
+ * and both of dw_gate and dw_up, not all three.  Sums run in a fixed order.  An infinity
+ * or a NaN of an input makes infinities or NaN of the sums that it is in (an infinite
+ * gate has no slope).  workspace: fc_gated_ffn_backward_workspace bytes (enough for fewer
+ * rows and features too), 32-byte aligned, this call's own until it has run.  rows == 0
+ * sets the weights' gradients to 0.  Outputs overlap nothing.  d_status: optional, as for
  * fc_mx4_matmul. */
 size_t fc_gated_ffn_backward_workspace(int64_t rows, int64_t features);
 fc_status fc_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* gate,

@@ -5,7 +5,8 @@
 // reverse.  A lane takes 16 elements (one or two 256-bit loads, 16 bytes of codes), eight
 // lanes a block's part of one row.  A weight's block is one CTA's.  Measured on GB300, 8192 x
 // 8192: bf16 to eight bits 30.2 us, 6.7 TB/s (0.98 of the measured copy rate), back 30.6; fp32
-// 48.3 and 49.2; a bf16 weight 41.8 (0.71: two barriers a block, and done once).
+// 48.3 and 49.2; a bf16 weight 41.8 (0.71: a CTA loads its one block, meets at a barrier and
+// encodes it with nothing more on its way).
 #include "block.h"
 #include "fp8.cuh"
 

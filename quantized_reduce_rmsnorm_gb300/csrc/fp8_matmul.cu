@@ -516,10 +516,10 @@ cudaError_t launch(const Fp8MatmulArgs& a, const Job& j, int parts, cudaStream_t
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, cudaStream_t st) {
   const Job j{a.x_scales, a.w_scales, a.out, a.status, a.rows, a.features, wait_cycles,
               (a.H + kK - 1) / kK, a.out_f32 ? 1 : 0};
-  // Few tokens, in tiles of at most 64 (128 tokens 8192 x 8192: 23.3 us, in one tile of 128
+  // Sizes are features x hidden.  Few tokens, in tiles of at most 64 (128 tokens 8192 x 8192: 23.3 us, in one tile of 128
   // 26.2): a thread of that kernel has a feature, so each token's factor is a load, and
   // the weights are read once for each tile of tokens.  k is cut into as many parts, of
-  // eight blocks at least, as keep two CTAs an SM; eight parts of 64 tokens only where there
+  // four blocks at least, as keep two CTAs an SM; eight parts of 64 tokens only where there
   // is then one, for their join (us, 1 / 2 / 4 / 8 parts: 1 token 8192 x 8192 16.8 / 14.8 /
   // 12.5 / 15.6, 16 tokens 1024 x 8192 14.7 / 9.3 / 6.3 / 4.7, 64 tokens 4096 x 4096 15.6 /
   // 10.8 / 9.0 / 10.1).  Above 128 tokens, and where k is not cut, the persistent kernel

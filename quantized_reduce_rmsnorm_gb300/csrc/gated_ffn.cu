@@ -10,9 +10,10 @@
 // the thread that has a token's row of both, so g and u leave the chip only where the
 // caller keeps them (in bf16, for the gradient).  dg and du go to the tensor core in bf16, by
 // the workspace.  In large products one bf16 number stands for each: its rounding, at most
-// 2^-9 of a term, is no more than a result's own, and independent from term to term.  In
-// small ones (gated_ffn_terms), where the errors of a few terms decide and more products cost
-// little, each is the sum of two bf16 numbers, 16 bits of it.
+// 2^-8 of a term, is no more than a result's own, and independent from term to term.  In
+// small ones (gated_ffn_terms), where more products cost little, and where the caller asks for
+// it, each is the sum of two bf16 numbers, 16 bits of it.
+// Sizes below are tokens x features x hidden, or features x hidden after the tokens.
 #include <algorithm>
 
 #include "block.h"
@@ -241,9 +242,9 @@ __global__ void __launch_bounds__(Few<BN>::kThreads, 2)
 // Bound by the products: 4096 tokens by 8192 x 8192 forward 606 to 645 us, 1.7 to 1.8 PFLOP/s
 // (0.9 or more of the measured burst rate, the rate of long runs under the power limit),
 // the tensor pipe active 87 % of the time at 2048 x 4096 x 4096, where the last of 3.4 turns
-// of the tiles leaves pairs idle; the gradient of 4096 x 4096 x 8192 671 to 704 us, of which
+// of the tiles leaves pairs idle; the gradient of 4096 x 8192 x 4096 650 to 711 us, of which
 // the factors' kernel is 50, the tensor pipe active 94 % of the products' time (two launches
-// with tiles in turn: 698; 777 x 2064 x 4112 70 us against 52).
+// with tiles in turn: 698; 777 x 4112 x 2064 70 us against 49).
 enum Pass { kForward, kBackward };
 
 struct Job {
@@ -796,13 +797,13 @@ cudaError_t launch_few(const GatedFfnArgs& a, int parts, cudaStream_t st) {
 
 cudaError_t launch_gated_ffn(const GatedFfnArgs& a, cudaStream_t st) {
   // A tile of 128 tokens where k is then cut in four at most: the join of eight parts takes
-  // longer than reading the weights twice (us, tiles of 128 / 64 tokens: 200 tokens 4096 x
-  // 1024 16.3 / 11.2; 200 x 4096 x 4096 21.6 / 24.9; 100 x 4096 x 4096 17.8 / 19.3).
+  // longer than reading the weights twice (us, tiles of 128 / 64 tokens: 200 x 1024 x 4096
+  // 16.3 / 11.2; 200 x 4096 x 4096 21.6 / 24.9; 100 x 4096 x 4096 17.8 / 19.3).
   const bool small = (a.features + 63) / 64 * ((a.rows + 127) / 128) * 4 <= num_sms();
   const int bn = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 || small ? 64 : 128;
   const int64_t stages = (a.H + kK - 1) / kK;
   const int64_t tiles = ((a.features + 63) / 64) * ((a.rows + bn - 1) / bn);
-  // k in as many parts, of eight stages at least, as keep two CTAs an SM, as for the 8-bit
+  // k in as many parts, of four stages at least, as keep two CTAs an SM, as for the 8-bit
   // product (us, 1 / 2 / 4 / 8 parts: 1 token 8192 x 8192 47.1 / 41.6 / 43.4 / 46.3, 1 token
   // 4096 x 4096 16.9 / 14.8 / 12.6 / 15.7, 64 tokens 2048 x 4096 21.8 / 14.0 / 11.5 / 12.8).
   // Above 128 tokens, and where k is not cut, the persistent kernel (us, it / few tokens: 333
@@ -848,12 +849,16 @@ cudaError_t launch_gated_ffn_grad(const GatedFfnGradArgs& a, cudaStream_t st) {
   if (cudaError_t e = bf16_map(m.in + 5, a.w_up, a.features, a.H, 64)) return e;
   if (cudaError_t e = bf16_map(m.in + 6, a.x, a.rows, a.H, 64)) return e;
   bool wide_dx = a.dx != nullptr;
-  // dx with k in parts, where k is long enough to pay for a launch of its own (us, in parts /
-  // with the weights' products: 64 tokens 4096 x 4096 37.8 / 76.6, 128 tokens 8192 x 4096 76 /
-  // 153, 64 x 496 x 4096 14.8 / 16.3, 64 x 384 x 1024 13.2 / 12.3, 128 x 256 x 4096 16.2 / 11.5):
-  // of up to 128 tokens, and of more where tiles of 128 leave SMs idle and k is long
+  // dx with k in parts, where k is long enough to pay for a launch of its own (us, two terms
+  // either way, in parts / with the weights' products: 64 x 4096 x 4096 37.8 / 76.6, 128 x 8192 x
+  // 4096 76 / 153, 64 x 496 x 4096 14.8 / 16.3, 64 x 384 x 1024 13.2 / 12.3, 128 x 256 x 4096 16.2 /
+  // 11.5): of up to 128 tokens, and of more where tiles of 128 leave SMs idle and k is long
   // beside the tokens (140 x 3696 x 4096 53 / 72, 300 x 1024 x 512 17.8 / 23.7, 500 x 1024 x 512
-  // 26.8 / 24.9).
+  // 26.8 / 24.9).  That kernel takes two terms and no other number of them: with one, above
+  // 2^19 factors, dx is made with the weights' products, which is faster next to the border
+  // where there are columns enough (us, one term in one launch / two in parts: 140 x 3792 x
+  // 4096 42.5 / 54.2) and slower where there are few (129 x 4112 x 1024 42.6 / 28.1, 300 x
+  // 4112 x 512 44.5 / 26.4): a caller who asks for two terms gets the second figures.
   const int64_t tiles = (a.H + 127) / 128 * ((a.rows + 127) / 128);
   const bool long_k = a.features >= kFewDxFeatures && a.features >= 3 * a.rows && tiles * 2 <= num_sms();
   if (a.dx && (a.rows <= kFewDx ? a.features >= kFewDxFeatures : terms == 2 && long_k)) {

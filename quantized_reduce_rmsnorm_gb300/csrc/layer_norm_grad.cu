@@ -11,8 +11,8 @@
 // stay in registers, each thread its own columns: no atomics, every order fixed.  A CTA
 // writes its sums once, and a second kernel adds the CTAs' in order.  Rows too wide for
 // one CTA's registers are cut over a cluster, whose CTAs exchange the row's sums.
-// Measured on GB300, 8192 x 5120 bf16 with everything asked for: 58.2 us, 5.8 TB/s (0.85
-// of the measured copy rate), of which the second kernel is about 5.
+// Measured on GB300 with everything asked for: 8192 x 5120 bf16 58.1 us, 5.8 TB/s (0.85
+// of the measured copy rate), of which the second kernel is about 5; fp32 102, 6.6 TB/s (0.97).
 #include <algorithm>
 
 #include "block.h"
@@ -258,8 +258,9 @@ cudaError_t launch_grad(GradJob& job, cudaStream_t st) {
   auto stages = [&](int CL) { return std::min(kMostStages, kMost / stage(CL)); };  // two at least
   // Eight columns a thread, and one CTA an SM of more than 320 threads: two of up to 640, at 48
   // registers a thread, spill (us, one / two, 8192 rows of 5120 bf16 58.2 / 82.9, 777 of
-  // 2064 fp32 10.0 / 15.4); 16 columns a thread are no faster (58.3, 12.2) and leave 777
-  // rows fewer warps; four stages, eight take 60.4.  Rows above 8192 columns take a cluster.
+  // 2064 fp32 without dh 10.0 / 15.4, inputs from memory: where they are in L2 it is 7.9); 16
+  // columns a thread are no faster (58.3, 12.2) and leave 777 rows fewer warps; four stages,
+  // eight take 60.4.  Rows above 8192 columns take a cluster.
   const int n = stages(1);
   if (threads(1) <= 640) return launch_staged<F32, 8, 1, 640, 1>(job, threads(1), n, n * stage(1), st);
   if (threads(1) <= 1024) return launch_staged<F32, 8, 1, 1024, 1>(job, threads(1), n, n * stage(1), st);

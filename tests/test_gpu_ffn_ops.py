@@ -681,6 +681,21 @@ def test_layer_norm_past_the_32_bit_offsets():
     assert torch.equal(dx[rows - k:], dx2)
 
 
+def test_layer_norm_of_the_most_rows():
+    """2^31 - 1 rows, in place: the last ones are as those of a small call."""
+    rows, hidden, k = 2 ** 31 - 1, 16, 9
+    x, w = torch.zeros(rows, hidden, dtype=B16, device="cuda"), randn(gen_of("w"), hidden, dtype=B16)
+    st = torch.zeros(rows, 2, device="cuda")
+    ends = (slice(0, k), slice(rows - k, rows))
+    for r in ends:
+        x[r] = randn(gen_of("most rows", r.start), k, hidden, dtype=B16)
+    want = [run_norm(x[r].clone(), None, w, w) for r in ends]
+    fc.layer_norm(x, x, weight=w, bias=w, eps=EPS, stats=st)
+    for r, (_, y, s) in zip(ends, want):
+        assert torch.equal(x[r], y) and torch.equal(st[r], s)
+    assert torch.equal(x[1 << 30], w) and st[1 << 30, 0] == 0
+
+
 def test_layer_norm_gradient_of_the_most_rows():
     """2^31 - 1 rows: the rows that a CTA stages ahead of its last ones would pass 2^31.  Whole
     numbers at both ends, with mean 0 and deviation 1 given: the result is exact."""
